@@ -41,6 +41,22 @@ class MoeSizes(ctypes.Structure):
                 ("recv_x", "recv_scales", "recv_meta", "counts", "flags", "tok_slot", "expert_out")]
 
 
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+
+
+class MoeGateOpts(ctypes.Structure):
+    """How the router turns logits into choices and weights (moe_gate_opts of include/moe_layout.h)."""
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("keep_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("logits_bf16", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 MOE_MAX_PARTS = 8
 
 
@@ -103,6 +119,13 @@ def _open(path: str):
     lib.moe_combine_parts.argtypes = [pdesc, pparts, vp, vp, vp, vp, vp]
     lib.moe_expert_stub_parts.argtypes = [pdesc, pparts, vp, vp, vp]
     lib.moe_reset_parts.argtypes = [pdesc, pparts, vp, vp]
+    popts = ctypes.POINTER(MoeGateOpts)
+    lib.moe_gate.argtypes = [pdesc, popts] + [vp] * 6
+    lib.moe_gate_grad.argtypes = [pdesc, popts] + [vp] * 6
+    lib.moe_sort.argtypes = [pdesc] + [vp] * 9
+    lib.moe_sort_grad.argtypes = [pdesc] + [vp] * 5
+    lib.moe_unsort.argtypes = [pdesc] + [vp] * 6
+    lib.moe_unsort_grad.argtypes = [pdesc] + [vp] * 8
     lib.moe_get_error.argtypes = [vp, vp]
     lib.moe_layout_dispatch_kernels.argtypes = [pdesc]
     lib.moe_layout_dispatch_kernels.restype = ctypes.c_int32
@@ -112,7 +135,8 @@ def _open(path: str):
                  "moe_expert_stub", "moe_combine", "moe_combine_packed", "moe_route_stats", "moe_reset",
                  "moe_expert_gate_up", "moe_expert_down", "moe_expert_mlp_noalloc", "moe_expert_gate_up_fp8",
                  "moe_expert_down_fp8", "moe_expert_mlp_noalloc_fp8", "moe_layout_dispatch_parts",
-                 "moe_combine_parts", "moe_expert_stub_parts", "moe_reset_parts", "moe_get_error"):
+                 "moe_combine_parts", "moe_expert_stub_parts", "moe_reset_parts", "moe_gate", "moe_gate_grad",
+                 "moe_sort", "moe_sort_grad", "moe_unsort", "moe_unsort_grad", "moe_get_error"):
         getattr(lib, name).restype = st
     return lib
 
@@ -269,6 +293,39 @@ def moe_expert_stub_parts(desc, parts: "PartBuffers", counts, err, stream=None):
 def moe_reset_parts(desc, parts: "PartBuffers", err, stream=None):
     _check(load().moe_reset_parts(ctypes.byref(desc), ctypes.byref(parts.table()), _ptr(err), _stream(stream)),
            "moe_reset_parts")
+
+
+def moe_gate(desc, opts: MoeGateOpts, logits, bias, topk_idx, topk_weights, err, stream=None):
+    _check(load().moe_gate(ctypes.byref(desc), ctypes.byref(opts), _ptr(logits), _ptr(bias), _ptr(topk_idx),
+                           _ptr(topk_weights), _ptr(err), _stream(stream)), "moe_gate")
+
+
+def moe_gate_grad(desc, opts: MoeGateOpts, logits, topk_idx, grad_weights, grad_logits, err, stream=None):
+    _check(load().moe_gate_grad(ctypes.byref(desc), ctypes.byref(opts), _ptr(logits), _ptr(topk_idx),
+                                _ptr(grad_weights), _ptr(grad_logits), _ptr(err), _stream(stream)), "moe_gate_grad")
+
+
+def moe_sort(desc, topk_idx, x, x_scales, region_offsets, packed_x, packed_scales, tok_packed, err, stream=None):
+    _check(load().moe_sort(ctypes.byref(desc), _ptr(topk_idx), _ptr(x), _ptr(x_scales), _ptr(region_offsets),
+                           _ptr(packed_x), _ptr(packed_scales), _ptr(tok_packed), _ptr(err), _stream(stream)),
+           "moe_sort")
+
+
+def moe_sort_grad(desc, grad_packed, tok_packed, grad_x, err, stream=None):
+    _check(load().moe_sort_grad(ctypes.byref(desc), _ptr(grad_packed), _ptr(tok_packed), _ptr(grad_x), _ptr(err),
+                                _stream(stream)), "moe_sort_grad")
+
+
+def moe_unsort(desc, packed_y, tok_packed, topk_weights, out, err, stream=None):
+    _check(load().moe_unsort(ctypes.byref(desc), _ptr(packed_y), _ptr(tok_packed), _ptr(topk_weights), _ptr(out),
+                             _ptr(err), _stream(stream)), "moe_unsort")
+
+
+def moe_unsort_grad(desc, packed_y, tok_packed, topk_weights, grad_out, grad_packed_y, grad_weights, err,
+                    stream=None):
+    _check(load().moe_unsort_grad(ctypes.byref(desc), _ptr(packed_y), _ptr(tok_packed), _ptr(topk_weights),
+                                  _ptr(grad_out), _ptr(grad_packed_y), _ptr(grad_weights), _ptr(err),
+                                  _stream(stream)), "moe_unsort_grad")
 
 
 def moe_get_error(err, stream=None) -> int:

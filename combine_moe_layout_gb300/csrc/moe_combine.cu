@@ -91,7 +91,7 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&acc)[8]) {
 // 668 us per combine inside the step), slower for decode-sized batches.
 constexpr int64_t kCombineTmaMinTokens = 16384;
 
-template <int K, bool PARTS>
+template <int K, bool PARTS, bool UNIT>
 __global__ void __launch_bounds__(kCombineThreads) combine_tma_kernel(CombineArgs a) {
   __shared__ __align__(128) uint4 stage[K][kCombineThreads];
   __shared__ uint64_t bar;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_tma_kernel(CombineArg
   clear_flags(a, b);
   if (tid < K) {
     int32_t slot = __ldg(a.tok_slot + tok * K + tid);
-    float w = __ldg(a.weights + tok * K + tid);
+    float w = UNIT ? 1.0f : __ldg(a.weights + tok * K + tid);
     if (slot >= a.nslots) {
       latch_error(a.err, MOE_EINVAL);
       slot = -1;
@@ -149,10 +149,11 @@ __global__ void __launch_bounds__(kCombineThreads) combine_tma_kernel(CombineArg
 }
 
 // K > 0: compile-time number of choices; K == 0: runtime k (<= kMaxTopk).
+// UNIT: every weight is 1 (the gradient of a sort), no weights are read.
 // Block b handles token b / chunks, column vectors [c*128*VPT, (c+1)*128*VPT)
 // with c = b % chunks; each thread owns VPT vectors and issues all their k
 // loads before it computes.
-template <int K, int VPT, bool PARTS>
+template <int K, int VPT, bool PARTS, bool UNIT>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a) {
   constexpr int KC = K > 0 ? K : kMaxTopk;
   const int k = K > 0 ? K : a.k;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a)
   for (int j = 0; j < KC; ++j) {
     if (j < k) {
       slot[j] = __ldg(a.tok_slot + tok * k + j);
-      w[j] = __ldg(a.weights + tok * k + j);
+      w[j] = UNIT ? 1.0f : __ldg(a.weights + tok * k + j);
       if (slot[j] >= a.nslots) {
         latch_error(a.err, MOE_EINVAL);
         slot[j] = -1;
@@ -222,17 +223,21 @@ moe_status launch_combine_k(CombineArgs a, int64_t ntok, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   use_pdl(cfg, attr);
-  const bool parts = a.parts.G > 1;
+  const bool parts = a.parts.G > 1, unit = a.weights == nullptr;  // parts always have weights
   if constexpr (K >= 4) {
     if (tma) {
-      if (cudaLaunchKernelEx(&cfg, parts ? combine_tma_kernel<K, true> : combine_tma_kernel<K, false>, a) !=
-          cudaSuccess)
+      if (cudaLaunchKernelEx(&cfg,
+                             parts ? combine_tma_kernel<K, true, false>
+                                   : (unit ? combine_tma_kernel<K, false, true> : combine_tma_kernel<K, false, false>),
+                             a) != cudaSuccess)
         return MOE_ECUDA;
       return launch_status();
     }
   }
-  if (cudaLaunchKernelEx(&cfg, parts ? combine_kernel<K, VPT, true> : combine_kernel<K, VPT, false>, a) !=
-      cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg,
+                         parts ? combine_kernel<K, VPT, true, false>
+                               : (unit ? combine_kernel<K, VPT, false, true> : combine_kernel<K, VPT, false, false>),
+                         a) != cudaSuccess)
     return MOE_ECUDA;
   return launch_status();
 }
@@ -256,6 +261,13 @@ moe_status launch_combine(const Sizes &s, const SlotParts &parts, int64_t y_rows
     case 8: return launch_combine_k<8, 1>(a, s.ntok, stream);
     default: return launch_combine_k<0, 1>(a, s.ntok, stream);
   }
+}
+
+moe_status launch_gather_sum(const Sizes &s, const uint16_t *rows, const float *weights, const int32_t *tok_packed,
+                             uint16_t *out, int32_t *err, cudaStream_t stream) {
+  SlotParts p = single_part(s, nullptr, nullptr, nullptr, nullptr, rows);
+  p.regions_per_part = 0;  // no flags to clear
+  return launch_combine(s, p, s.ntok * s.k, weights, tok_packed, out, err, stream);
 }
 
 }  // namespace moe

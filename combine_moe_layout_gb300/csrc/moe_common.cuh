@@ -400,5 +400,9 @@ moe_status launch_layout_dispatch(const Sizes &s, const int32_t *topk_idx, const
                                   int num_sms, cudaStream_t stream);
 moe_status launch_combine(const Sizes &s, const SlotParts &parts, int64_t y_rows, const float *weights,
                           const int32_t *tok_slot, uint16_t *out, int32_t *err, cudaStream_t stream);
+// Combine over packed rows with no flags: out[t] = sum_j weights[t][j] rows[tok_packed[t][j]]; null weights are 1.
+// ntok > 0.
+moe_status launch_gather_sum(const Sizes &s, const uint16_t *rows, const float *weights, const int32_t *tok_packed,
+                             uint16_t *out, int32_t *err, cudaStream_t stream);
 
 }  // namespace moe

@@ -1,0 +1,513 @@
+// Router gate: logits -> the k experts of each token and their weights, and the
+// gradient of the weights with respect to the logits.
+//
+// With l the logits of a token and b the selection bias (0 when absent):
+//   s_e = exp(l_e - max l) / sum_i exp(l_i - max l)   (softmax)
+//       = 1 / (1 + exp(-l_e))                         (sigmoid)
+//   group score = sum of the group's group_top largest s_e + b_e; the
+//     keep_groups best groups stay
+//   ids = the k largest s_e + b_e of those groups, ties to the lowest index
+//   w_j = scale s_{ids j}, divided by the sum of the chosen s when renormalised
+// Without a bias the ids are chosen by l itself: s increases with l, so the
+// order is the same and two logits whose scores round to the same 32-bit value
+// keep it. The same holds for a group score of one member.
+//
+// Gradient, with g_j = dL/dw_j:
+//   softmax, plain:         dl_e = s_e (scale g_e [e chosen] - sum_j scale g_j s_j)
+//   softmax, renormalised:  a softmax over the chosen: dl_j = v_j scale (g_j - sum_i g_i v_i),
+//                           v the weights at scale 1; 0 elsewhere
+//   sigmoid:                dl_j = ds_j s_j (1 - s_j), ds_j = scale g_j, or
+//                           scale (g_j - sum_i g_i v_i) / sum s when renormalised
+// The bias and the groups only select, so no gradient passes through them.
+//
+// Both kernels take one warp per token: a lane holds E/32 logits in registers
+// (groups of four neighbours, so a row is read with 16-byte (fp32) or 8-byte
+// (bf16) loads) and a choice is one warp maximum over order-preserving integer
+// keys and one warp minimum over the indices that hold it.
+#include <cuda_bf16.h>
+
+#include <cfloat>
+
+#include "moe_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kGateWarps = 8;
+constexpr int kGateMaxExperts = 1024;
+constexpr int kGateMaxGroups = 32;
+
+struct GateArgs {
+  const void *logits;
+  const float *bias;
+  int32_t *idx;        // [N][k]
+  float *weights;      // [N][k]
+  const float *gw;     // gradient: dL/dweights [N][k]
+  void *gl;            // gradient: dL/dlogits [N][E]
+  int32_t *err;
+  int64_t n;
+  int E, k, sigmoid, renorm, groups, keep, top, early;
+  int group_size, lanes_per_group;
+  uint64_t group_magic;  // ceil(2^32 / group_size): index / group_size = (index * magic) >> 32
+  float scale;
+};
+
+// Order-preserving key of a float (larger float, larger key), 0 for "not
+// available" (-inf). -0 and +0 share a key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Expert of value i of a lane: four neighbours per lane and pass.
+__device__ __forceinline__ int expert_of(int i, int lane) { return ((i >> 2) * 32 + lane) * 4 + (i & 3); }
+
+// A lane's logits of a row. NaN counts as -inf (and is reported), +inf as the
+// largest finite value (the limit of both scores).
+template <int VPL, bool BF16, bool VEC>
+__device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, int lane, float (&l)[VPL], bool *nan) {
+  const int64_t base = t * E;
+#pragma unroll
+  for (int p = 0; p < VPL / 4; ++p) {
+    const int e0 = (p * 32 + lane) * 4;
+    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if constexpr (VEC) {
+      if (e0 < E) {
+        if constexpr (BF16) {
+          const uint2 r = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(logits) + base + e0);
+          v[0] = __uint_as_float(r.x << 16);
+          v[1] = __uint_as_float(r.x & 0xffff0000u);
+          v[2] = __uint_as_float(r.y << 16);
+          v[3] = __uint_as_float(r.y & 0xffff0000u);
+        } else {
+          const float4 r = *reinterpret_cast<const float4 *>(static_cast<const float *>(logits) + base + e0);
+          v[0] = r.x;
+          v[1] = r.y;
+          v[2] = r.z;
+          v[3] = r.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e0 + c < E) {
+          if constexpr (BF16)
+            v[c] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(logits)[base + e0 + c]) << 16);
+          else
+            v[c] = static_cast<const float *>(logits)[base + e0 + c];
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (v[c] != v[c]) {
+        *nan = true;
+        v[c] = -INFINITY;
+      }
+      l[4 * p + c] = fminf(v[c], FLT_MAX);
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void *logits, int64_t i) {
+  float v;
+  if constexpr (BF16)
+    v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(logits)[i]) << 16);
+  else
+    v = static_cast<const float *>(logits)[i];
+  return v != v ? -INFINITY : fminf(v, FLT_MAX);
+}
+
+__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// Which groups stay, as a bit per group (the same in every lane). The warp's
+// values go through shared memory (gs); lanes_per_group lanes share a group and
+// take its group_top largest one by one.
+__device__ __forceinline__ uint32_t kept_groups(const GateArgs &a, const float *gs, int lane) {
+  const int lpg = a.lanes_per_group;
+  const int grp = lane / lpg, sub = lane - grp * lpg;
+  const bool live = grp < a.groups;
+  const float *v = gs + grp * a.group_size;
+  uint64_t taken = 0;  // bit i: value sub + i * lpg (fewer than 64 for 1024 experts)
+  float score = 0.0f;
+  int found = 0;
+  for (int r = 0; r < a.top; ++r) {
+    float best = -INFINITY;
+    int bi = a.group_size;
+    if (live)
+      for (int i = 0, x = sub; x < a.group_size; ++i, x += lpg)
+        if (!((taken >> i) & 1ull) && v[x] > best) {
+          best = v[x];
+          bi = x;
+        }
+    for (int o = lpg >> 1; o > 0; o >>= 1) {
+      const float ob = __shfl_xor_sync(0xffffffffu, best, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
+      if (ob > best || (ob == best && oi < bi)) {
+        best = ob;
+        bi = oi;
+      }
+    }
+    if (best > -INFINITY) {  // members that are not available add nothing
+      score += best;
+      ++found;
+    }
+    const int d = bi - sub;
+    if (bi < a.group_size && d >= 0 && d % lpg == 0) taken |= 1ull << (d / lpg);
+  }
+  if (!live || found == 0) score = -INFINITY;
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const float o = __shfl_sync(0xffffffffu, score, g * lpg);
+    if (o > score || (o == score && g < grp)) ++rank;
+  }
+  const uint32_t lanes = __ballot_sync(0xffffffffu, live && found > 0 && rank < a.keep);
+  uint32_t kept = 0;
+  for (int g = 0; g < a.groups; ++g) kept |= ((lanes >> (g * lpg)) & 1u) << g;
+  return kept;
+}
+
+template <int VPL, bool BF16, bool VEC>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
+  extern __shared__ float gate_sm[];  // [warps][E], with groups only
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  grid_dependency_wait();
+  if (a.early) grid_dependents_launch();
+  if (t >= a.n) return;
+
+  float l[VPL];
+  bool nan = false;
+  load_row<VPL, BF16, VEC>(a.logits, t, a.E, lane, l, &nan);
+
+  float mx = -INFINITY, sum = 1.0f;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i]);
+    mx = warp_max(mx);
+    if (mx == -INFINITY) mx = 0.0f;  // nothing available: every score is 0
+    if (!a.renorm || a.bias != nullptr || a.groups > 1) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += expf(l[i] - mx);
+      sum = warp_sum(sum);
+      if (sum == 0.0f) sum = 1.0f;
+    }
+  }
+
+  uint32_t key[VPL];
+  if (a.bias == nullptr && (a.groups <= 1 || a.top == 1)) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = order_key(l[i]);
+    if (a.groups > 1) {
+      float *gs = gate_sm + warp * a.E;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (expert_of(i, lane) < a.E) gs[expert_of(i, lane)] = l[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = expert_of(i, lane);
+      float s = -INFINITY;
+      if (e < a.E && l[i] > -INFINITY) {
+        s = a.sigmoid ? sigmoid_of(l[i]) : expf(l[i] - mx) / sum;
+        if (a.bias != nullptr) s += __ldg(a.bias + e);
+        if (s != s) {
+          nan = true;
+          s = -INFINITY;
+        }
+      }
+      if (a.groups > 1 && e < a.E) gate_sm[warp * a.E + e] = s;
+      key[i] = order_key(a.bias != nullptr ? s : l[i]);
+    }
+  }
+  if (a.groups > 1) {
+    __syncwarp();
+    const uint32_t kept = kept_groups(a, gate_sm + warp * a.E, lane);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!((kept >> ((expert_of(i, lane) * a.group_magic >> 32) & 31u)) & 1u)) key[i] = 0;
+  }
+  if (__any_sync(0xffffffffu, nan) && lane == 0) latch_error(a.err, MOE_EINVAL);
+
+  // the k choices, one warp maximum each; lane j keeps choice j
+  int my_e = -1;
+  float my_l = -INFINITY;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    if (top == 0) break;  // nothing left
+    int cand = 0x7fffffff;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == top) cand = expert_of(i, lane);
+    const int e = __reduce_min_sync(0xffffffffu, cand);
+    float lv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (expert_of(i, lane) == e) {
+        lv = l[i];
+        key[i] = 0;
+      }
+    lv = __shfl_sync(0xffffffffu, lv, (e >> 2) & 31);
+    if (lane == j) {
+      my_e = e;
+      my_l = lv;
+    }
+  }
+
+  float w = 0.0f;
+  if (a.sigmoid) {
+    if (my_e >= 0) w = sigmoid_of(my_l);
+    if (a.renorm) {
+      const float s = warp_sum(w);
+      w = s > 0.0f ? w / s : 0.0f;
+    }
+  } else if (a.renorm) {
+    const float m = warp_max(my_l);
+    if (my_e >= 0) w = expf(my_l - m);
+    const float s = warp_sum(w);
+    w = s > 0.0f ? w / s : 0.0f;
+  } else if (my_e >= 0) {
+    w = expf(my_l - mx) / sum;
+  }
+  if (lane < a.k) {
+    a.idx[t * a.k + lane] = my_e;
+    a.weights[t * a.k + lane] = w * a.scale;
+  }
+}
+
+template <int VPL, bool BF16, bool VEC>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  grid_dependency_wait();
+  if (a.early) grid_dependents_launch();
+  if (t >= a.n) return;
+
+  int my_e = -1;
+  float g = 0.0f, my_l = -INFINITY;
+  if (lane < a.k) {
+    my_e = a.idx[t * a.k + lane];
+    if (my_e < 0 || my_e >= a.E) {
+      if (my_e != kMaskedExpert) latch_error(a.err, MOE_EINVAL);
+      my_e = -1;
+    } else {
+      g = a.gw[t * a.k + lane] * a.scale;
+      my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
+    }
+  }
+  float out[VPL];
+  float d = 0.0f;  // dL/dl of this lane's choice
+  if (a.sigmoid) {
+    const float s = my_e >= 0 ? sigmoid_of(my_l) : 0.0f;
+    if (a.renorm) {
+      const float total = warp_sum(s);
+      if (total > 0.0f) {
+        const float mean = warp_sum(g * (s / total));
+        d = (g - mean) / total * s * (1.0f - s);
+      }
+    } else {
+      d = g * s * (1.0f - s);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
+  } else if (a.renorm) {
+    const float m = warp_max(my_l);
+    const float p = my_l > -INFINITY ? expf(my_l - m) : 0.0f;
+    const float total = warp_sum(p);
+    if (total > 0.0f) {
+      const float v = p / total;
+      d = v * (g - warp_sum(g * v));
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
+  } else {
+    float l[VPL];
+    bool nan = false;
+    load_row<VPL, BF16, VEC>(a.logits, t, a.E, lane, l, &nan);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i]);
+    mx = warp_max(mx);
+    if (mx == -INFINITY) mx = 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = expf(l[i] - mx);
+      sum += l[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    d = my_l > -INFINITY ? g * (expf(my_l - mx) * inv) : 0.0f;
+    const float total = warp_sum(d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) out[i] = -total * (l[i] * inv);
+  }
+  if (my_e < 0) d = 0.0f;
+  for (int j = 0; j < a.k; ++j) {
+    const int e = __shfl_sync(0xffffffffu, my_e, j);
+    const float dj = __shfl_sync(0xffffffffu, d, j);
+    if (e < 0) continue;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (expert_of(i, lane) == e) out[i] += dj;
+  }
+  const int64_t base = t * a.E;
+#pragma unroll
+  for (int p = 0; p < VPL / 4; ++p) {
+    const int e0 = (p * 32 + lane) * 4;
+    if constexpr (VEC) {
+      if (e0 >= a.E) continue;
+      if constexpr (BF16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(out[4 * p], out[4 * p + 1]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(out[4 * p + 2], out[4 * p + 3]);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.gl) + base + e0) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+      } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.gl) + base + e0) =
+            make_float4(out[4 * p], out[4 * p + 1], out[4 * p + 2], out[4 * p + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e0 + c < a.E) {
+          if constexpr (BF16)
+            static_cast<__nv_bfloat16 *>(a.gl)[base + e0 + c] = __float2bfloat16_rn(out[4 * p + c]);
+          else
+            static_cast<float *>(a.gl)[base + e0 + c] = out[4 * p + c];
+        }
+    }
+  }
+}
+
+template <int VPL>
+moe_status launch_gate_v(const GateArgs &a, bool bf16, bool vec, bool grad, cudaStream_t stream) {
+  void (*fn)(GateArgs) =
+      grad ? (bf16 ? (vec ? gate_grad_kernel<VPL, true, true> : gate_grad_kernel<VPL, true, false>)
+                   : (vec ? gate_grad_kernel<VPL, false, true> : gate_grad_kernel<VPL, false, false>))
+           : (bf16 ? (vec ? gate_kernel<VPL, true, true> : gate_kernel<VPL, true, false>)
+                   : (vec ? gate_kernel<VPL, false, true> : gate_kernel<VPL, false, false>));
+  cudaLaunchConfig_t cfg = {};
+  const int64_t blocks = (a.n + kGateWarps - 1) / kGateWarps;
+  if (blocks > 0x7fffffffll) return MOE_EINVAL;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(kGateWarps * 32, 1, 1);
+  // at most 8 warps x 1024 experts x 4 bytes = 32 KB
+  cfg.dynamicSmemBytes = !grad && a.groups > 1 ? static_cast<size_t>(kGateWarps) * a.E * sizeof(float) : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  use_pdl(cfg, attr);
+  if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_status();
+}
+
+moe_status launch_gate(const GateArgs &a, bool bf16, bool grad, cudaStream_t stream) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | (grad ? reinterpret_cast<uintptr_t>(a.gl) : 0);
+  const bool vec = a.E % 4 == 0 && (at & (bf16 ? 7u : 15u)) == 0;
+  if (a.E <= 128) return launch_gate_v<4>(a, bf16, vec, grad, stream);
+  if (a.E <= 256) return launch_gate_v<8>(a, bf16, vec, grad, stream);
+  if (a.E <= 512) return launch_gate_v<16>(a, bf16, vec, grad, stream);
+  return launch_gate_v<32>(a, bf16, vec, grad, stream);
+}
+
+moe_status gate_args(const moe_desc *desc, const moe_gate_opts *o, GateArgs *a) {
+  Sizes s;
+  const moe_status st = check_desc(desc, &s);
+  if (st != MOE_OK) return st;
+  if (o == nullptr || s.E > kGateMaxExperts) return MOE_EINVAL;
+  if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+  if ((o->renormalize | o->logits_bf16) & ~1) return MOE_EINVAL;
+  if (!(o->scale - o->scale == 0.0f)) return MOE_EINVAL;  // not finite
+  const int g = o->num_groups;
+  if (g < 0 || g > kGateMaxGroups) return MOE_EINVAL;
+  *a = GateArgs{};
+  a->n = s.ntok;
+  a->E = s.E;
+  a->k = s.k;
+  a->sigmoid = o->score == MOE_SCORE_SIGMOID;
+  a->renorm = o->renormalize;
+  a->scale = o->scale;
+  a->early = early_trigger(s.ntok);
+  a->groups = 1;
+  if (g > 1) {
+    if (s.E % g != 0) return MOE_EINVAL;
+    const int size = s.E / g;
+    if (o->keep_groups < 1 || o->keep_groups > g || o->group_top < 1 || o->group_top > size ||
+        static_cast<int64_t>(o->keep_groups) * size < s.k)
+      return MOE_EINVAL;
+    a->groups = g;
+    a->keep = o->keep_groups;
+    a->top = o->group_top;
+    a->group_size = size;
+    a->group_magic = ((1ull << 32) + size - 1) / size;
+    int lpg = 32;
+    while (lpg * g > 32) lpg >>= 1;
+    a->lanes_per_group = lpg;
+  }
+  return MOE_OK;
+}
+
+bool aligned_elem(const void *p, bool bf16) { return (reinterpret_cast<uintptr_t>(p) & (bf16 ? 1u : 3u)) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_gate(const moe_desc *desc, const moe_gate_opts *opts, const void *logits, const float *bias,
+                               int32_t *topk_idx, float *topk_weights, int32_t *err, void *stream) {
+  GateArgs a;
+  const moe_status st = gate_args(desc, opts, &a);
+  if (st != MOE_OK) return st;
+  if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
+  if (a.n == 0) return MOE_OK;
+  const bool bf16 = opts->logits_bf16 != 0;
+  if (logits == nullptr || topk_idx == nullptr || topk_weights == nullptr) return MOE_EINVAL;
+  if (!aligned_elem(logits, bf16) || !aligned4(bias) || !aligned4(topk_idx) || !aligned4(topk_weights))
+    return MOE_EINVAL;
+  a.logits = logits;
+  a.bias = bias;
+  a.idx = topk_idx;
+  a.weights = topk_weights;
+  a.err = err;
+  return launch_gate(a, bf16, false, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status moe_gate_grad(const moe_desc *desc, const moe_gate_opts *opts, const void *logits,
+                                    const int32_t *topk_idx, const float *grad_weights, void *grad_logits,
+                                    int32_t *err, void *stream) {
+  GateArgs a;
+  const moe_status st = gate_args(desc, opts, &a);
+  if (st != MOE_OK) return st;
+  if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
+  if (a.n == 0) return MOE_OK;
+  const bool bf16 = opts->logits_bf16 != 0;
+  if (logits == nullptr || topk_idx == nullptr || grad_weights == nullptr || grad_logits == nullptr)
+    return MOE_EINVAL;
+  if (!aligned_elem(logits, bf16) || !aligned_elem(grad_logits, bf16) || !aligned4(topk_idx) ||
+      !aligned4(grad_weights))
+    return MOE_EINVAL;
+  a.logits = logits;
+  a.idx = const_cast<int32_t *>(topk_idx);
+  a.gw = grad_weights;
+  a.gl = grad_logits;
+  a.err = err;
+  return launch_gate(a, bf16, true, static_cast<cudaStream_t>(stream));
+}

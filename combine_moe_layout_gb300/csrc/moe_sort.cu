@@ -1,0 +1,450 @@
+// Token sort: the rows of one device's tokens in expert order and back, with
+// their gradients. The packed layout is the receive hook's (rows in (expert,
+// source rank, token) order, region offsets, the forward map tok_packed), made
+// from the tokens directly: no slots, flags or per-region bound, and half the
+// bytes.
+//
+//   sort         packed[p(t, j)] = x[t]
+//   sort_grad    dx[t] = sum_j dpacked[p(t, j)]
+//   unsort       out[t] = sum_j w[t][j] y[p(t, j)]
+//   unsort_grad  dy[p(t, j)] = w[t][j] dout[t],  dw[t][j] = sum_h y[p(t, j)][h] dout[t][h]
+//
+// p(t, j) is the rank of (expert, t, j) among the choices that name an expert,
+// so it is the same on every run. All four move each row once per choice and
+// are bound by HBM; the forward map lets each of them walk the tokens and read
+// or write the token's own row once.
+//
+// Ranking: one thread-block cluster over the flattened choices, cut into one
+// contiguous piece per warp. Every warp counts its piece per expert in its own
+// shared-memory row (equal experts of 32 choices found with match.any, so no
+// atomics), a scan over the warps, the cluster's CTAs (distributed shared
+// memory) and the experts turns the counts into positions, and a second pass
+// over the piece hands them out in order. A warp whose piece holds the first
+// choice of a source rank reads that rank's region offsets off its counters.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "moe_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kRankThreads = 1024;
+constexpr int kRankMaxCluster = 8;
+constexpr int kRankMaxExperts = 8192;
+constexpr int kRankSmem = 200 * 1024;
+constexpr int kRankBatch = 8;  // loads in flight per lane
+
+struct RankArgs {
+  const int32_t *topk_idx;
+  int32_t *region_offsets;  // [E * R + 1]
+  int32_t *tok_packed;      // [R * T * k]
+  int32_t *err;
+  int64_t n;                // R * T * k
+  int64_t per_rank;         // T * k
+  int64_t per_warp;         // choices of a warp's piece: a multiple of 32
+  int E, R, warps, early;   // warps: warps per CTA that take a piece
+};
+
+// The expert of choice i, or -1 for a masked or invalid one.
+__device__ __forceinline__ int expert_at(const RankArgs &a, int64_t i, int64_t end, bool *bad) {
+  if (i >= end) return -1;
+  const int e = __ldg(a.topk_idx + i);
+  if (e >= 0 && e < a.E) return e;
+  if (e != kMaskedExpert) *bad = true;
+  return -1;
+}
+
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(RankArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ int32_t rsm[];
+  int32_t *hist = rsm;                      // [warps][E]: counts, then positions
+  int32_t *total = hist + a.warps * a.E;    // [E]: counts of this CTA
+  int32_t *base = total + a.E;              // [E]: position of this CTA's first choice of an expert
+  __shared__ int32_t warp_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+
+  grid_dependency_wait();
+  if (a.early) grid_dependents_launch();
+  for (int i = tid; i < a.warps * a.E; i += kRankThreads) hist[i] = 0;
+  __syncthreads();
+
+  const int64_t c0 = min((static_cast<int64_t>(cta) * a.warps + warp) * a.per_warp, a.n);
+  const int64_t c1 = warp < a.warps ? min(c0 + a.per_warp, a.n) : c0;
+  int32_t *mine = hist + warp * a.E;
+  bool bad = false;
+  for (int64_t i0 = c0; i0 < c1; i0 += 32 * kRankBatch) {
+    int e[kRankBatch];
+#pragma unroll
+    for (int b = 0; b < kRankBatch; ++b) e[b] = expert_at(a, i0 + b * 32 + lane, c1, &bad);
+#pragma unroll
+    for (int b = 0; b < kRankBatch; ++b) {
+      const unsigned same = __match_any_sync(0xffffffffu, e[b]);
+      if (e[b] >= 0 && lane == __ffs(same) - 1) mine[e[b]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  if (bad) latch_error(a.err, MOE_EINVAL);
+  __syncthreads();
+
+  for (int e = tid; e < a.E; e += kRankThreads) {
+    int run = 0;
+    for (int w = 0; w < a.warps; ++w) {
+      const int c = hist[w * a.E + e];
+      hist[w * a.E + e] = run;
+      run += c;
+    }
+    total[e] = run;
+  }
+  cluster.sync();  // every CTA's counts are visible to the cluster
+
+  // exclusive scan over the experts of the cluster's counts: thread tid owns experts [e0, e1)
+  const int per = (a.E + kRankThreads - 1) / kRankThreads;
+  const int e0 = min(tid * per, a.E), e1 = min(e0 + per, a.E);
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    int all = 0, before = 0;
+    for (int q = 0; q < ctas; ++q) {
+      const int c = *cluster.map_shared_rank(total + e, q);
+      if (q < cta) before += c;
+      all += c;
+    }
+    base[e] = sum + before;
+    sum += all;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int first = incl - sum;
+  for (int w = 0; w < warp; ++w) first += warp_sums[w];
+  for (int e = e0; e < e1; ++e) base[e] += first;
+  if (cta == 0 && tid == kRankThreads - 1) a.region_offsets[static_cast<int64_t>(a.E) * a.R] = first + sum;
+  __syncthreads();
+  for (int i = tid; i < a.warps * a.E; i += kRankThreads) hist[i] += base[i % a.E];
+  __syncthreads();
+
+  // the choices of the piece in order, source rank by source rank
+  for (int64_t i = c0; i < c1;) {
+    const int64_t src = i / a.per_rank;
+    const int64_t end = min((src + 1) * a.per_rank, c1);
+    if (i == src * a.per_rank)
+      for (int e = lane; e < a.E; e += 32) a.region_offsets[static_cast<int64_t>(e) * a.R + src] = mine[e];
+    __syncwarp();
+    for (int64_t i0 = i; i0 < end; i0 += 32 * kRankBatch) {
+      int e[kRankBatch];
+#pragma unroll
+      for (int b = 0; b < kRankBatch; ++b) e[b] = expert_at(a, i0 + b * 32 + lane, end, &bad);
+#pragma unroll
+      for (int b = 0; b < kRankBatch; ++b) {
+        const unsigned same = __match_any_sync(0xffffffffu, e[b]);
+        const int at = e[b] >= 0 ? mine[e[b]] : 0;
+        __syncwarp();
+        if (e[b] >= 0 && lane == __ffs(same) - 1) mine[e[b]] = at + __popc(same);
+        __syncwarp();
+        const int64_t c = i0 + b * 32 + lane;
+        if (c < end) a.tok_packed[c] = e[b] >= 0 ? at + __popc(same & ((1u << lane) - 1u)) : -1;
+      }
+    }
+    i = end;
+  }
+  cluster.sync();  // no CTA leaves while another may still read its counts
+}
+
+__global__ void empty_offsets_kernel(int32_t *region_offsets, int64_t n) {
+  grid_dependency_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i < n) region_offsets[i] = 0;
+}
+
+// Row copy: thread v of a token's row loads 16 bytes once and stores them to
+// the token's k packed rows; the thread at the start of each 128 bytes carries
+// the scale of that block too.
+struct RowArgs {
+  const uint8_t *x;
+  const float *scales;
+  const int32_t *tok_packed;
+  uint8_t *packed;
+  float *packed_scales;
+  int32_t *err;
+  int64_t ntok, nrows;
+  int V, k, nsc;          // V: 16-byte vectors of a row
+  int tpb, chunks, vpc;   // tokens per block; chunks of vpc vectors per row
+};
+
+template <bool QUANT>
+__global__ void __launch_bounds__(256) sort_rows_kernel(RowArgs a) {
+  const int tl = threadIdx.x / a.vpc, vl = threadIdx.x - tl * a.vpc;
+  const int64_t blk = blockIdx.x / a.chunks;
+  const int v = static_cast<int>(blockIdx.x - blk * a.chunks) * a.vpc + vl;
+  const int64_t t = blk * a.tpb + tl;
+  const bool live = tl < a.tpb && t < a.ntok && v < a.V;
+  grid_dependency_wait();
+  if constexpr (QUANT) {
+    // 8 bf16 elements a thread; 16 neighbouring threads share a 128-element block
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (live) r = __ldcs(reinterpret_cast<const uint4 *>(a.x) + t * a.V + v);
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+    float f[8];
+    float amax = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[2 * q] = __uint_as_float(u[q] << 16);
+      f[2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+      amax = fmaxf(amax, fmaxf(fabsf(f[2 * q]), fabsf(f[2 * q + 1])));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const BlockScale bs = block_scale(amax);
+    uint32_t c[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      c[q] = static_cast<uint32_t>(e4m3x2_of_quotients(f[4 * q], f[4 * q + 1], bs)) |
+             (static_cast<uint32_t>(e4m3x2_of_quotients(f[4 * q + 2], f[4 * q + 3], bs)) << 16);
+    if (!live) return;
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t p = __ldg(a.tok_packed + t * a.k + j);
+      if (p < 0) continue;
+      reinterpret_cast<uint2 *>(a.packed)[static_cast<int64_t>(p) * a.V + v] = make_uint2(c[0], c[1]);
+      if ((v & 15) == 0) a.packed_scales[static_cast<int64_t>(p) * a.nsc + (v >> 4)] = bs.s;
+    }
+  } else {
+    if (!live) return;
+    const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(a.x) + t * a.V + v);
+    float sc = 0.0f;
+    const bool has = a.nsc > 0 && (v & 7) == 0;
+    if (has) sc = a.scales[t * a.nsc + (v >> 3)];
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t p = __ldg(a.tok_packed + t * a.k + j);
+      if (p < 0) continue;
+      reinterpret_cast<uint4 *>(a.packed)[static_cast<int64_t>(p) * a.V + v] = r;
+      if (has) a.packed_scales[static_cast<int64_t>(p) * a.nsc + (v >> 3)] = sc;
+    }
+  }
+}
+
+// Gradients of unsort: one CTA per token holds its piece of dout in registers
+// and walks the k choices, loading y, storing w * dout and adding up y . dout.
+struct UnsortGradArgs {
+  const uint16_t *y;
+  const int32_t *tok_packed;
+  const float *weights;
+  const uint16_t *gout;
+  uint16_t *gy;
+  float *gw;  // may be null
+  int32_t *err;
+  int64_t nrows;
+  int V, k;
+};
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &r, float (&f)[8]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = __uint_as_float(u[q] << 16);
+    f[2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 scale_bf16x8(const float (&f)[8], float w) {
+  uint32_t u[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * q] * w, f[2 * q + 1] * w);
+    u[q] = *reinterpret_cast<const uint32_t *>(&p);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+constexpr int kUnsortGradMaxWarps = 8;
+
+__global__ void __launch_bounds__(kUnsortGradMaxWarps * 32) unsort_grad_kernel(UnsortGradArgs a) {
+  __shared__ float part[kMaxTopk][kUnsortGradMaxWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int64_t t = blockIdx.x;
+  grid_dependency_wait();
+  const uint4 *g = reinterpret_cast<const uint4 *>(a.gout) + t * a.V;
+  for (int j = 0; j < a.k; ++j) {
+    const int32_t p = __ldg(a.tok_packed + t * a.k + j);
+    if (p >= a.nrows && tid == 0) latch_error(a.err, MOE_EINVAL);
+    float dot = 0.0f;
+    if (p >= 0 && p < a.nrows) {
+      const float w = __ldg(a.weights + t * a.k + j);
+      const uint4 *y = reinterpret_cast<const uint4 *>(a.y) + static_cast<int64_t>(p) * a.V;
+      uint4 *gy = reinterpret_cast<uint4 *>(a.gy) + static_cast<int64_t>(p) * a.V;
+      for (int v = tid; v < a.V; v += nt) {
+        float gf[8], yf[8];
+        unpack_bf16x8(__ldg(g + v), gf);
+        unpack_bf16x8(__ldcs(y + v), yf);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dot = fmaf(yf[q], gf[q], dot);
+        __stcs(gy + v, scale_bf16x8(gf, w));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) part[j][warp] = dot;
+  }
+  __syncthreads();
+  if (a.gw != nullptr && tid < a.k) {
+    float s = 0.0f;
+    for (int w = 0; w < nt / 32; ++w) s += part[tid][w];
+    a.gw[t * a.k + tid] = s;
+  }
+}
+
+// Cluster shape of the ranking: one CTA up to 8192 choices (a cluster barrier
+// costs more than the passes it would split), then one more per 8192.
+moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_offsets, int32_t *tok_packed,
+                       int32_t *err, cudaStream_t stream) {
+  if (s.E > kRankMaxExperts) return MOE_EINVAL;
+  const int64_t n = s.ntok * s.k;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = MOE_PDL;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (n == 0) {
+    const int64_t words = static_cast<int64_t>(s.E) * s.R + 1;
+    cfg.gridDim = dim3(static_cast<unsigned>((words + 255) / 256), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    if (cudaLaunchKernelEx(&cfg, empty_offsets_kernel, region_offsets, words) != cudaSuccess) return MOE_ECUDA;
+    return launch_status();
+  }
+  int warps = kRankSmem / 4 / s.E - 2;
+  if (warps > kRankThreads / 32) warps = kRankThreads / 32;
+  if (warps < 1) return MOE_EINVAL;
+  int64_t ctas = (n + 8191) / 8192;
+  if (ctas > kRankMaxCluster) ctas = kRankMaxCluster;
+  const int64_t pieces = ctas * warps;
+  const int64_t per_warp = ((n + pieces - 1) / pieces + 31) / 32 * 32;
+  const size_t smem = static_cast<size_t>(warps + 2) * s.E * sizeof(int32_t);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem)) != cudaSuccess)
+    return MOE_ECUDA;
+  RankArgs a{topk_idx, region_offsets, tok_packed, err, n, static_cast<int64_t>(s.T) * s.k, per_warp,
+             s.E, s.R, warps, early_trigger(s.ntok)};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kRankThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, rank_kernel, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_status();
+}
+
+moe_status launch_sort_rows(const Sizes &s, const void *x, const float *x_scales, const int32_t *tok_packed,
+                            void *packed, float *packed_scales, int32_t *err, cudaStream_t stream) {
+  const int V = static_cast<int>(s.in_row_bytes / 16);
+  RowArgs a{static_cast<const uint8_t *>(x), x_scales, tok_packed, static_cast<uint8_t *>(packed), packed_scales,
+            err, s.ntok, s.ntok * s.k, V, s.k, s.nsc, 1, 1, V};
+  // blocks of at most 256 threads, cut so that the threads of a row's last block are not idle; whole 16-lane
+  // groups (a quantised block) stay together
+  a.chunks = (V + 255) / 256;
+  a.vpc = (V + a.chunks - 1) / a.chunks;
+  if (a.chunks > 1) a.vpc = (a.vpc + 31) / 32 * 32;
+  a.chunks = (V + a.vpc - 1) / a.vpc;
+  a.tpb = a.chunks > 1 ? 1 : 256 / a.vpc;
+  const int64_t blocks = (s.ntok + a.tpb - 1) / a.tpb * a.chunks;
+  if (blocks > 0x7fffffffll) return MOE_EINVAL;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>((a.tpb * a.vpc + 31) / 32 * 32), 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  use_pdl(cfg, attr);
+  if (cudaLaunchKernelEx(&cfg, s.quant ? sort_rows_kernel<true> : sort_rows_kernel<false>, a) != cudaSuccess)
+    return MOE_ECUDA;
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_sort(const moe_desc *desc, const int32_t *topk_idx, const void *x, const float *x_scales,
+                               int32_t *region_offsets, void *packed_x, float *packed_scales, int32_t *tok_packed,
+                               int32_t *err, void *stream) {
+  Sizes s;
+  moe_status st = check_desc(desc, &s);
+  if (st != MOE_OK) return st;
+  if (region_offsets == nullptr || err == nullptr || !aligned4(region_offsets) || !aligned4(err)) return MOE_EINVAL;
+  if (s.ntok > 0) {
+    if (topk_idx == nullptr || x == nullptr || packed_x == nullptr || tok_packed == nullptr) return MOE_EINVAL;
+    if (s.nsc > 0 && packed_scales == nullptr) return MOE_EINVAL;
+    if (s.dtype == MOE_FP8_E4M3 && x_scales == nullptr) return MOE_EINVAL;
+    if (!aligned4(topk_idx) || !aligned16(x) || !aligned4(x_scales) || !aligned16(packed_x) ||
+        !aligned4(packed_scales) || !aligned4(tok_packed))
+      return MOE_EINVAL;
+  }
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  st = launch_rank(s, topk_idx, region_offsets, tok_packed, err, cs);
+  if (st != MOE_OK || s.ntok == 0) return st;
+  return launch_sort_rows(s, x, x_scales, tok_packed, packed_x, packed_scales, err, cs);
+}
+
+extern "C" moe_status moe_sort_grad(const moe_desc *desc, const uint16_t *grad_packed, const int32_t *tok_packed,
+                                    uint16_t *grad_x, int32_t *err, void *stream) {
+  Sizes s;
+  const moe_status st = check_desc(desc, &s);
+  if (st != MOE_OK) return st;
+  if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
+  if (s.ntok == 0) return MOE_OK;
+  if (grad_packed == nullptr || tok_packed == nullptr || grad_x == nullptr) return MOE_EINVAL;
+  if (!aligned16(grad_packed) || !aligned4(tok_packed) || !aligned16(grad_x)) return MOE_EINVAL;
+  return launch_gather_sum(s, grad_packed, nullptr, tok_packed, grad_x, err, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status moe_unsort(const moe_desc *desc, const uint16_t *packed_y, const int32_t *tok_packed,
+                                 const float *topk_weights, uint16_t *out, int32_t *err, void *stream) {
+  Sizes s;
+  const moe_status st = check_desc(desc, &s);
+  if (st != MOE_OK) return st;
+  if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
+  if (s.ntok == 0) return MOE_OK;
+  if (packed_y == nullptr || tok_packed == nullptr || topk_weights == nullptr || out == nullptr) return MOE_EINVAL;
+  if (!aligned16(packed_y) || !aligned4(tok_packed) || !aligned4(topk_weights) || !aligned16(out)) return MOE_EINVAL;
+  return launch_gather_sum(s, packed_y, topk_weights, tok_packed, out, err, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status moe_unsort_grad(const moe_desc *desc, const uint16_t *packed_y, const int32_t *tok_packed,
+                                      const float *topk_weights, const uint16_t *grad_out, uint16_t *grad_packed_y,
+                                      float *grad_weights, int32_t *err, void *stream) {
+  Sizes s;
+  const moe_status st = check_desc(desc, &s);
+  if (st != MOE_OK) return st;
+  if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
+  if (s.ntok == 0) return MOE_OK;
+  if (packed_y == nullptr || tok_packed == nullptr || topk_weights == nullptr || grad_out == nullptr ||
+      grad_packed_y == nullptr)
+    return MOE_EINVAL;
+  if (!aligned16(packed_y) || !aligned4(tok_packed) || !aligned4(topk_weights) || !aligned16(grad_out) ||
+      !aligned16(grad_packed_y) || !aligned4(grad_weights))
+    return MOE_EINVAL;
+  if (s.ntok > 0x7fffffffll) return MOE_EINVAL;
+  UnsortGradArgs a{packed_y, tok_packed, topk_weights, grad_out, grad_packed_y, grad_weights, err, s.ntok * s.k,
+                   s.H / 8, s.k};
+  int warps = (a.V + 31) / 32;
+  if (warps > kUnsortGradMaxWarps) warps = kUnsortGradMaxWarps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(s.ntok), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(warps) * 32, 1, 1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  use_pdl(cfg, attr);
+  if (cudaLaunchKernelEx(&cfg, unsort_grad_kernel, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_status();
+}

@@ -380,6 +380,112 @@ moe_status moe_expert_stub_parts(const moe_desc *desc, const moe_parts *parts, c
 /* moe_reset over parts: clears every part's flags and the error word. */
 moe_status moe_reset_parts(const moe_desc *desc, const moe_parts *parts, int32_t *err, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the experts of one device: the router, the token sort and its way
+ * back, each with its gradient. Of the desc they use R, T, H, E, k and dtype
+ * (num_sms is ignored; max_m only has to satisfy the desc rules); a device that
+ * is no part of an EP group uses R = 1. Tensors are device memory. None of them
+ * uses the count + 1 flags, keeps state or allocates. The results do not depend
+ * on timing: every sum has a fixed order.
+ * --------------------------------------------------------------------------- */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t score;       /* moe_score of the logits */
+  int32_t renormalize; /* 1: the k weights are divided by their sum */
+  int32_t num_groups;  /* 0 or 1: none; else groups of E / num_groups contiguous experts, at most 32 */
+  int32_t keep_groups; /* with groups: how many of them a token may choose from */
+  int32_t group_top;   /* with groups: a group's score is the sum of its group_top best */
+  int32_t logits_bf16; /* 0: float logits, 1: bfloat16 */
+  float scale;         /* factor of every weight */
+} moe_gate_opts;
+
+/* Router ("NVSHMEM and DeepEP", high-throughput section, for the group-limited
+ * form): the k experts of each token and their weights.
+ *   s = softmax(logits) or 1 / (1 + exp(-logits)), in fp32;
+ *   with groups, the keep_groups groups with the largest sum of their
+ *   group_top largest s + bias stay (ties to the lower group);
+ *   topk_idx = the k experts left with the largest s + bias, largest first, ties
+ *   to the lowest expert; without a bias the order is that of the logits
+ *   themselves, also where 32-bit scores are equal;
+ *   topk_weights = scale * s of the chosen (without the bias), divided by their
+ *   sum when renormalize (0 where that sum is 0).
+ * An expert whose logit (or s + bias) is -inf is never chosen; when fewer than k
+ * are left the remaining entries are -1 with weight 0, the masked choices of
+ * moe_layout and moe_sort. A logit of +inf counts as the largest finite float.
+ *   logits [R][T][E] float or bfloat16; bias [E] float or NULL (read);
+ *   topk_idx [R][T][k] int32, topk_weights [R][T][k] float (written).
+ * E at most 1024. Host errors: MOE_EINVAL (also keep_groups * E / num_groups < k,
+ * a scale that is not finite). Device errors: a NaN logit, or NaN s + bias ->
+ * MOE_EINVAL (the expert counts as -inf). */
+moe_status moe_gate(const moe_desc *desc, const moe_gate_opts *opts, const void *logits, const float *bias,
+                    int32_t *topk_idx, float *topk_weights, int32_t *err, void *stream);
+
+/* Gradient of moe_gate's weights with respect to the logits (the choice itself
+ * and the bias have none):
+ *   softmax:              dl_e = s_e (scale g_e [e chosen] - sum_j scale g_j s_j)
+ *   softmax, renormalize: dl_j = w_j (g_j - sum_i g_i w_i / scale), 0 elsewhere
+ *   sigmoid:              dl_j = d_j s_j (1 - s_j), 0 elsewhere, with d_j = scale g_j, or
+ *                         (scale g_j - sum_i g_i w_i) / sum_i s_i when renormalize
+ * over the chosen experts j, in fp32 and rounded once.
+ *   logits, topk_idx as moe_gate has them (an entry of -1 takes no part);
+ *   grad_weights [R][T][k] float (read); grad_logits [R][T][E], the logits' type
+ *   (written whole).
+ * Device errors: an expert id outside [0, E) other than -1 -> MOE_EINVAL (it
+ * takes no part). */
+moe_status moe_gate_grad(const moe_desc *desc, const moe_gate_opts *opts, const void *logits, const int32_t *topk_idx,
+                         const float *grad_weights, void *grad_logits, int32_t *err, void *stream);
+
+/* Token sort: the rows of the R*T tokens packed by expert, in the layout of
+ * moe_dispatch_recv, with no slots or flags in between. Packed rows are in
+ * (expert, source rank, token, choice) order:
+ *   region_offsets[e*R + src] = packed rows before those of (e, src),
+ *   region_offsets[E*R] = their total; tok_packed[src][t][j] = the packed row of
+ *   choice j, -1 for a masked choice (-1 in topk_idx).
+ * They feed moe_expert_gate_up and its fp8 form as the receive hook's do, and
+ * moe_unsort. An expert may repeat within a token.
+ *   topk_idx [R][T][k] int32; x [R][T] rows of desc dtype (bf16, e4m3 with
+ *   x_scales [R][T][H/128], or bf16 quantised on the way as in moe_dispatch)
+ *   (read); region_offsets [E*R + 1] int32, packed_x [R*T*k] rows, packed_scales
+ *   [R*T*k][H/128] float (NULL for bf16), tok_packed [R][T][k] int32 (written;
+ *   packed rows at or above the total are not touched). Rows 16-byte aligned.
+ * Host errors: MOE_EINVAL, also for more than 8192 experts. Device errors: any
+ * other expert id outside [0, E) -> MOE_EINVAL (a masked choice). */
+moe_status moe_sort(const moe_desc *desc, const int32_t *topk_idx, const void *x, const float *x_scales,
+                    int32_t *region_offsets, void *packed_x, float *packed_scales, int32_t *tok_packed, int32_t *err,
+                    void *stream);
+
+/* Gradient of moe_sort with respect to x: grad_x[src][t] = bf16_rne( sum_j
+ * grad_packed[tok_packed[src][t][j]] ), in fp32 and choice order; 0 for a token
+ * with every choice masked. The gradient of quantised rows passes the quantiser
+ * as if it were the identity.
+ *   grad_packed [R*T*k][H] bf16, tok_packed (read); grad_x [R][T][H] bf16
+ *   (written), both row buffers 16-byte aligned.
+ * Device errors: tok_packed >= R*T*k -> MOE_EINVAL (the term is skipped). */
+moe_status moe_sort_grad(const moe_desc *desc, const uint16_t *grad_packed, const int32_t *tok_packed,
+                         uint16_t *grad_x, int32_t *err, void *stream);
+
+/* The way back: out[src][t] = bf16_rne( sum_j topk_weights[src][t][j] *
+ * packed_y[tok_packed[src][t][j]] ), as moe_combine_packed, without flags.
+ *   packed_y [R*T*k][H] bf16, tok_packed, topk_weights [R][T][k] float (read);
+ *   out [R][T][H] bf16 (written), both row buffers 16-byte aligned.
+ * Device errors: tok_packed >= R*T*k -> MOE_EINVAL (the term is skipped). */
+moe_status moe_unsort(const moe_desc *desc, const uint16_t *packed_y, const int32_t *tok_packed,
+                      const float *topk_weights, uint16_t *out, int32_t *err, void *stream);
+
+/* Gradients of moe_unsort: for every choice with a packed row p = tok_packed[src][t][j],
+ *   grad_packed_y[p] = bf16_rne( topk_weights[src][t][j] * grad_out[src][t] ),
+ *   grad_weights[src][t][j] = sum_h packed_y[p][h] * grad_out[src][t][h] in fp32;
+ * a choice without one gets grad_weights 0.
+ *   packed_y, tok_packed, topk_weights as moe_unsort; grad_out [R][T][H] bf16
+ *   (read); grad_packed_y [R*T*k][H] bf16 (written for packed rows only);
+ *   grad_weights [R][T][k] float, or NULL when it is not wanted (written). Row
+ *   buffers 16-byte aligned.
+ * Device errors: tok_packed >= R*T*k -> MOE_EINVAL (the choice is skipped). */
+moe_status moe_unsort_grad(const moe_desc *desc, const uint16_t *packed_y, const int32_t *tok_packed,
+                           const float *topk_weights, const uint16_t *grad_out, uint16_t *grad_packed_y,
+                           float *grad_weights, int32_t *err, void *stream);
+
 /* Synchronise `stream`, read the device error word, clear it, and return its
  * value (MOE_OK if no kernel latched an error). Host-synchronising. */
 moe_status moe_get_error(int32_t *err, void *stream);
