@@ -57,6 +57,18 @@ class MoeGateOpts(ctypes.Structure):
     ]
 
 
+class MoeLoraDesc(ctypes.Structure):
+    """A shared projection with low-rank adapters (moe_lora_desc of include/moe_layout.h)."""
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32),
+        ("in_dim", ctypes.c_int32),
+        ("out_dim", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("num_adapters", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+    ]
+
+
 MOE_MAX_PARTS = 8
 
 
@@ -126,6 +138,7 @@ def _open(path: str):
     lib.moe_sort_grad.argtypes = [pdesc] + [vp] * 5
     lib.moe_unsort.argtypes = [pdesc] + [vp] * 6
     lib.moe_unsort_grad.argtypes = [pdesc] + [vp] * 8
+    lib.moe_lora_linear.argtypes = [ctypes.POINTER(MoeLoraDesc)] + [vp] * 10
     lib.moe_get_error.argtypes = [vp, vp]
     lib.moe_layout_dispatch_kernels.argtypes = [pdesc]
     lib.moe_layout_dispatch_kernels.restype = ctypes.c_int32
@@ -136,7 +149,7 @@ def _open(path: str):
                  "moe_expert_gate_up", "moe_expert_down", "moe_expert_mlp_noalloc", "moe_expert_gate_up_fp8",
                  "moe_expert_down_fp8", "moe_expert_mlp_noalloc_fp8", "moe_layout_dispatch_parts",
                  "moe_combine_parts", "moe_expert_stub_parts", "moe_reset_parts", "moe_gate", "moe_gate_grad",
-                 "moe_sort", "moe_sort_grad", "moe_unsort", "moe_unsort_grad", "moe_get_error"):
+                 "moe_sort", "moe_sort_grad", "moe_unsort", "moe_unsort_grad", "moe_lora_linear", "moe_get_error"):
         getattr(lib, name).restype = st
     return lib
 
@@ -326,6 +339,11 @@ def moe_unsort_grad(desc, packed_y, tok_packed, topk_weights, grad_out, grad_pac
     _check(load().moe_unsort_grad(ctypes.byref(desc), _ptr(packed_y), _ptr(tok_packed), _ptr(topk_weights),
                                   _ptr(grad_out), _ptr(grad_packed_y), _ptr(grad_weights), _ptr(err),
                                   _stream(stream)), "moe_unsort_grad")
+
+
+def moe_lora_linear(desc: MoeLoraDesc, x, w, lora_a, lora_b, scales, adapter, u, y, err, stream=None):
+    _check(load().moe_lora_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b), _ptr(scales),
+                                  _ptr(adapter), _ptr(u), _ptr(y), _ptr(err), _stream(stream)), "moe_lora_linear")
 
 
 def moe_get_error(err, stream=None) -> int:

@@ -1,0 +1,827 @@
+// A projection shared by all requests of a batch with each request's low-rank
+// adapter beside it:
+//
+//   y[t] = bf16( x[t] W^T + s_a (x[t] A_a^T) B_a^T ),  a = adapter[t], or no second term for a = -1
+//
+// x [T][in], W [out][in], A_a [rank][in], B_a [out][rank], all bf16, K-major.
+// The adapters are extra K blocks of the projection's own accumulation, in fp32
+// on the tensor cores: with u[t] = s_a x[t] A_a^T rounded to bf16, the tile's
+// product goes on with u and B_a for every adapter a among its tokens, each time
+// writing only the accumulator rows of the tokens that use it (the MMA's
+// disable-output-lane mask, so no adapter's value, not even a NaN, reaches
+// another request's row). y is rounded once. Rounding u to bf16, which is what
+// the tensor cores take, costs 2^-9 of the adapter's term: at most what rounding
+// y costs where that term is all of it.
+//
+// Two kernels:
+//   lora_shrink_kernel  u[t] = s_a x[t] A_a^T. A tile is 128 tokens against the
+//     stacked rows of up to 128 / rank adapters that occur among them (one
+//     adapter's 256 rows at most): a token's own columns are picked in the
+//     epilogue. in is split over a cluster of CTAs whose partial sums meet in
+//     distributed shared memory in a fixed order.
+//   lora_gemm_kernel    the projection with its extra K blocks. Tiles of 128
+//     tokens x BN outputs; TMA brings x and W (then u and B_a) tiles, one lane
+//     issues tcgen05.mma, four warps find the tile's adapters and their rows.
+//     With few tiles in is split over a cluster as above; with many a CTA walks
+//     its tiles with two accumulators, so that a tile's stores overlap the next
+//     one's products. It starts on x and W while the shrink kernel is running;
+//     only the loads of u wait for that.
+//
+// Shared memory and tensor memory: a CTA that takes c of the 512 tensor-memory
+// columns of an SM takes at least c / 512 of its shared memory, so that CTAs
+// that share an SM never wait for one another's columns (a cluster whose CTAs
+// did could wait for ever). Every other wait is bounded, as in the expert stage.
+#include <cuda_bf16.h>
+
+#include "moe_tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kLBM = 128;           // tokens of a tile
+constexpr int kLBK = 64;            // K elements of a stage: one 128-byte swizzle row
+constexpr int kLRow = kLBK * 2;     // bytes of a tile row
+constexpr int kLMaxStages = 8;
+constexpr int kLMaxRank = 256;
+constexpr int kLSmemMax = 227 * 1024;
+constexpr int kLStatic = 8192;      // room for a kernel's static shared memory
+constexpr int kLBytesPerCol = 228 * 1024 / 512;  // shared memory that goes with one tensor-memory column
+constexpr int kShrinkThreads = 192;
+constexpr int kGemmLThreads = 320;
+constexpr int kShrinkCols = 128;    // adapter rows of a shrink tile (or one adapter's, if it has more)
+constexpr int kLMaxCluster = 8;
+
+struct LoraArgs {
+  const int32_t *adapter;
+  const float *scales;
+  __nv_bfloat16 *u;  // [T][rank]
+  __nv_bfloat16 *y;  // [T][out]
+  int32_t *err;
+  int T, K, N, rank, adapters;
+  int xrows;           // rows of an x box (a multiple of 8, at most 128)
+  int xbytes;          // bytes of an x tile in a stage (a multiple of 1024)
+  int stage, stages;   // bytes and number of the ring's stages
+  int kblocks;
+  // shrink
+  int per_pass, passes;  // adapters of a tile, and the most tiles that the adapters of 128 tokens need
+  uint32_t cols;         // tensor-memory columns
+  // projection
+  int lora, ntiles_n, mtiles, group_n;
+};
+
+__device__ __forceinline__ uint32_t lora_cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t lora_cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void lora_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 peer_load(uint32_t saddr, uint32_t rank) {
+  uint32_t p;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(p)
+               : "memory");
+  return v;
+}
+
+template <int ID>
+__device__ __forceinline__ void bar128() {
+  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+}
+
+// bar128 that also tells every thread whether v was set in all of them.
+template <int ID>
+__device__ __forceinline__ bool bar128_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(ID)
+      : "memory");
+  return r != 0;
+}
+
+// 8 consecutive fp32 accumulator columns of this thread's row.
+__device__ __forceinline__ void tmem_load8_wait(uint32_t taddr, float (&f)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+// mma_bf16 accumulating into the rows (tensor-memory lanes) whose bit is clear in `off` only.
+__device__ __forceinline__ void mma_bf16_rows(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              const uint4 &off) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 round8(const float (&f)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+    u[q] = *reinterpret_cast<const uint32_t *>(&p);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// One warp's wait: lane 0 polls, every lane learns the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *err, int lane) {
+  int ok = 0;
+  if (lane == 0) ok = role_wait(bar, parity, abort, err) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// Scratch of tile_adapters.
+struct AdapterScratch {
+  int32_t ids[kLBM];
+  int32_t pos[kLBM];
+  int32_t counts[4];
+};
+
+// The distinct adapters of a tile's tokens, in order of first use, by 128
+// threads (thread m: token t0 + m). Returns their number and this token's place
+// in the list (-1: no adapter). An id outside [-1, adapters) counts as none and
+// sets *bad.
+template <int BAR>
+__device__ __forceinline__ int tile_adapters(const LoraArgs &a, int t0, int m, AdapterScratch &s, int32_t *list, int *slot,
+                                             bool *bad) {
+  const int lane = m & 31, warp = m >> 5;
+  int id = -1;
+  if (t0 + m < a.T) {
+    id = __ldg(a.adapter + t0 + m);
+    if (id < -1 || id >= a.adapters) {
+      *bad = true;
+      id = -1;
+    }
+  }
+  s.ids[m] = id;
+  bar128<BAR>();
+  int first = m;
+  for (int j = (m & ~3); j >= 0; j -= 4) {
+    const int4 v = *reinterpret_cast<const int4 *>(s.ids + j);
+    if (v.w == id && j + 3 < first) first = j + 3;
+    if (v.z == id && j + 2 < first) first = j + 2;
+    if (v.y == id && j + 1 < first) first = j + 1;
+    if (v.x == id && j < first) first = j;
+  }
+  const bool is_first = id >= 0 && first == m;
+  const unsigned firsts = __ballot_sync(0xffffffffu, is_first);
+  if (lane == 0) s.counts[warp] = __popc(firsts);
+  bar128<BAR>();
+  int before = 0, n = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < warp) before += s.counts[w];
+    n += s.counts[w];
+  }
+  if (is_first) {
+    const int p = before + __popc(firsts & ((1u << lane) - 1u));
+    s.pos[m] = p;
+    list[p] = id;
+  }
+  bar128<BAR>();
+  *slot = id >= 0 ? s.pos[first] : -1;
+  return n;
+}
+
+// ---------------------------------------------------------------------------
+// u[t] = s_a x[t] A_a^T
+// ---------------------------------------------------------------------------
+struct ShrinkShared {
+  AdapterScratch scratch;
+  int32_t list[kLBM];
+  uint64_t full[kLMaxStages], empty[kLMaxStages], tfull, done;
+  uint32_t tmem;
+  int abort, n;
+};
+
+__global__ void __launch_bounds__(kShrinkThreads)
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
+                       const LoraArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) ShrinkShared sh;
+  uint8_t *smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
+  volatile int *abort = &sh.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int splits = static_cast<int>(lora_cluster_size()), split = static_cast<int>(lora_cluster_rank());
+  const int item = static_cast<int>(blockIdx.x) / splits;
+  const int mt = item / a.passes, pass = item - mt * a.passes;
+  const int t0 = mt * kLBM;
+
+  if (tid == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(sh.full + s, 1);
+      mbar_init(sh.empty + s, 1);
+    }
+    mbar_init(&sh.tfull, 1);
+    mbar_init(&sh.done, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&map_x);
+    prefetch_tensormap(&map_a);
+  }
+  grid_dependency_wait();
+  int slot = -1;
+  if (warp >= 2) {
+    bool bad = false;
+    const int n = tile_adapters<1>(a, t0, tid - 64, sh.scratch, sh.list, &slot, &bad);
+    if (bad && pass == 0 && split == 0) latch_error(a.err, MOE_EINVAL);
+    if (tid == 64) sh.n = n;
+  }
+  __syncthreads();
+  const int first = pass * a.per_pass;
+  const int nact = min(sh.n - first, a.per_pass);  // adapters of this tile
+  if (nact <= 0) {  // the same in every CTA of the cluster
+    grid_dependents_launch();
+    return;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&sh.tmem), a.cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // only now may the projection's CTAs arrive: this CTA has its tensor memory
+  grid_dependents_launch();
+  const uint32_t tmem = sh.tmem;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
+  float *red = reinterpret_cast<float *>(smem);  // [128][rank]: this split's sums, once the ring is idle
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
+        if (!role_wait(sh.empty + s, ph ^ 1u, abort, a.err)) break;
+        const uint32_t sx = smem_addr(smem + s * a.stage), sa = sx + a.xbytes, fb = smem_addr(sh.full + s);
+        mbar_arrive_expect_tx(sh.full + s, bytes);
+        tma_load_2d(sx, &map_x, kb * kLBK, t0, fb);
+        for (int i = 0; i < nact; ++i)
+          tma_load_2d(sa + i * a.rank * kLRow, &map_a, kb * kLBK, sh.list[first + i] * a.rank, fb);
+      }
+      for (uint32_t s = 0; s < static_cast<uint32_t>(a.stages) && s < it; ++s) {
+        const uint32_t last = s + ((it - 1 - s) / a.stages) * a.stages;
+        mbar_wait_bounded(sh.full + s, (last / a.stages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
+        if (!role_wait(sh.full + s, ph, abort, a.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sx = smem_addr(smem + s * a.stage), sa = sx + a.xbytes;
+#pragma unroll
+        for (int kk = 0; kk < kLBK / 16; ++kk)
+          mma_bf16(tmem, sw128_desc(sx + kk * 32), sw128_desc(sa + kk * 32), idesc, (it | kk) != 0);
+        mma_commit(smem_addr(sh.empty + s));
+      }
+      if (ok) mma_commit(smem_addr(&sh.tfull));
+      mma_commit(smem_addr(&sh.done));
+      mbar_wait_bounded(&sh.done, 0);
+    }
+    __syncwarp();
+  } else {
+    // this token's own columns of the tile
+    const int q = warp & 3, m = q * 32 + lane;
+    if (warp_wait(&sh.tfull, 0, abort, a.err, lane)) {
+      tc_fence_after();
+      // thread tid - 64 found the slot of token tid - 64; accumulator row m is token m
+      const int own = __ldg(a.adapter + min(t0 + m, a.T - 1));
+      int mine = -1;
+      if (t0 + m < a.T)
+        for (int i = 0; i < nact; ++i)
+          if (sh.list[first + i] == own) mine = i;
+      for (int i = 0; i < nact; ++i) {
+        if (!__any_sync(0xffffffffu, mine == i)) continue;
+        for (int c = 0; c < a.rank; c += 8) {
+          float f[8];
+          tmem_load8_wait(tmem + (static_cast<uint32_t>(q * 32) << 16) + i * a.rank + c, f);
+          if (mine == i) {
+            float4 *d = reinterpret_cast<float4 *>(red + m * a.rank + c);
+            d[0] = make_float4(f[0], f[1], f[2], f[3]);
+            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+  }
+  lora_cluster_sync();
+  // the splits' sums in their order, each CTA a share of the rows
+  const int rows = min(kLBM, a.T - t0), vecs = a.rank / 8;
+  for (int i = split * kShrinkThreads + tid; i < rows * vecs; i += splits * kShrinkThreads) {
+    const int m = i / vecs, c = (i - m * vecs) * 8;
+    const int id = __ldg(a.adapter + t0 + m);
+    bool mine = false;
+    for (int p = 0; p < nact; ++p) mine |= sh.list[first + p] == id;
+    if (!mine) continue;
+    const float sc = a.scales != nullptr ? __ldg(a.scales + id) : 1.0f;
+    const uint32_t at = smem_addr(red + m * a.rank + c);
+    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int p = 0; p < splits; ++p) {
+      const float4 lo = peer_load(at, p), hi = peer_load(at + 16, p);
+      f[0] += lo.x;
+      f[1] += lo.y;
+      f[2] += lo.z;
+      f[3] += lo.w;
+      f[4] += hi.x;
+      f[5] += hi.y;
+      f[6] += hi.z;
+      f[7] += hi.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= sc;
+    *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(t0 + m) * a.rank + c) = round8(f);
+  }
+  lora_cluster_sync();  // no CTA leaves while another may still read its sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, a.cols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The projection with the adapters as extra K blocks.
+// ---------------------------------------------------------------------------
+struct GemmShared {
+  AdapterScratch scratch;
+  int32_t list[2][kLBM];        // the adapters of a tile's tokens
+  uint4 off[2][kLBM];           // for each of them, the rows that do not use it
+  uint64_t full[kLMaxStages], empty[kLMaxStages];
+  uint64_t tfull[2], tempty[2], lfull[2], lempty[2], done;
+  int count[2];
+  uint32_t tmem;
+  int abort;
+};
+
+static_assert(sizeof(GemmShared) <= kLStatic && sizeof(ShrinkShared) <= kLStatic, "");
+
+struct LTile {
+  int t0, n0;
+};
+
+// Tile w: groups of group_n n-tiles, each group swept over the m-tiles with its
+// n-tiles innermost, so that the CTAs running at one time share both the
+// group's weight tiles and each m-tile's rows in L2.
+template <int BN>
+__device__ __forceinline__ LTile ltile_of(int w, const LoraArgs &a) {
+  const int per_group = a.mtiles * a.group_n;
+  const int g = w / per_group, r = w - g * per_group;
+  const int gw = min(a.group_n, a.ntiles_n - g * a.group_n);
+  const int mt = r / gw;
+  return LTile{mt * kLBM, (g * a.group_n + r - mt * gw) * BN};
+}
+
+template <int BN, bool SPLIT>
+__global__ void __launch_bounds__(kGemmLThreads, 1)
+    lora_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                     const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_b,
+                     const LoraArgs a) {
+  constexpr int kAcc = SPLIT ? 1 : 2;               // accumulators
+  constexpr uint32_t kCols = kAcc * BN;
+  constexpr uint32_t kWBytes = BN * kLRow;
+  constexpr int kRedPitch = BN + 4;                 // floats of a row of partial sums
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) GemmShared sh;
+  uint8_t *smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
+  volatile int *abort = &sh.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int splits = SPLIT ? static_cast<int>(lora_cluster_size()) : 1;
+  const int split = SPLIT ? static_cast<int>(lora_cluster_rank()) : 0;
+  const int first = SPLIT ? static_cast<int>(blockIdx.x) / splits : static_cast<int>(blockIdx.x);
+  const int stride = SPLIT ? static_cast<int>(gridDim.x) / splits : static_cast<int>(gridDim.x);
+  const int total = a.mtiles * a.ntiles_n;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
+  const int rblocks = (a.rank + kLBK - 1) / kLBK;   // K blocks of one adapter
+
+  if (tid == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(sh.full + s, 1);
+      mbar_init(sh.empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(sh.tfull + b, 1);
+      mbar_init(sh.tempty + b, 4);
+      mbar_init(sh.lfull + b, 1);
+      mbar_init(sh.lempty + b, 2);
+    }
+    mbar_init(&sh.done, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid == 32) {
+    prefetch_tensormap(&map_x);
+    prefetch_tensormap(&map_w);
+    prefetch_tensormap(&map_u);
+    prefetch_tensormap(&map_b);
+  }
+  // With adapters the shrink kernel comes before this one: it let this grid
+  // start only after its own dependency wait, so x is there, and only the
+  // producer waits for it, before its first load of u.
+  if (!a.lora) grid_dependency_wait();
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&sh.tmem), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- TMA producer ----
+      uint32_t it = 0;
+      int lt = 0;
+      bool ok = true;
+      for (int w = first; ok && w < total; w += stride, ++lt) {
+        const LTile t = ltile_of<BN>(w, a);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
+          if (!role_wait(sh.empty + s, ph ^ 1u, abort, a.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes, fb = smem_addr(sh.full + s);
+          mbar_arrive_expect_tx(sh.full + s, static_cast<uint32_t>(a.xrows) * kLRow + kWBytes);
+          tma_load_2d(sw, &map_w, kb * kLBK, t.n0, fb);
+          if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_w, kb * kLBK, t.n0 + kBoxRows, fb);
+          tma_load_2d(sx, &map_x, kb * kLBK, t.t0, fb);
+        }
+        if (!ok || !a.lora) continue;
+        const int b = lt & 1;
+        if (!role_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err)) break;
+        const int blocks = sh.count[b] * rblocks;
+        for (int j = split; j < blocks; j += splits, ++it) {
+          const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
+          if (!role_wait(sh.empty + s, ph ^ 1u, abort, a.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes, fb = smem_addr(sh.full + s);
+          const int row = sh.list[b][j / rblocks] * a.N + t.n0, k = (j % rblocks) * kLBK;
+          mbar_arrive_expect_tx(sh.full + s, static_cast<uint32_t>(a.xrows) * kLRow + kWBytes);
+          tma_load_2d(sw, &map_b, k, row, fb);
+          if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_b, k, row + kBoxRows, fb);
+          grid_dependency_wait();  // u is written (returns at once after the first time)
+          tma_load_2d(sx, &map_u, k, t.t0, fb);
+        }
+        mbar_arrive(smem_addr(sh.lempty + b));
+      }
+      // the last load issued into each stage lands before the CTA may exit
+      for (uint32_t s = 0; s < static_cast<uint32_t>(a.stages) && s < it; ++s) {
+        const uint32_t last = s + ((it - 1 - s) / a.stages) * a.stages;
+        mbar_wait_bounded(sh.full + s, (last / a.stages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- MMA issuer ----
+      uint32_t it = 0;
+      int lt = 0;
+      const uint32_t idesc = idesc_bf16(kLBM, BN);
+      bool ok = true;
+      for (int w = first; ok && w < total; w += stride, ++lt) {
+        const int buf = lt % kAcc;
+        if (!role_wait(sh.tempty + buf, ((lt / kAcc) & 1) ^ 1u, abort, a.err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * BN;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t s = it % a.stages;
+          if (!role_wait(sh.full + s, (it / a.stages) & 1u, abort, a.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes;
+#pragma unroll
+          for (int kk = 0; kk < kLBK / 16; ++kk)
+            mma_bf16(d, sw128_desc(sx + kk * 32), sw128_desc(sw + kk * 32), idesc, ((kb - kb0) | kk) != 0);
+          mma_commit(smem_addr(sh.empty + s));
+        }
+        if (!ok) break;
+        if (a.lora) {
+          const int b = lt & 1;
+          if (!role_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err)) break;
+          const int blocks = sh.count[b] * rblocks;
+          for (int j = split; j < blocks; j += splits, ++it) {
+            const uint32_t s = it % a.stages;
+            if (!role_wait(sh.full + s, (it / a.stages) & 1u, abort, a.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes;
+            const uint4 off = sh.off[b][j / rblocks];
+            // columns past the rank are zeros in both tiles, so a step's last ones add nothing
+            const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
+            for (int kk = 0; kk * 16 < cols; ++kk)
+              mma_bf16_rows(d, sw128_desc(sx + kk * 32), sw128_desc(sw + kk * 32), idesc, off);
+            mma_commit(smem_addr(sh.empty + s));
+          }
+          mbar_arrive(smem_addr(sh.lempty + b));
+        }
+        if (ok) mma_commit(smem_addr(sh.tfull + buf));
+      }
+      // every MMA issued completes before the tensor memory is freed
+      mma_commit(smem_addr(&sh.done));
+      mbar_wait_bounded(&sh.done, 0);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // ---- epilogue: warp w reads TMEM lanes 32 * (w % 4) .. + 31 ----
+    const int q = warp & 3, m = q * 32 + lane;
+    int lt = 0;
+    for (int w = first; w < total; w += stride, ++lt) {
+      const int buf = lt % kAcc;
+      if (!warp_wait(sh.tfull + buf, (lt / kAcc) & 1u, abort, a.err, lane)) break;
+      tc_fence_after();
+      const LTile t = ltile_of<BN>(w, a);
+      const bool valid = t.t0 + m < a.T;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
+      if constexpr (SPLIT) {
+        float *red = reinterpret_cast<float *>(smem) + m * kRedPitch;
+        if (__any_sync(0xffffffffu, valid)) {
+          for (int c = 0; c < BN; c += 8) {
+            float f[8];
+            tmem_load8_wait(tb + c, f);
+            if (valid) {
+              *reinterpret_cast<float4 *>(red + c) = make_float4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<float4 *>(red + c + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
+      } else {
+        __nv_bfloat16 *row = a.y + static_cast<int64_t>(valid ? t.t0 + m : 0) * a.N + t.n0;
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t r[32];
+          tmem_load32_wait(tb + c, r);
+          if (!valid) continue;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (t.n0 + c + v * 8 < a.N) {
+              float f[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[v * 8 + j]);
+              *reinterpret_cast<uint4 *>(row + c + v * 8) = round8(f);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(sh.tempty + buf));
+    }
+  } else if (a.lora) {
+    // ---- the tile's adapters and the rows that do not use each of them ----
+    const int m = tid - 192;
+    int lt = 0;
+    for (int w = first; w < total; w += stride, ++lt) {
+      const int b = lt & 1;
+      const LTile t = ltile_of<BN>(w, a);
+      // the four warps go on or give up together: the barriers below take all of them
+      if (!bar128_and<2>(warp_wait(sh.lempty + b, ((lt >> 1) & 1) ^ 1u, abort, a.err, lane))) break;
+      int slot = -1;
+      bool bad = false;  // reported by the shrink kernel
+      sh.off[b][m] = make_uint4(~0u, ~0u, ~0u, ~0u);
+      const int n = tile_adapters<2>(a, t.t0, m, sh.scratch, sh.list[b], &slot, &bad);
+      if (slot >= 0) atomicAnd(reinterpret_cast<uint32_t *>(&sh.off[b][slot]) + (m >> 5), ~(1u << (m & 31)));
+      if (m == 0) sh.count[b] = n;
+      bar128<2>();
+      if (m == 0) mbar_arrive(smem_addr(sh.lfull + b));
+    }
+  }
+  __syncwarp();
+  if constexpr (SPLIT) {
+    lora_cluster_sync();
+    if (first < total) {
+      // the splits' sums in their order, each CTA a share of the rows
+      const LTile t = ltile_of<BN>(first, a);
+      const int rows = min(kLBM, a.T - t.t0);
+      constexpr int vecs = BN / 8;
+      for (int i = split * kGemmLThreads + tid; i < rows * vecs; i += splits * kGemmLThreads) {
+        const int m = i / vecs, c = (i - m * vecs) * 8;
+        if (t.n0 + c >= a.N) continue;
+        const uint32_t at = smem_addr(reinterpret_cast<float *>(smem) + m * kRedPitch + c);
+        float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int p = 0; p < splits; ++p) {
+          const float4 lo = peer_load(at, p), hi = peer_load(at + 16, p);
+          f[0] += lo.x;
+          f[1] += lo.y;
+          f[2] += lo.z;
+          f[3] += lo.w;
+          f[4] += hi.x;
+          f[5] += hi.y;
+          f[6] += hi.z;
+          f[7] += hi.w;
+        }
+        *reinterpret_cast<uint4 *>(a.y + static_cast<int64_t>(t.t0 + m) * a.N + t.n0 + c) = round8(f);
+      }
+    }
+    lora_cluster_sync();  // no CTA leaves while another may still read its sums
+  }
+  // this grid ends after the shrink kernel also where no tile had an adapter:
+  // what comes next in the stream waits for this grid only
+  grid_dependency_wait();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+// 2-D map of a row-major [rows][K] bf16 matrix, boxes of box_rows x 64 elements, 128-byte swizzle.
+bool make_box_map(CUtensorMap *map, const void *base, int64_t K, int64_t rows, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(kLBK), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch with a cluster of `cluster` CTAs and programmatic dependent launch.
+template <class... P, class... Q>
+moe_status launch_cluster(void (*fn)(P...), int grid, int threads, int cluster, int smem, cudaStream_t stream,
+                          Q &&...args) {
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = MOE_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, fn, args...) != cudaSuccess) return MOE_ECUDA;
+  return launch_status();
+}
+
+// A launch's dynamic shared memory: what it uses, and at least its columns'
+// share. (All 512 columns: the most a CTA can have, which leaves no room for
+// another one's share.)
+int with_columns(int smem, int cols) {
+  int share = cols * kLBytesPerCol;
+  if (share > kLSmemMax - kLStatic) share = kLSmemMax - kLStatic;
+  return smem > share ? smem : share;
+}
+
+moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
+  const int most = a.adapters < a.T ? (a.adapters < kLBM ? a.adapters : kLBM) : (a.T < kLBM ? a.T : kLBM);
+  a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
+  if (a.per_pass > most) a.per_pass = most;
+  a.passes = (most + a.per_pass - 1) / a.per_pass;
+  int n = (a.per_pass * a.rank + 15) & ~15;
+  a.cols = 32;
+  while (static_cast<int>(a.cols) < n) a.cols <<= 1;
+  // the adapters' rows end on whole 1024-byte swizzle groups, and the MMA's last
+  // 16-row step may read one group past them
+  a.stage = a.xbytes + n * kLRow;
+  a.stages = 4;
+  int splits = kLMaxCluster;
+  while (splits > 1 && (a.mtiles * splits > sms || splits > a.kblocks)) splits >>= 1;
+  // the accumulator's 128 rows are read from the x tile's place also where the
+  // tile has fewer rows: what follows it inside the allocation is read then
+  int smem = 1024 + a.stages * a.stage + kLBM * kLRow;
+  const int red = 1024 + kLBM * a.rank * 4;
+  if (smem < red) smem = red;
+  smem = with_columns(smem, static_cast<int>(a.cols));
+  CUtensorMap mx, ma;
+  if (!make_box_map(&mx, x, a.K, a.T, a.xrows) ||
+      !make_box_map(&ma, lora_a, a.K, static_cast<int64_t>(a.adapters) * a.rank, a.rank))
+    return MOE_ECUDA;
+  const int64_t grid = static_cast<int64_t>(a.mtiles) * a.passes * splits;
+  if (grid > 0x7fffffffll) return MOE_EINVAL;
+  return launch_cluster(lora_shrink_kernel, static_cast<int>(grid), kShrinkThreads, splits, smem, stream, mx, ma, a);
+}
+
+template <int BN, bool SPLIT>
+moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lora_b, int splits, int sms,
+                       cudaStream_t stream) {
+  a.ntiles_n = (a.N + BN - 1) / BN;
+  a.stage = a.xbytes + BN * kLRow;
+  a.stages = 4;
+  const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
+  if (tiles > 0x7fffffffll / kLMaxCluster) return MOE_EINVAL;
+  const int64_t grid = SPLIT ? tiles * splits : (tiles < sms ? tiles : sms);
+  a.group_n = a.ntiles_n < 8 ? a.ntiles_n : 8;
+  const int smem = with_columns(1024 + a.stages * a.stage, (SPLIT ? 1 : 2) * BN);
+  if (smem > kLSmemMax - kLStatic) return MOE_EINVAL;
+  CUtensorMap mx, mw, mu, mb;
+  if (!make_box_map(&mx, x, a.K, a.T, a.xrows) || !make_box_map(&mw, w, a.K, a.N, kBoxRows)) return MOE_ECUDA;
+  mu = mx;
+  mb = mw;  // not used without adapters
+  if (a.lora && (!make_box_map(&mu, a.u, a.rank, a.T, a.xrows) ||
+                 !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBoxRows)))
+    return MOE_ECUDA;
+  return launch_cluster(lora_gemm_kernel<BN, SPLIT>, static_cast<int>(grid), kGemmLThreads, SPLIT ? splits : 1, smem,
+                        stream, mx, mw, mu, mb, a);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, const void *w, const void *lora_a,
+                                      const void *lora_b, const float *scales, const int32_t *adapter, void *u, void *y,
+                                      int32_t *err, void *stream) {
+  if (desc == nullptr) return MOE_EINVAL;
+  const int T = desc->num_tokens, K = desc->in_dim, N = desc->out_dim, r = desc->rank, A = desc->num_adapters;
+  if (T < 0 || K < 8 || N < 8 || A < 0 || K % 8 != 0 || N % 8 != 0 || desc->num_sms < 0) return MOE_EINVAL;
+  if (A > 0 && (r < 8 || r > kLMaxRank || r % 8 != 0)) return MOE_EINVAL;
+  // weight rows are 32-bit TMA coordinates, a tile's last ones may lie up to 256 past the end
+  if (static_cast<int64_t>(A) * N > INT32_MAX - 256 || static_cast<int64_t>(A) * r > INT32_MAX - 256 ||
+      T > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256)
+    return MOE_EINVAL;
+  if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (x == nullptr || w == nullptr || y == nullptr || !aligned16(x) || !aligned16(w) || !aligned16(y))
+    return MOE_EINVAL;
+  if (A > 0 && (lora_a == nullptr || lora_b == nullptr || adapter == nullptr || u == nullptr || !aligned16(lora_a) ||
+                !aligned16(lora_b) || !aligned4(scales) || !aligned4(adapter) || !aligned16(u)))
+    return MOE_EINVAL;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int sms = desc->num_sms > 0 ? desc->num_sms : sm_count();
+  LoraArgs a{};
+  a.adapter = adapter;
+  a.scales = scales;
+  a.u = static_cast<__nv_bfloat16 *>(u);
+  a.y = static_cast<__nv_bfloat16 *>(y);
+  a.err = err;
+  a.T = T;
+  a.K = K;
+  a.N = N;
+  a.rank = A > 0 ? r : kLBK;
+  a.adapters = A;
+  a.lora = A > 0;
+  a.xrows = T >= kLBM ? kLBM : (T + 7) / 8 * 8;
+  a.xbytes = a.xrows * kLRow;
+  a.kblocks = (K + kLBK - 1) / kLBK;
+  a.mtiles = (T + kLBM - 1) / kLBM;
+  if (a.lora) {
+    const moe_status st = launch_shrink(a, x, lora_a, sms, cs);
+    if (st != MOE_OK) return st;
+  }
+  const int64_t tiles256 = static_cast<int64_t>(a.mtiles) * ((N + 255) / 256);
+  const int64_t tiles128 = static_cast<int64_t>(a.mtiles) * ((N + 127) / 128);
+  if (tiles256 >= sms) return launch_gemm<256, false>(a, x, w, lora_b, 1, sms, cs);
+  int splits = kLMaxCluster;
+  while (splits > 1 && (tiles128 * splits > sms || splits > a.kblocks)) splits >>= 1;
+  if (splits > 1) return launch_gemm<128, true>(a, x, w, lora_b, splits, sms, cs);
+  return launch_gemm<128, false>(a, x, w, lora_b, 1, sms, cs);
+}

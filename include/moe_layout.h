@@ -486,6 +486,44 @@ moe_status moe_unsort_grad(const moe_desc *desc, const uint16_t *packed_y, const
                            const float *topk_weights, const uint16_t *grad_out, uint16_t *grad_packed_y,
                            float *grad_weights, int32_t *err, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * A dense projection beside the experts (the shared expert's linears, an
+ * attention projection) that all requests of a batch share, with the low-rank
+ * adapter of each request added in the same accumulation.
+ * --------------------------------------------------------------------------- */
+typedef struct {
+  int32_t num_tokens;   /* T >= 0 */
+  int32_t in_dim;       /* a multiple of 8 */
+  int32_t out_dim;      /* a multiple of 8 */
+  int32_t rank;         /* a multiple of 8, at most 256 (ignored without adapters) */
+  int32_t num_adapters; /* A >= 0; 0: the projection alone */
+  int32_t num_sms;      /* SMs the projection's CTAs are spread over; 0 = all */
+} moe_lora_desc;
+
+/* For every token t with a = adapter[t]:
+ *   u[t] = bf16_rne( scales[a] * x[t] lora_a[a]^T ),
+ *   y[t] = bf16_rne( x[t] w^T + u[t] lora_b[a]^T ),
+ * products in bf16 accumulated in fp32 on the tensor cores; adapter -1 has no
+ * second term. Adapters of a smaller rank are padded with zero rows of lora_a or
+ * zero columns of lora_b. The adapters may be in any order over the tokens; a
+ * run of 128 tokens costs least with few of them.
+ *   x [T][in_dim], w [out_dim][in_dim], lora_a [A][rank][in_dim],
+ *   lora_b [A][out_dim][rank] bf16; scales [A] float or NULL (all 1);
+ *   adapter [T] int32 (read);
+ *   u [T][rank] bf16 (written: rows of tokens with an adapter; a scratch buffer
+ *   the caller may reuse after the call in stream order); y [T][out_dim] bf16
+ *   (written). All matrices 16-byte aligned. With A = 0 lora_a, lora_b, scales,
+ *   adapter and u may be NULL.
+ * Reads nothing before the dependency wait of its first kernel, so every input
+ * may come from the kernel enqueued immediately before the call.
+ * Host errors: MOE_EINVAL (sizes, pointers, A * out_dim or A * rank above 2^31 - 1);
+ * MOE_ECUDA when no TMA tensor map can be made. Device errors: an adapter id
+ * outside [-1, A) -> MOE_EINVAL (taken as -1); a stalled pipeline ->
+ * MOE_ETIMEOUT. */
+moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, const void *w, const void *lora_a,
+                           const void *lora_b, const float *scales, const int32_t *adapter, void *u, void *y,
+                           int32_t *err, void *stream);
+
 /* Synchronise `stream`, read the device error word, clear it, and return its
  * value (MOE_OK if no kernel latched an error). Host-synchronising. */
 moe_status moe_get_error(int32_t *err, void *stream);

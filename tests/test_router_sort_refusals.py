@@ -101,3 +101,30 @@ def test_the_binding_refuses_host_and_strided_tensors():
     host = torch.zeros((4, 8))
     with pytest.raises(ValueError):
         B.moe_gate(d, o, host, None, host, host, host)
+
+
+def lora_desc(T=4, K=64, N=64, r=16, A=2, sms=0):
+    return B.MoeLoraDesc(T, K, N, r, A, sms)
+
+
+LORA = [P] * 9  # x, w, lora_a, lora_b, scales, adapter, u, y, err
+
+
+@pytest.mark.parametrize("d", [lora_desc(T=-1), lora_desc(K=60), lora_desc(K=0), lora_desc(N=12), lora_desc(N=0),
+                               lora_desc(r=12), lora_desc(r=0), lora_desc(r=264), lora_desc(A=-1), lora_desc(sms=-1),
+                               lora_desc(A=1 << 26, N=64)])
+def test_lora_refuses_sizes(d):
+    assert call("moe_lora_linear", d, *LORA) == B.MOE_EINVAL
+
+
+@pytest.mark.parametrize("at,value", [(0, 0), (1, 0), (2, 0), (3, 0), (5, 0), (6, 0), (7, 0), (8, 0), (0, P + 8), (1, P + 2),
+                                      (2, P + 8), (3, P + 8), (4, P + 2), (5, P + 2), (6, P + 8), (7, P + 8),
+                                      (8, P + 2)])
+def test_lora_refuses_missing_or_unaligned_buffers(at, value):
+    args = list(LORA)
+    args[at] = value
+    assert call("moe_lora_linear", lora_desc(), *args) == B.MOE_EINVAL
+
+
+def test_lora_with_no_tokens_does_nothing():
+    assert call("moe_lora_linear", lora_desc(T=0), 0, 0, 0, 0, 0, 0, 0, 0, P) == B.MOE_OK
