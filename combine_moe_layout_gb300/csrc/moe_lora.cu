@@ -130,6 +130,33 @@ __device__ __forceinline__ void tmem_load8_wait(uint32_t taddr, float (&f)[8]) {
   for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+// The four K = 16 steps of one 64-wide K block, from the low words of the
+// tiles' shared-memory descriptors (kDescHi is the high word of every
+// descriptor of this layout; a step is 32 bytes, 2 in the descriptor's units).
+// One thread issues them at a few cycles an instruction, and a block's products
+// take 256 cycles (BN = 128): descriptors made anew for every step took longer
+// than that.
+constexpr uint32_t kDescHi = static_cast<uint32_t>(sw128_desc(0) >> 32);
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return static_cast<uint32_t>(sw128_desc(saddr)); }
+
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+
 // mma_bf16 accumulating into the rows (tensor-memory lanes) whose bit is clear in `off` only.
 __device__ __forceinline__ void mma_bf16_rows(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               const uint4 &off) {
@@ -156,6 +183,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   int ok = 0;
   if (lane == 0) ok = role_wait(bar, parity, abort, err) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// Position in the ring of stages: the stage and the parity of its use. Kept by
+// counting: the number of stages is a run-time value, and dividing by it in
+// every K block took longer than the block's products.
+struct Ring {
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == static_cast<uint32_t>(stages)) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// Waits (bounded) until the last load issued into each stage has landed; r is
+// the position after `it` loads.
+__device__ __forceinline__ void drain_ring(uint64_t *full, Ring r, uint32_t it, int stages) {
+  for (uint32_t i = 0; i < static_cast<uint32_t>(stages) && i < it; ++i) {
+    if (r.s == 0) {
+      r.s = stages;
+      r.ph ^= 1u;
+    }
+    --r.s;
+    mbar_wait_bounded(full + r.s, r.ph);
+  }
 }
 
 // Scratch of tile_adapters.
@@ -232,7 +285,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = static_cast<int>(lora_cluster_size()), split = static_cast<int>(lora_cluster_rank());
   const int item = static_cast<int>(blockIdx.x) / splits;
-  const int mt = item / a.passes, pass = item - mt * a.passes;
+  // the first adapters of every tile first: the CTAs of further ones mostly find nothing to do
+  const int pass = item / a.mtiles, mt = item - pass * a.mtiles;
   const int t0 = mt * kLBM;
 
   if (tid == 0) {
@@ -248,6 +302,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
     prefetch_tensormap(&map_a);
   }
   grid_dependency_wait();
+  // the projection's CTAs may come: they find what this kernel's predecessors wrote, and by the rule on shared
+  // memory they leave this CTA its tensor memory
+  grid_dependents_launch();
   int slot = -1;
   if (warp >= 2) {
     bool bad = false;
@@ -258,10 +315,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   __syncthreads();
   const int first = pass * a.per_pass;
   const int nact = min(sh.n - first, a.per_pass);  // adapters of this tile
-  if (nact <= 0) {  // the same in every CTA of the cluster
-    grid_dependents_launch();
-    return;
-  }
+  if (nact <= 0) return;  // the same in every CTA of the cluster
   if (warp == 1) {
     tmem_alloc(smem_addr(&sh.tmem), a.cols);
     tmem_relinquish();
@@ -269,8 +323,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // only now may the projection's CTAs arrive: this CTA has its tensor memory
-  grid_dependents_launch();
   const uint32_t tmem = sh.tmem;
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
@@ -279,39 +331,37 @@ __global__ void __launch_bounds__(kShrinkThreads)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
+      Ring r;
       const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
-        if (!role_wait(sh.empty + s, ph ^ 1u, abort, a.err)) break;
+      for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
+        const uint32_t s = r.s;
+        if (!role_wait(sh.empty + s, r.ph ^ 1u, abort, a.err)) break;
         const uint32_t sx = smem_addr(smem + s * a.stage), sa = sx + a.xbytes, fb = smem_addr(sh.full + s);
         mbar_arrive_expect_tx(sh.full + s, bytes);
         tma_load_2d(sx, &map_x, kb * kLBK, t0, fb);
         for (int i = 0; i < nact; ++i)
           tma_load_2d(sa + i * a.rank * kLRow, &map_a, kb * kLBK, sh.list[first + i] * a.rank, fb);
       }
-      for (uint32_t s = 0; s < static_cast<uint32_t>(a.stages) && s < it; ++s) {
-        const uint32_t last = s + ((it - 1 - s) / a.stages) * a.stages;
-        mbar_wait_bounded(sh.full + s, (last / a.stages) & 1u);
-      }
+      drain_ring(sh.full, r, it, a.stages);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t it = 0;
+      Ring r;
       const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
+      const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
+      const uint32_t empty = smem_addr(sh.empty);
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
-        if (!role_wait(sh.full + s, ph, abort, a.err)) {
+      for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
+        const uint32_t s = r.s;
+        if (!role_wait(sh.full + s, r.ph, abort, a.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sx = smem_addr(smem + s * a.stage), sa = sx + a.xbytes;
-#pragma unroll
-        for (int kk = 0; kk < kLBK / 16; ++kk)
-          mma_bf16(tmem, sw128_desc(sx + kk * 32), sw128_desc(sa + kk * 32), idesc, (it | kk) != 0);
-        mma_commit(smem_addr(sh.empty + s));
+        const uint32_t lo = xlo + s * step;
+        mma_block(tmem, lo, lo + xstep, idesc, kb != kb0);
+        mma_commit(empty + s * 8);
       }
       if (ok) mma_commit(smem_addr(&sh.tfull));
       mma_commit(smem_addr(&sh.done));
@@ -472,13 +522,14 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     if (lane == 0) {
       // ---- TMA producer ----
       uint32_t it = 0;
+      Ring r;
       int lt = 0;
       bool ok = true;
       for (int w = first; ok && w < total; w += stride, ++lt) {
         const LTile t = ltile_of<BN>(w, a);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
-          if (!role_wait(sh.empty + s, ph ^ 1u, abort, a.err)) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
+          const uint32_t s = r.s;
+          if (!role_wait(sh.empty + s, r.ph ^ 1u, abort, a.err)) {
             ok = false;
             break;
           }
@@ -492,9 +543,9 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         const int b = lt & 1;
         if (!role_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err)) break;
         const int blocks = sh.count[b] * rblocks;
-        for (int j = split; j < blocks; j += splits, ++it) {
-          const uint32_t s = it % a.stages, ph = (it / a.stages) & 1u;
-          if (!role_wait(sh.empty + s, ph ^ 1u, abort, a.err)) {
+        for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
+          const uint32_t s = r.s;
+          if (!role_wait(sh.empty + s, r.ph ^ 1u, abort, a.err)) {
             ok = false;
             break;
           }
@@ -509,45 +560,42 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         mbar_arrive(smem_addr(sh.lempty + b));
       }
       // the last load issued into each stage lands before the CTA may exit
-      for (uint32_t s = 0; s < static_cast<uint32_t>(a.stages) && s < it; ++s) {
-        const uint32_t last = s + ((it - 1 - s) / a.stages) * a.stages;
-        mbar_wait_bounded(sh.full + s, (last / a.stages) & 1u);
-      }
+      drain_ring(sh.full, r, it, a.stages);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       // ---- MMA issuer ----
-      uint32_t it = 0;
+      Ring r;
       int lt = 0;
       const uint32_t idesc = idesc_bf16(kLBM, BN);
+      const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
+      const uint32_t empty = smem_addr(sh.empty);
       bool ok = true;
       for (int w = first; ok && w < total; w += stride, ++lt) {
         const int buf = lt % kAcc;
         if (!role_wait(sh.tempty + buf, ((lt / kAcc) & 1) ^ 1u, abort, a.err)) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * BN;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const uint32_t s = it % a.stages;
-          if (!role_wait(sh.full + s, (it / a.stages) & 1u, abort, a.err)) {
+        for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
+          const uint32_t s = r.s;
+          if (!role_wait(sh.full + s, r.ph, abort, a.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes;
-#pragma unroll
-          for (int kk = 0; kk < kLBK / 16; ++kk)
-            mma_bf16(d, sw128_desc(sx + kk * 32), sw128_desc(sw + kk * 32), idesc, ((kb - kb0) | kk) != 0);
-          mma_commit(smem_addr(sh.empty + s));
+          const uint32_t lo = xlo + s * step;
+          mma_block(d, lo, lo + xstep, idesc, kb != kb0);
+          mma_commit(empty + s * 8);
         }
         if (!ok) break;
         if (a.lora) {
           const int b = lt & 1;
           if (!role_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err)) break;
           const int blocks = sh.count[b] * rblocks;
-          for (int j = split; j < blocks; j += splits, ++it) {
-            const uint32_t s = it % a.stages;
-            if (!role_wait(sh.full + s, (it / a.stages) & 1u, abort, a.err)) {
+          for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
+            const uint32_t s = r.s;
+            if (!role_wait(sh.full + s, r.ph, abort, a.err)) {
               ok = false;
               break;
             }
@@ -720,6 +768,17 @@ int with_columns(int smem, int cols) {
   return smem > share ? smem : share;
 }
 
+// Stages of a ring of at most `bytes` (and at least 4, or as many as there are K blocks).
+int ring_stages(int stage, int blocks, int bytes) {
+  int n = bytes / stage;
+  if (n > kLMaxStages) n = kLMaxStages;
+  if (n > blocks) n = blocks;
+  return n < 4 ? 4 : n;
+}
+
+constexpr int kShrinkRing = 96 * 1024;
+constexpr int kSplitRing = 96 * 1024;  // two CTAs, or one and a shrink CTA, share an SM
+
 moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   const int most = a.adapters < a.T ? (a.adapters < kLBM ? a.adapters : kLBM) : (a.T < kLBM ? a.T : kLBM);
   a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
@@ -731,9 +790,9 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
   // the adapters' rows end on whole 1024-byte swizzle groups, and the MMA's last
   // 16-row step may read one group past them
   a.stage = a.xbytes + n * kLRow;
-  a.stages = 4;
   int splits = kLMaxCluster;
   while (splits > 1 && (a.mtiles * splits > sms || splits > a.kblocks)) splits >>= 1;
+  a.stages = ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kShrinkRing);
   // the accumulator's 128 rows are read from the x tile's place also where the
   // tile has fewer rows: what follows it inside the allocation is read then
   int smem = 1024 + a.stages * a.stage + kLBM * kLRow;
@@ -754,7 +813,7 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
                        cudaStream_t stream) {
   a.ntiles_n = (a.N + BN - 1) / BN;
   a.stage = a.xbytes + BN * kLRow;
-  a.stages = 4;
+  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kSplitRing) : 4;
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
   if (tiles > 0x7fffffffll / kLMaxCluster) return MOE_EINVAL;
   const int64_t grid = SPLIT ? tiles * splits : (tiles < sms ? tiles : sms);
