@@ -133,11 +133,11 @@ __device__ __forceinline__ void tmem_load8_wait(uint32_t taddr, float (&f)[8]) {
 // The four K = 16 steps of one 64-wide K block, from the low words of the
 // tiles' shared-memory descriptors (kDescHi is the high word of every
 // descriptor of this layout; a step is 32 bytes, 2 in the descriptor's units).
-// One thread issues them at a few cycles an instruction, and a block's products
-// take 256 cycles (BN = 128): descriptors made anew for every step took longer
-// than that.
+// A block's products take 256 cycles (BN = 128); descriptors made anew for every
+// step took longer than that.
 constexpr uint32_t kDescHi = static_cast<uint32_t>(sw128_desc(0) >> 32);
 
+__device__ __forceinline__ uint64_t full_desc(uint32_t lo) { return (static_cast<uint64_t>(kDescHi) << 32) | lo; }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return static_cast<uint32_t>(sw128_desc(saddr)); }
 
 __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
@@ -178,11 +178,31 @@ __device__ __forceinline__ uint4 round8(const float (&f)[8]) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// One warp's wait: lane 0 polls, every lane learns the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *err, int lane) {
+// A whole warp's bounded wait on an mbarrier phase: every lane gets the same
+// answer, so the warp stays together. As role_wait otherwise.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   int ok = 0;
-  if (lane == 0) ok = role_wait(bar, parity, abort, err) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  if ((threadIdx.x & 31) == 0) ok = role_wait(bar, parity, abort, err) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  // the other lanes order their later accesses after the phase too
+  return ok != 0 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+}
+
+// One lane of a warp that is all here. The producer's and the MMA issuer's
+// loops are run by the whole warp with only this lane issuing: their operands
+// are then the same in every lane, and four MMAs with their commit take about
+// 160 cycles to issue instead of 245 from a loop that a single lane runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e)
+      :
+      : "memory");
+  return e != 0;
 }
 
 // Position in the ring of stages: the stage and the parity of its use. Kept by
@@ -323,46 +343,47 @@ __global__ void __launch_bounds__(kShrinkThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
   float *red = reinterpret_cast<float *>(smem);  // [128][rank]: this split's sums, once the ring is idle
 
+  const bool leader = elect_one();  // used by warps 0 and 1
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      Ring r;
-      const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
-      for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
-        const uint32_t s = r.s;
-        if (!role_wait(sh.empty + s, r.ph ^ 1u, abort, a.err)) break;
-        const uint32_t sx = smem_addr(smem + s * a.stage), sa = sx + a.xbytes, fb = smem_addr(sh.full + s);
-        mbar_arrive_expect_tx(sh.full + s, bytes);
+    uint32_t it = 0;
+    Ring r;
+    const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
+    for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
+      if (!warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err)) break;
+      if (leader) {
+        const uint32_t sx = smem_addr(smem) + r.s * a.stage, sa = sx + a.xbytes, fb = smem_addr(sh.full) + r.s * 8;
+        mbar_arrive_expect_tx(sh.full + r.s, bytes);
         tma_load_2d(sx, &map_x, kb * kLBK, t0, fb);
         for (int i = 0; i < nact; ++i)
           tma_load_2d(sa + i * a.rank * kLRow, &map_a, kb * kLBK, sh.list[first + i] * a.rank, fb);
       }
-      drain_ring(sh.full, r, it, a.stages);
+      __syncwarp();
     }
+    if (leader) drain_ring(sh.full, r, it, a.stages);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      Ring r;
-      const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
-      const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
-      const uint32_t empty = smem_addr(sh.empty);
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
-        const uint32_t s = r.s;
-        if (!role_wait(sh.full + s, r.ph, abort, a.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t lo = xlo + s * step;
+    Ring r;
+    const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
+    const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
+    const uint32_t empty = smem_addr(sh.empty);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
+      ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t lo = xlo + r.s * step;
         mma_block(tmem, lo, lo + xstep, idesc, kb != kb0);
-        mma_commit(empty + s * 8);
+        mma_commit(empty + r.s * 8);
       }
+      __syncwarp();
+    }
+    if (leader) {
       if (ok) mma_commit(smem_addr(&sh.tfull));
       mma_commit(smem_addr(&sh.done));
       mbar_wait_bounded(&sh.done, 0);
@@ -371,7 +392,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   } else {
     // this token's own columns of the tile
     const int q = warp & 3, m = q * 32 + lane;
-    if (warp_wait(&sh.tfull, 0, abort, a.err, lane)) {
+    if (warp_wait(&sh.tfull, 0, abort, a.err)) {
       tc_fence_after();
       // thread tid - 64 found the slot of token tid - 64; accumulator row m is token m
       const int own = __ldg(a.adapter + min(t0 + m, a.T - 1));
@@ -516,103 +537,136 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+  const bool leader = elect_one();  // used by warps 0 and 1
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- TMA producer ----
-      uint32_t it = 0;
-      Ring r;
-      int lt = 0;
-      bool ok = true;
-      for (int w = first; ok && w < total; w += stride, ++lt) {
-        const LTile t = ltile_of<BN>(w, a);
-        for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
-          const uint32_t s = r.s;
-          if (!role_wait(sh.empty + s, r.ph ^ 1u, abort, a.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes, fb = smem_addr(sh.full + s);
-          mbar_arrive_expect_tx(sh.full + s, static_cast<uint32_t>(a.xrows) * kLRow + kWBytes);
+    // ---- TMA producer ----
+    uint32_t it = 0;
+    Ring r;
+    int lt = 0;
+    bool ok = true, waited = false;
+    const uint32_t ring = smem_addr(smem), fulls = smem_addr(sh.full);
+    const uint32_t bytes = static_cast<uint32_t>(a.xrows) * kLRow + kWBytes;
+    // arms stage s for a block of the adapters and asks for its B_a tile
+    const auto load_b = [&](uint32_t s, int row, int k) {
+      const uint32_t sw = ring + s * a.stage + a.xbytes, fb = fulls + s * 8;
+      mbar_arrive_expect_tx(sh.full + s, bytes);
+      tma_load_2d(sw, &map_b, k, row, fb);
+      if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_b, k, row + kBoxRows, fb);
+    };
+    for (int w = first; ok && w < total; w += stride, ++lt) {
+      const LTile t = ltile_of<BN>(w, a);
+      for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
+        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+        if (!ok) break;
+        if (leader) {
+          const uint32_t sx = ring + r.s * a.stage, sw = sx + a.xbytes, fb = fulls + r.s * 8;
+          mbar_arrive_expect_tx(sh.full + r.s, bytes);
           tma_load_2d(sw, &map_w, kb * kLBK, t.n0, fb);
           if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_w, kb * kLBK, t.n0 + kBoxRows, fb);
           tma_load_2d(sx, &map_x, kb * kLBK, t.t0, fb);
         }
-        if (!ok || !a.lora) continue;
-        const int b = lt & 1;
-        if (!role_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err)) break;
-        const int blocks = sh.count[b] * rblocks;
-        for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
-          const uint32_t s = r.s;
-          if (!role_wait(sh.empty + s, r.ph ^ 1u, abort, a.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes, fb = smem_addr(sh.full + s);
-          const int row = sh.list[b][j / rblocks] * a.N + t.n0, k = (j % rblocks) * kLBK;
-          mbar_arrive_expect_tx(sh.full + s, static_cast<uint32_t>(a.xrows) * kLRow + kWBytes);
-          tma_load_2d(sw, &map_b, k, row, fb);
-          if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_b, k, row + kBoxRows, fb);
-          grid_dependency_wait();  // u is written (returns at once after the first time)
-          tma_load_2d(sx, &map_u, k, t.t0, fb);
-        }
-        mbar_arrive(smem_addr(sh.lempty + b));
+        __syncwarp();
       }
-      // the last load issued into each stage lands before the CTA may exit
-      drain_ring(sh.full, r, it, a.stages);
+      if (!ok || !a.lora) continue;
+      const int b = lt & 1;
+      ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
+      if (!ok) break;
+      const int blocks = sh.count[b] * rblocks;
+      const int mine = (blocks - split + splits - 1) / splits;  // blocks of this CTA: split, split + splits, ...
+      // The first B_a tiles are asked for before the wait for u, as far as the
+      // ring goes: no block of the adapters gives its stage back without u.
+      int early = waited ? 0 : min(mine, a.stages);
+      const Ring r0 = r;
+      for (int i = 0; i < early; ++i, ++it, r.next(a.stages)) {
+        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+        if (!ok) {
+          early = i;
+          break;
+        }
+        const int j = split + i * splits;
+        if (leader) load_b(r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK);
+        __syncwarp();
+      }
+      if (early > 0) {
+        grid_dependency_wait();  // u is written
+        waited = true;
+        Ring ru = r0;
+        for (int i = 0; i < early; ++i, ru.next(a.stages))
+          if (leader)
+            tma_load_2d(ring + ru.s * a.stage, &map_u, ((split + i * splits) % rblocks) * kLBK, t.t0, fulls + ru.s * 8);
+        __syncwarp();
+      }
+      for (int i = early; ok && i < mine; ++i, ++it, r.next(a.stages)) {
+        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+        if (!ok) break;
+        const int j = split + i * splits;
+        if (leader) {
+          load_b(r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK);
+          tma_load_2d(ring + r.s * a.stage, &map_u, (j % rblocks) * kLBK, t.t0, fulls + r.s * 8);
+        }
+        __syncwarp();
+      }
+      if (leader) mbar_arrive(smem_addr(sh.lempty + b));
+      __syncwarp();
     }
+    // the last load issued into each stage lands before the CTA may exit
+    if (leader) drain_ring(sh.full, r, it, a.stages);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- MMA issuer ----
-      Ring r;
-      int lt = 0;
-      const uint32_t idesc = idesc_bf16(kLBM, BN);
-      const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
-      const uint32_t empty = smem_addr(sh.empty);
-      bool ok = true;
-      for (int w = first; ok && w < total; w += stride, ++lt) {
-        const int buf = lt % kAcc;
-        if (!role_wait(sh.tempty + buf, ((lt / kAcc) & 1) ^ 1u, abort, a.err)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * BN;
-        for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
-          const uint32_t s = r.s;
-          if (!role_wait(sh.full + s, r.ph, abort, a.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t lo = xlo + s * step;
-          mma_block(d, lo, lo + xstep, idesc, kb != kb0);
-          mma_commit(empty + s * 8);
-        }
+    // ---- MMA issuer ----
+    Ring r;
+    int lt = 0;
+    const uint32_t idesc = idesc_bf16(kLBM, BN);
+    const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
+    const uint32_t empty = smem_addr(sh.empty);
+    bool ok = true;
+    for (int w = first; ok && w < total; w += stride, ++lt) {
+      const int buf = lt % kAcc;
+      ok = warp_wait(sh.tempty + buf, ((lt / kAcc) & 1) ^ 1u, abort, a.err);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * BN;
+      for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
+        ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
         if (!ok) break;
-        if (a.lora) {
-          const int b = lt & 1;
-          if (!role_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err)) break;
-          const int blocks = sh.count[b] * rblocks;
-          for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
-            const uint32_t s = r.s;
-            if (!role_wait(sh.full + s, r.ph, abort, a.err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sx = smem_addr(smem + s * a.stage), sw = sx + a.xbytes;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t lo = xlo + r.s * step;
+          mma_block(d, lo, lo + xstep, idesc, kb != kb0);
+          mma_commit(empty + r.s * 8);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (a.lora) {
+        const int b = lt & 1;
+        ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
+        if (!ok) break;
+        const int blocks = sh.count[b] * rblocks;
+        for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
+          ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t lo = xlo + r.s * step;
             const uint4 off = sh.off[b][j / rblocks];
             // columns past the rank are zeros in both tiles, so a step's last ones add nothing
             const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
             for (int kk = 0; kk * 16 < cols; ++kk)
-              mma_bf16_rows(d, sw128_desc(sx + kk * 32), sw128_desc(sw + kk * 32), idesc, off);
-            mma_commit(smem_addr(sh.empty + s));
+              mma_bf16_rows(d, full_desc(lo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
+            mma_commit(empty + r.s * 8);
           }
-          mbar_arrive(smem_addr(sh.lempty + b));
+          __syncwarp();
         }
-        if (ok) mma_commit(smem_addr(sh.tfull + buf));
+        if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       }
-      // every MMA issued completes before the tensor memory is freed
+      if (ok && leader) mma_commit(smem_addr(sh.tfull + buf));
+      __syncwarp();
+    }
+    // every MMA issued completes before the tensor memory is freed
+    if (leader) {
       mma_commit(smem_addr(&sh.done));
       mbar_wait_bounded(&sh.done, 0);
     }
@@ -623,7 +677,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     int lt = 0;
     for (int w = first; w < total; w += stride, ++lt) {
       const int buf = lt % kAcc;
-      if (!warp_wait(sh.tfull + buf, (lt / kAcc) & 1u, abort, a.err, lane)) break;
+      if (!warp_wait(sh.tfull + buf, (lt / kAcc) & 1u, abort, a.err)) break;
       tc_fence_after();
       const LTile t = ltile_of<BN>(w, a);
       const bool valid = t.t0 + m < a.T;
@@ -669,7 +723,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       const int b = lt & 1;
       const LTile t = ltile_of<BN>(w, a);
       // the four warps go on or give up together: the barriers below take all of them
-      if (!bar128_and<2>(warp_wait(sh.lempty + b, ((lt >> 1) & 1) ^ 1u, abort, a.err, lane))) break;
+      if (!bar128_and<2>(warp_wait(sh.lempty + b, ((lt >> 1) & 1) ^ 1u, abort, a.err))) break;
       int slot = -1;
       bool bad = false;  // reported by the shrink kernel
       sh.off[b][m] = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -781,8 +835,12 @@ constexpr int kSplitRing = 96 * 1024;  // two CTAs, or one and a shrink CTA, sha
 
 moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   const int most = a.adapters < a.T ? (a.adapters < kLBM ? a.adapters : kLBM) : (a.T < kLBM ? a.T : kLBM);
-  a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
-  if (a.per_pass > most) a.per_pass = most;
+  int splits = kLMaxCluster;
+  while (splits > 1 && (a.mtiles * splits > sms || splits > a.kblocks)) splits >>= 1;
+  // few tokens: their adapters are spread over the SMs that are left
+  const int spread = sms / (a.mtiles * splits) > 1 ? sms / (a.mtiles * splits) : 1;
+  a.per_pass = (most + spread - 1) / spread;
+  if (a.per_pass > kShrinkCols / a.rank) a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
   a.passes = (most + a.per_pass - 1) / a.per_pass;
   int n = (a.per_pass * a.rank + 15) & ~15;
   a.cols = 32;
@@ -790,8 +848,6 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
   // the adapters' rows end on whole 1024-byte swizzle groups, and the MMA's last
   // 16-row step may read one group past them
   a.stage = a.xbytes + n * kLRow;
-  int splits = kLMaxCluster;
-  while (splits > 1 && (a.mtiles * splits > sms || splits > a.kblocks)) splits >>= 1;
   a.stages = ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kShrinkRing);
   // the accumulator's 128 rows are read from the x tile's place also where the
   // tile has fewer rows: what follows it inside the allocation is read then
