@@ -63,10 +63,11 @@ struct LoraArgs {
   int stage, stages;   // bytes and number of the ring's stages
   int kblocks;
   // shrink
-  int per_pass, passes;  // adapters of a tile, and the most tiles that the adapters of 128 tokens need
+  int per_pass, groups;  // adapters of one pass over K, and the CTAs that share a tile's passes
   uint32_t cols;         // tensor-memory columns
   // projection
   int lora, ntiles_n, mtiles, group_n;
+  int whole, total;      // tiles taken whole, and tiles and halves in all
 };
 
 __device__ __forceinline__ uint32_t lora_cluster_rank() {
@@ -95,6 +96,33 @@ __device__ __forceinline__ float4 peer_load(uint32_t saddr, uint32_t rank) {
                : "r"(p)
                : "memory");
   return v;
+}
+
+// The sum over the cluster's CTAs, in their order, of 8 floats at this
+// shared-memory address. All loads are issued before the first is used: one
+// after the other they take a quarter of a microsecond each.
+__device__ __forceinline__ void cluster_sum8(uint32_t saddr, int ctas, float (&f)[8]) {
+  float4 lo[kLMaxCluster], hi[kLMaxCluster];
+#pragma unroll
+  for (int p = 0; p < kLMaxCluster; ++p)
+    if (p < ctas) {
+      lo[p] = peer_load(saddr, p);
+      hi[p] = peer_load(saddr + 16, p);
+    }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+#pragma unroll
+  for (int p = 0; p < kLMaxCluster; ++p)
+    if (p < ctas) {
+      f[0] += lo[p].x;
+      f[1] += lo[p].y;
+      f[2] += lo[p].z;
+      f[3] += lo[p].w;
+      f[4] += hi[p].x;
+      f[5] += hi[p].y;
+      f[6] += hi[p].z;
+      f[7] += hi[p].w;
+    }
 }
 
 template <int ID>
@@ -289,7 +317,7 @@ __device__ __forceinline__ int tile_adapters(const LoraArgs &a, int t0, int m, A
 // ---------------------------------------------------------------------------
 struct ShrinkShared {
   AdapterScratch scratch;
-  int32_t list[kLBM];
+  int32_t list[kLBM], slot[kLBM];  // the tile's adapters, and each token's place among them (-1: none)
   uint64_t full[kLMaxStages], empty[kLMaxStages], tfull, done;
   uint32_t tmem;
   int abort, n;
@@ -305,10 +333,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = static_cast<int>(lora_cluster_size()), split = static_cast<int>(lora_cluster_rank());
   const int item = static_cast<int>(blockIdx.x) / splits;
-  // the first adapters of every tile first: the CTAs of further ones mostly find nothing to do
-  const int pass = item / a.mtiles, mt = item - pass * a.mtiles;
+  const int group = item / a.mtiles, mt = item - group * a.mtiles;
   const int t0 = mt * kLBM;
 
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&sh.tmem), a.cols);
+    tmem_relinquish();
+  }
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(sh.full + s, 1);
@@ -323,131 +354,110 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   grid_dependency_wait();
   // the projection's CTAs may come: they find what this kernel's predecessors wrote, and by the rule on shared
-  // memory they leave this CTA its tensor memory
+  // memory they leave every CTA of this kernel its tensor memory
   grid_dependents_launch();
   int slot = -1;
   if (warp >= 2) {
     bool bad = false;
     const int n = tile_adapters<1>(a, t0, tid - 64, sh.scratch, sh.list, &slot, &bad);
-    if (bad && pass == 0 && split == 0) latch_error(a.err, MOE_EINVAL);
+    if (bad && group == 0 && split == 0) latch_error(a.err, MOE_EINVAL);
     if (tid == 64) sh.n = n;
-  }
-  __syncthreads();
-  const int first = pass * a.per_pass;
-  const int nact = min(sh.n - first, a.per_pass);  // adapters of this tile
-  if (nact <= 0) return;  // the same in every CTA of the cluster
-  if (warp == 1) {
-    tmem_alloc(smem_addr(&sh.tmem), a.cols);
-    tmem_relinquish();
+    sh.slot[tid - 64] = slot;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+  const bool leader = elect_one();  // used by warps 0 and 1
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
+  const int rows = min(kLBM, a.T - t0), vecs = a.rank / 8;
   float *red = reinterpret_cast<float *>(smem);  // [128][rank]: this split's sums, once the ring is idle
+  Ring r;
+  uint32_t it = 0, ph = 0;
 
-  const bool leader = elect_one();  // used by warps 0 and 1
-  if (warp == 0) {
-    uint32_t it = 0;
-    Ring r;
-    const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
-    for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
-      if (!warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err)) break;
+  // the tile's adapters, per_pass at a time (the same passes in every CTA of the cluster)
+  for (int first = group * a.per_pass; first < sh.n; first += a.groups * a.per_pass, ph ^= 1u) {
+    const int nact = min(sh.n - first, a.per_pass);
+    if (warp == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
+      for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
+        if (!warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err)) break;
+        if (leader) {
+          const uint32_t sx = smem_addr(smem) + r.s * a.stage, sa = sx + a.xbytes, fb = smem_addr(sh.full) + r.s * 8;
+          mbar_arrive_expect_tx(sh.full + r.s, bytes);
+          tma_load_2d(sx, &map_x, kb * kLBK, t0, fb);
+          for (int i = 0; i < nact; ++i)
+            tma_load_2d(sa + i * a.rank * kLRow, &map_a, kb * kLBK, sh.list[first + i] * a.rank, fb);
+        }
+        __syncwarp();
+      }
+      if (leader) drain_ring(sh.full, r, it, a.stages);
+      __syncwarp();
+    } else if (warp == 1) {
+      const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
+      const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
+      const uint32_t empty = smem_addr(sh.empty);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
+        ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t lo = xlo + r.s * step;
+          mma_block(tmem, lo, lo + xstep, idesc, kb != kb0);
+          mma_commit(empty + r.s * 8);
+        }
+        __syncwarp();
+      }
       if (leader) {
-        const uint32_t sx = smem_addr(smem) + r.s * a.stage, sa = sx + a.xbytes, fb = smem_addr(sh.full) + r.s * 8;
-        mbar_arrive_expect_tx(sh.full + r.s, bytes);
-        tma_load_2d(sx, &map_x, kb * kLBK, t0, fb);
-        for (int i = 0; i < nact; ++i)
-          tma_load_2d(sa + i * a.rank * kLRow, &map_a, kb * kLBK, sh.list[first + i] * a.rank, fb);
+        if (ok) mma_commit(smem_addr(&sh.tfull));
+        mma_commit(smem_addr(&sh.done));
+        mbar_wait_bounded(&sh.done, ph);
       }
       __syncwarp();
-    }
-    if (leader) drain_ring(sh.full, r, it, a.stages);
-    __syncwarp();
-  } else if (warp == 1) {
-    Ring r;
-    const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
-    const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
-    const uint32_t empty = smem_addr(sh.empty);
-    bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
-      ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t lo = xlo + r.s * step;
-        mma_block(tmem, lo, lo + xstep, idesc, kb != kb0);
-        mma_commit(empty + r.s * 8);
-      }
-      __syncwarp();
-    }
-    if (leader) {
-      if (ok) mma_commit(smem_addr(&sh.tfull));
-      mma_commit(smem_addr(&sh.done));
-      mbar_wait_bounded(&sh.done, 0);
-    }
-    __syncwarp();
-  } else {
-    // this token's own columns of the tile
-    const int q = warp & 3, m = q * 32 + lane;
-    if (warp_wait(&sh.tfull, 0, abort, a.err)) {
-      tc_fence_after();
-      // thread tid - 64 found the slot of token tid - 64; accumulator row m is token m
-      const int own = __ldg(a.adapter + min(t0 + m, a.T - 1));
-      int mine = -1;
-      if (t0 + m < a.T)
-        for (int i = 0; i < nact; ++i)
-          if (sh.list[first + i] == own) mine = i;
-      for (int i = 0; i < nact; ++i) {
-        if (!__any_sync(0xffffffffu, mine == i)) continue;
-        for (int c = 0; c < a.rank; c += 8) {
-          float f[8];
-          tmem_load8_wait(tmem + (static_cast<uint32_t>(q * 32) << 16) + i * a.rank + c, f);
-          if (mine == i) {
-            float4 *d = reinterpret_cast<float4 *>(red + m * a.rank + c);
-            d[0] = make_float4(f[0], f[1], f[2], f[3]);
-            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      // each token's own columns of the tile (accumulator row m is token t0 + m)
+      const int q = warp & 3, m = q * 32 + lane;
+      const int mine = sh.slot[m] - first;
+      if (warp_wait(&sh.tfull, ph, abort, a.err)) {
+        tc_fence_after();
+        for (int i = 0; i < nact; ++i) {
+          if (!__any_sync(0xffffffffu, mine == i)) continue;
+          for (int c = 0; c < a.rank; c += 8) {
+            float f[8];
+            tmem_load8_wait(tmem + (static_cast<uint32_t>(q * 32) << 16) + i * a.rank + c, f);
+            if (mine == i) {
+              float4 *d = reinterpret_cast<float4 *>(red + m * a.rank + c);
+              d[0] = make_float4(f[0], f[1], f[2], f[3]);
+              d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
           }
         }
+        tc_fence_before();
       }
-      tc_fence_before();
+      __syncwarp();
     }
-    __syncwarp();
-  }
-  lora_cluster_sync();
-  // the splits' sums in their order, each CTA a share of the rows
-  const int rows = min(kLBM, a.T - t0), vecs = a.rank / 8;
-  for (int i = split * kShrinkThreads + tid; i < rows * vecs; i += splits * kShrinkThreads) {
-    const int m = i / vecs, c = (i - m * vecs) * 8;
-    const int id = __ldg(a.adapter + t0 + m);
-    bool mine = false;
-    for (int p = 0; p < nact; ++p) mine |= sh.list[first + p] == id;
-    if (!mine) continue;
-    const float sc = a.scales != nullptr ? __ldg(a.scales + id) : 1.0f;
-    const uint32_t at = smem_addr(red + m * a.rank + c);
-    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int p = 0; p < splits; ++p) {
-      const float4 lo = peer_load(at, p), hi = peer_load(at + 16, p);
-      f[0] += lo.x;
-      f[1] += lo.y;
-      f[2] += lo.z;
-      f[3] += lo.w;
-      f[4] += hi.x;
-      f[5] += hi.y;
-      f[6] += hi.z;
-      f[7] += hi.w;
-    }
+    lora_cluster_sync();
+    // the splits' sums, row m in CTA m % splits
+    const int own = (rows - split + splits - 1) / splits;
+    for (int i = tid; i < own * vecs; i += kShrinkThreads) {
+      const int q = i / vecs, m = q * splits + split, c = (i - q * vecs) * 8;
+      const int p = sh.slot[m] - first;
+      if (p < 0 || p >= nact) continue;
+      const float sc = a.scales != nullptr ? __ldg(a.scales + sh.list[first + p]) : 1.0f;
+      float f[8];
+      cluster_sum8(smem_addr(red + m * a.rank + c), splits, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= sc;
-    *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(t0 + m) * a.rank + c) = round8(f);
-  }
-  lora_cluster_sync();  // no CTA leaves while another may still read its sums
-  if (warp == 1) {
+      for (int j = 0; j < 8; ++j) f[j] *= sc;
+      *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(t0 + m) * a.rank + c) = round8(f);
+    }
+    fence_proxy_async_smem();  // the ring is loaded again where the sums were
+    lora_cluster_sync();       // and no CTA leaves while another may still read its sums
     tc_fence_after();
-    tmem_dealloc(tmem, a.cols);
   }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, a.cols);
 }
 
 // ---------------------------------------------------------------------------
@@ -467,19 +477,27 @@ struct GemmShared {
 static_assert(sizeof(GemmShared) <= kLStatic && sizeof(ShrinkShared) <= kLStatic, "");
 
 struct LTile {
-  int t0, n0;
+  int t0, n0, cols;
 };
 
 // Tile w: groups of group_n n-tiles, each group swept over the m-tiles with its
 // n-tiles innermost, so that the CTAs running at one time share both the
-// group's weight tiles and each m-tile's rows in L2.
+// group's weight tiles and each m-tile's rows in L2. The tiles from `whole` on
+// are cut in halves of 128 outputs, numbered one after the other: the last,
+// partial wave of whole tiles would keep less than half of the SMs busy.
 template <int BN>
 __device__ __forceinline__ LTile ltile_of(int w, const LoraArgs &a) {
+  int half = 0, cols = BN;
+  if (BN > 128 && w >= a.whole) {
+    half = (w - a.whole) & 1;
+    w = a.whole + ((w - a.whole) >> 1);
+    cols = BN / 2;
+  }
   const int per_group = a.mtiles * a.group_n;
   const int g = w / per_group, r = w - g * per_group;
   const int gw = min(a.group_n, a.ntiles_n - g * a.group_n);
   const int mt = r / gw;
-  return LTile{mt * kLBM, (g * a.group_n + r - mt * gw) * BN};
+  return LTile{mt * kLBM, (g * a.group_n + r - mt * gw) * BN + half * (BN / 2), cols};
 }
 
 template <int BN, bool SPLIT>
@@ -489,7 +507,6 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
                      const LoraArgs a) {
   constexpr int kAcc = SPLIT ? 1 : 2;               // accumulators
   constexpr uint32_t kCols = kAcc * BN;
-  constexpr uint32_t kWBytes = BN * kLRow;
   constexpr int kRedPitch = BN + 4;                 // floats of a row of partial sums
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) GemmShared sh;
@@ -500,7 +517,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   const int split = SPLIT ? static_cast<int>(lora_cluster_rank()) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.x) / splits : static_cast<int>(blockIdx.x);
   const int stride = SPLIT ? static_cast<int>(gridDim.x) / splits : static_cast<int>(gridDim.x);
-  const int total = a.mtiles * a.ntiles_n;
+  const int total = a.total;
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
   const int rblocks = (a.rank + kLBK - 1) / kLBK;   // K blocks of one adapter
@@ -529,11 +546,11 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   // With adapters the shrink kernel comes before this one: it let this grid
   // start only after its own dependency wait, so x is there, and only the
   // producer waits for it, before its first load of u.
-  if (!a.lora) grid_dependency_wait();
   if (warp == 1) {
     tmem_alloc(smem_addr(&sh.tmem), kCols);
     tmem_relinquish();
   }
+  if (!a.lora) grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -547,13 +564,12 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     int lt = 0;
     bool ok = true, waited = false;
     const uint32_t ring = smem_addr(smem), fulls = smem_addr(sh.full);
-    const uint32_t bytes = static_cast<uint32_t>(a.xrows) * kLRow + kWBytes;
-    // arms stage s for a block of the adapters and asks for its B_a tile
-    const auto load_b = [&](uint32_t s, int row, int k) {
+    // arms stage s for a block of the tile and asks for its rows of W or of B_a
+    const auto load_w = [&](const CUtensorMap *map, uint32_t s, int row, int k, int cols) {
       const uint32_t sw = ring + s * a.stage + a.xbytes, fb = fulls + s * 8;
-      mbar_arrive_expect_tx(sh.full + s, bytes);
-      tma_load_2d(sw, &map_b, k, row, fb);
-      if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_b, k, row + kBoxRows, fb);
+      mbar_arrive_expect_tx(sh.full + s, static_cast<uint32_t>(a.xrows + cols) * kLRow);
+      tma_load_2d(sw, map, k, row, fb);
+      if (cols > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, map, k, row + kBoxRows, fb);
     };
     for (int w = first; ok && w < total; w += stride, ++lt) {
       const LTile t = ltile_of<BN>(w, a);
@@ -561,11 +577,8 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
         if (!ok) break;
         if (leader) {
-          const uint32_t sx = ring + r.s * a.stage, sw = sx + a.xbytes, fb = fulls + r.s * 8;
-          mbar_arrive_expect_tx(sh.full + r.s, bytes);
-          tma_load_2d(sw, &map_w, kb * kLBK, t.n0, fb);
-          if (BN > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, &map_w, kb * kLBK, t.n0 + kBoxRows, fb);
-          tma_load_2d(sx, &map_x, kb * kLBK, t.t0, fb);
+          load_w(&map_w, r.s, t.n0, kb * kLBK, t.cols);
+          tma_load_2d(ring + r.s * a.stage, &map_x, kb * kLBK, t.t0, fulls + r.s * 8);
         }
         __syncwarp();
       }
@@ -586,7 +599,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
           break;
         }
         const int j = split + i * splits;
-        if (leader) load_b(r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK);
+        if (leader) load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
         __syncwarp();
       }
       if (early > 0) {
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         if (!ok) break;
         const int j = split + i * splits;
         if (leader) {
-          load_b(r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK);
+          load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
           tma_load_2d(ring + r.s * a.stage, &map_u, (j % rblocks) * kLBK, t.t0, fulls + r.s * 8);
         }
         __syncwarp();
@@ -611,6 +624,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       __syncwarp();
     }
+    grid_dependents_launch();  // what comes next may set itself up during the last products and stores
     // the last load issued into each stage lands before the CTA may exit
     if (leader) drain_ring(sh.full, r, it, a.stages);
     __syncwarp();
@@ -618,7 +632,6 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     // ---- MMA issuer ----
     Ring r;
     int lt = 0;
-    const uint32_t idesc = idesc_bf16(kLBM, BN);
     const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
     const uint32_t empty = smem_addr(sh.empty);
     bool ok = true;
@@ -627,7 +640,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       ok = warp_wait(sh.tempty + buf, ((lt / kAcc) & 1) ^ 1u, abort, a.err);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + buf * BN;
+      const uint32_t d = tmem + buf * BN, idesc = idesc_bf16(kLBM, ltile_of<BN>(w, a).cols);
       for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
         ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
         if (!ok) break;
@@ -696,7 +709,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         }
       } else {
         __nv_bfloat16 *row = a.y + static_cast<int64_t>(valid ? t.t0 + m : 0) * a.N + t.n0;
-        for (int c = 0; c < BN; c += 32) {
+        for (int c = 0; c < t.cols; c += 32) {
           uint32_t r[32];
           tmem_load32_wait(tb + c, r);
           if (!valid) continue;
@@ -738,26 +751,16 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   if constexpr (SPLIT) {
     lora_cluster_sync();
     if (first < total) {
-      // the splits' sums in their order, each CTA a share of the rows
+      // the splits' sums, row m in CTA m % splits
       const LTile t = ltile_of<BN>(first, a);
       const int rows = min(kLBM, a.T - t.t0);
       constexpr int vecs = BN / 8;
-      for (int i = split * kGemmLThreads + tid; i < rows * vecs; i += splits * kGemmLThreads) {
-        const int m = i / vecs, c = (i - m * vecs) * 8;
+      const int own = (rows - split + splits - 1) / splits;
+      for (int i = tid; i < own * vecs; i += kGemmLThreads) {
+        const int q = i / vecs, m = q * splits + split, c = (i - q * vecs) * 8;
         if (t.n0 + c >= a.N) continue;
-        const uint32_t at = smem_addr(reinterpret_cast<float *>(smem) + m * kRedPitch + c);
-        float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int p = 0; p < splits; ++p) {
-          const float4 lo = peer_load(at, p), hi = peer_load(at + 16, p);
-          f[0] += lo.x;
-          f[1] += lo.y;
-          f[2] += lo.z;
-          f[3] += lo.w;
-          f[4] += hi.x;
-          f[5] += hi.y;
-          f[6] += hi.z;
-          f[7] += hi.w;
-        }
+        float f[8];
+        cluster_sum8(smem_addr(reinterpret_cast<float *>(smem) + m * kRedPitch + c), splits, f);
         *reinterpret_cast<uint4 *>(a.y + static_cast<int64_t>(t.t0 + m) * a.N + t.n0 + c) = round8(f);
       }
     }
@@ -794,7 +797,11 @@ bool make_box_map(CUtensorMap *map, const void *base, int64_t K, int64_t rows, i
 template <class... P, class... Q>
 moe_status launch_cluster(void (*fn)(P...), int grid, int threads, int cluster, int smem, cudaStream_t stream,
                           Q &&...args) {
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ECUDA;
+  // the largest carve-out, so that an SM which runs one of the two kernels has room for the other
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess)
+    return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -841,7 +848,8 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
   const int spread = sms / (a.mtiles * splits) > 1 ? sms / (a.mtiles * splits) : 1;
   a.per_pass = (most + spread - 1) / spread;
   if (a.per_pass > kShrinkCols / a.rank) a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
-  a.passes = (most + a.per_pass - 1) / a.per_pass;
+  a.groups = (most + a.per_pass - 1) / a.per_pass;
+  if (a.groups > spread) a.groups = spread;
   int n = (a.per_pass * a.rank + 15) & ~15;
   a.cols = 32;
   while (static_cast<int>(a.cols) < n) a.cols <<= 1;
@@ -859,7 +867,7 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
   if (!make_box_map(&mx, x, a.K, a.T, a.xrows) ||
       !make_box_map(&ma, lora_a, a.K, static_cast<int64_t>(a.adapters) * a.rank, a.rank))
     return MOE_ECUDA;
-  const int64_t grid = static_cast<int64_t>(a.mtiles) * a.passes * splits;
+  const int64_t grid = static_cast<int64_t>(a.mtiles) * a.groups * splits;
   if (grid > 0x7fffffffll) return MOE_EINVAL;
   return launch_cluster(lora_shrink_kernel, static_cast<int>(grid), kShrinkThreads, splits, smem, stream, mx, ma, a);
 }
@@ -869,10 +877,18 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
                        cudaStream_t stream) {
   a.ntiles_n = (a.N + BN - 1) / BN;
   a.stage = a.xbytes + BN * kLRow;
-  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kSplitRing) : 4;
+  // BN 128: six stages, whose 192 KB cover the latency of loads from L2 (four of 32 KB: 0.35 us a block, 256
+  // cycles of products)
+  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kSplitRing) : (BN > 128 ? 4 : 6);
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
-  if (tiles > 0x7fffffffll / kLMaxCluster) return MOE_EINVAL;
+  if (tiles > 0x3fffffffll / kLMaxCluster) return MOE_EINVAL;
+  a.whole = a.total = static_cast<int>(tiles);
   const int64_t grid = SPLIT ? tiles * splits : (tiles < sms ? tiles : sms);
+  const int rest = static_cast<int>(tiles % grid);
+  if (BN > 128 && !SPLIT && rest > 0 && 2 * rest <= grid) {
+    a.whole -= rest;
+    a.total += rest;
+  }
   a.group_n = a.ntiles_n < 8 ? a.ntiles_n : 8;
   const int smem = with_columns(1024 + a.stages * a.stage, (SPLIT ? 1 : 2) * BN);
   if (smem > kLSmemMax - kLStatic) return MOE_EINVAL;
