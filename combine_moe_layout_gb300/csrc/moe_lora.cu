@@ -15,9 +15,8 @@
 //
 // Two kernels:
 //   lora_shrink_kernel  u[t] = s_a x[t] A_a^T. A tile is 128 tokens against the
-//     stacked rows of up to 128 / rank adapters that occur among them (one
-//     adapter's 256 rows at most): a token's own columns are picked in the
-//     epilogue. in is split over a cluster of CTAs whose partial sums meet in
+//     stacked rows of up to 256 / rank adapters that occur among them: a token's
+//     own columns are picked in the epilogue. in is split over a cluster of CTAs whose partial sums meet in
 //     distributed shared memory in a fixed order.
 //   lora_gemm_kernel    the projection with its extra K blocks. Tiles of 128
 //     tokens x BN outputs; TMA brings x and W (then u and B_a) tiles, one lane
@@ -48,8 +47,9 @@ constexpr int kLStatic = 8192;      // room for a kernel's static shared memory
 constexpr int kLBytesPerCol = 228 * 1024 / 512;  // shared memory that goes with one tensor-memory column
 constexpr int kShrinkThreads = 192;
 constexpr int kGemmLThreads = 320;
-constexpr int kShrinkCols = 128;    // adapter rows of a shrink tile (or one adapter's, if it has more)
-constexpr int kLMaxCluster = 8;
+constexpr int kShrinkCols = 256;    // adapter rows of a shrink tile
+constexpr int kLMaxCluster = 8;    // of the shrink kernel
+constexpr int kLMaxSplit = 4;      // of the projection
 
 struct LoraArgs {
   const int32_t *adapter;
@@ -468,7 +468,7 @@ struct GemmShared {
   int32_t list[2][kLBM];        // the adapters of a tile's tokens
   uint4 off[2][kLBM];           // for each of them, the rows that do not use it
   uint64_t full[kLMaxStages], empty[kLMaxStages];
-  uint64_t tfull[2], tempty[2], lfull[2], lempty[2], done;
+  uint64_t tfull[2], tempty[2], lfull[2], lempty[2], ufull, uempty, done;
   int count[2];
   uint32_t tmem;
   int abort;
@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) GemmShared sh;
   uint8_t *smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
+  const uint32_t ubuf = smem_addr(smem) + a.stages * a.stage;  // the tile's u, one x-shaped tile per 64 columns
   volatile int *abort = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = SPLIT ? static_cast<int>(lora_cluster_size()) : 1;
@@ -533,6 +534,8 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       mbar_init(sh.lfull + b, 1);
       mbar_init(sh.lempty + b, 2);
     }
+    mbar_init(&sh.ufull, 1);
+    mbar_init(&sh.uempty, 1);
     mbar_init(&sh.done, 1);
     sh.abort = 0;
     fence_mbar_init();
@@ -564,10 +567,10 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     int lt = 0;
     bool ok = true, waited = false;
     const uint32_t ring = smem_addr(smem), fulls = smem_addr(sh.full);
-    // arms stage s for a block of the tile and asks for its rows of W or of B_a
+    uint32_t uphase = 0;  // tiles whose u was loaded
+    // asks for the tile's rows of W or of B_a in stage s
     const auto load_w = [&](const CUtensorMap *map, uint32_t s, int row, int k, int cols) {
       const uint32_t sw = ring + s * a.stage + a.xbytes, fb = fulls + s * 8;
-      mbar_arrive_expect_tx(sh.full + s, static_cast<uint32_t>(a.xrows + cols) * kLRow);
       tma_load_2d(sw, map, k, row, fb);
       if (cols > kBoxRows) tma_load_2d(sw + kBoxRows * kLRow, map, k, row + kBoxRows, fb);
     };
@@ -577,6 +580,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
         if (!ok) break;
         if (leader) {
+          mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(a.xrows + t.cols) * kLRow);
           load_w(&map_w, r.s, t.n0, kb * kLBK, t.cols);
           tma_load_2d(ring + r.s * a.stage, &map_x, kb * kLBK, t.t0, fulls + r.s * 8);
         }
@@ -587,46 +591,46 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
       if (!ok) break;
       const int blocks = sh.count[b] * rblocks;
-      const int mine = (blocks - split + splits - 1) / splits;  // blocks of this CTA: split, split + splits, ...
       // The first B_a tiles are asked for before the wait for u, as far as the
-      // ring goes: no block of the adapters gives its stage back without u.
-      int early = waited ? 0 : min(mine, a.stages);
-      const Ring r0 = r;
-      for (int i = 0; i < early; ++i, ++it, r.next(a.stages)) {
-        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
-        if (!ok) {
-          early = i;
-          break;
-        }
-        const int j = split + i * splits;
-        if (leader) load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
-        __syncwarp();
-      }
-      if (early > 0) {
-        grid_dependency_wait();  // u is written
+      // ring goes: no block of the adapters gives its stage back without u. The
+      // tile's u is loaded once: every CTA reads the same few rows, and once per
+      // adapter (64 tokens, 32 adapters of rank 16) they took 0.7 us a block.
+      bool u_asked = false;
+      const auto load_u = [&]() {
+        if (!waited) grid_dependency_wait();  // u is written
         waited = true;
-        Ring ru = r0;
-        for (int i = 0; i < early; ++i, ru.next(a.stages))
-          if (leader)
-            tma_load_2d(ring + ru.s * a.stage, &map_u, ((split + i * splits) % rblocks) * kLBK, t.t0, fulls + ru.s * 8);
-        __syncwarp();
-      }
-      for (int i = early; ok && i < mine; ++i, ++it, r.next(a.stages)) {
-        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
-        if (!ok) break;
-        const int j = split + i * splits;
+        u_asked = true;
+        ok = warp_wait(&sh.uempty, (uphase & 1u) ^ 1u, abort, a.err);
+        if (!ok) return;
+        ++uphase;
         if (leader) {
+          mbar_arrive_expect_tx(&sh.ufull, static_cast<uint32_t>(rblocks * a.xrows) * kLRow);
+          for (int q = 0; q < rblocks; ++q)
+            tma_load_2d(ubuf + q * a.xbytes, &map_u, q * kLBK, t.t0, smem_addr(&sh.ufull));
+        }
+        __syncwarp();
+      };
+      int ahead = waited ? 0 : a.stages;  // blocks to ask for before u
+      for (int j = split; ok && j < blocks; j += splits, ++it, r.next(a.stages), --ahead) {
+        if (!u_asked && ahead <= 0) load_u();
+        ok = ok && warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+        if (!ok) break;
+        if (leader) {
+          mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(t.cols) * kLRow);
           load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
-          tma_load_2d(ring + r.s * a.stage, &map_u, (j % rblocks) * kLBK, t.t0, fulls + r.s * 8);
         }
         __syncwarp();
       }
+      if (ok && !u_asked && split < blocks) load_u();
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       __syncwarp();
     }
     grid_dependents_launch();  // what comes next may set itself up during the last products and stores
-    // the last load issued into each stage lands before the CTA may exit
-    if (leader) drain_ring(sh.full, r, it, a.stages);
+    // the last loads land before the CTA may exit
+    if (leader) {
+      drain_ring(sh.full, r, it, a.stages);
+      if (uphase > 0) mbar_wait_bounded(&sh.ufull, (uphase - 1) & 1u);
+    }
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer ----
@@ -634,6 +638,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     int lt = 0;
     const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
     const uint32_t empty = smem_addr(sh.empty);
+    uint32_t uphase = 0;  // tiles whose u was used
     bool ok = true;
     for (int w = first; ok && w < total; w += stride, ++lt) {
       const int buf = lt % kAcc;
@@ -658,22 +663,30 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
         if (!ok) break;
         const int blocks = sh.count[b] * rblocks;
+        if (split < blocks) {
+          ok = warp_wait(&sh.ufull, uphase & 1u, abort, a.err);
+          if (!ok) break;
+          ++uphase;
+        }
         for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
           ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            const uint32_t lo = xlo + r.s * step;
+            const uint32_t lo = xlo + r.s * step, ulo = desc_lo(ubuf) + (j % rblocks) * xstep;
             const uint4 off = sh.off[b][j / rblocks];
             // columns past the rank are zeros in both tiles, so a step's last ones add nothing
             const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
             for (int kk = 0; kk * 16 < cols; ++kk)
-              mma_bf16_rows(d, full_desc(lo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
+              mma_bf16_rows(d, full_desc(ulo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
             mma_commit(empty + r.s * 8);
           }
           __syncwarp();
         }
-        if (leader) mbar_arrive(smem_addr(sh.lempty + b));
+        if (leader) {
+          mbar_arrive(smem_addr(sh.lempty + b));
+          if (split < blocks) mma_commit(smem_addr(&sh.uempty));
+        }
       }
       if (ok && leader) mma_commit(smem_addr(sh.tfull + buf));
       __syncwarp();
@@ -829,25 +842,29 @@ int with_columns(int smem, int cols) {
   return smem > share ? smem : share;
 }
 
-// Stages of a ring of at most `bytes` (and at least 4, or as many as there are K blocks).
+// Stages of a ring of at most `bytes`, no more than there are K blocks, and at least 3.
 int ring_stages(int stage, int blocks, int bytes) {
   int n = bytes / stage;
   if (n > kLMaxStages) n = kLMaxStages;
   if (n > blocks) n = blocks;
-  return n < 4 ? 4 : n;
+  return n < 3 ? 3 : n;
 }
 
-constexpr int kShrinkRing = 96 * 1024;
-constexpr int kSplitRing = 96 * 1024;  // two CTAs, or one and a shrink CTA, share an SM
+// Rings of CTAs that are to share an SM: a shrink CTA and one of the
+// projection, or two of the projection. The projection's 256-wide tiles take a
+// whole SM, and the shrink kernel before them need not leave any room.
+constexpr int kShrinkRing = 84 * 1024;
+constexpr int kShrinkRingAlone = 192 * 1024;
+constexpr int kSplitRing = 96 * 1024;
 
-moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
+moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, bool alone, cudaStream_t stream) {
   const int most = a.adapters < a.T ? (a.adapters < kLBM ? a.adapters : kLBM) : (a.T < kLBM ? a.T : kLBM);
   int splits = kLMaxCluster;
   while (splits > 1 && (a.mtiles * splits > sms || splits > a.kblocks)) splits >>= 1;
   // few tokens: their adapters are spread over the SMs that are left
   const int spread = sms / (a.mtiles * splits) > 1 ? sms / (a.mtiles * splits) : 1;
   a.per_pass = (most + spread - 1) / spread;
-  if (a.per_pass > kShrinkCols / a.rank) a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
+  if (a.per_pass > kShrinkCols / a.rank) a.per_pass = kShrinkCols / a.rank;
   a.groups = (most + a.per_pass - 1) / a.per_pass;
   if (a.groups > spread) a.groups = spread;
   int n = (a.per_pass * a.rank + 15) & ~15;
@@ -856,10 +873,10 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
   // the adapters' rows end on whole 1024-byte swizzle groups, and the MMA's last
   // 16-row step may read one group past them
   a.stage = a.xbytes + n * kLRow;
-  a.stages = ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kShrinkRing);
-  // the accumulator's 128 rows are read from the x tile's place also where the
-  // tile has fewer rows: what follows it inside the allocation is read then
-  int smem = 1024 + a.stages * a.stage + kLBM * kLRow;
+  a.stages = ring_stages(a.stage, (a.kblocks + splits - 1) / splits, alone ? kShrinkRingAlone : kShrinkRing);
+  // the products take 128 rows from the x tile's place also where the tile has
+  // fewer: what follows it inside the allocation is read then
+  int smem = 1024 + a.stages * a.stage + kLBM * kLRow - a.xbytes;
   const int red = 1024 + kLBM * a.rank * 4;
   if (smem < red) smem = red;
   smem = with_columns(smem, static_cast<int>(a.cols));
@@ -877,11 +894,15 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
                        cudaStream_t stream) {
   a.ntiles_n = (a.N + BN - 1) / BN;
   a.stage = a.xbytes + BN * kLRow;
-  // BN 128: six stages, whose 192 KB cover the latency of loads from L2 (four of 32 KB: 0.35 us a block, 256
-  // cycles of products)
-  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kSplitRing) : (BN > 128 ? 4 : 6);
+  const int rblocks = a.lora ? (a.rank + kLBK - 1) / kLBK : 0;
+  // what follows the ring: u, and the rest of the 128 rows of x that the products take (as in the shrink kernel)
+  const int tail = rblocks * a.xbytes + kLBM * kLRow - a.xbytes;
+  // BN 256: four stages, or three beside a u of rank above 64. BN 128: three (with six, which keep the shrink
+  // kernel's CTAs off the SM, no block came sooner)
+  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kSplitRing)
+                   : (BN > 128 && rblocks <= 1 ? 4 : 3);
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
-  if (tiles > 0x3fffffffll / kLMaxCluster) return MOE_EINVAL;
+  if (tiles > 0x3fffffffll / kLMaxSplit) return MOE_EINVAL;
   a.whole = a.total = static_cast<int>(tiles);
   const int64_t grid = SPLIT ? tiles * splits : (tiles < sms ? tiles : sms);
   const int rest = static_cast<int>(tiles % grid);
@@ -890,14 +911,15 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
     a.total += rest;
   }
   a.group_n = a.ntiles_n < 8 ? a.ntiles_n : 8;
-  const int smem = with_columns(1024 + a.stages * a.stage, (SPLIT ? 1 : 2) * BN);
+  const int smem = with_columns(1024 + a.stages * a.stage + tail, (SPLIT ? 1 : 2) * BN);
   if (smem > kLSmemMax - kLStatic) return MOE_EINVAL;
+  constexpr int kBox = BN < kBoxRows ? BN : kBoxRows;
   CUtensorMap mx, mw, mu, mb;
-  if (!make_box_map(&mx, x, a.K, a.T, a.xrows) || !make_box_map(&mw, w, a.K, a.N, kBoxRows)) return MOE_ECUDA;
+  if (!make_box_map(&mx, x, a.K, a.T, a.xrows) || !make_box_map(&mw, w, a.K, a.N, kBox)) return MOE_ECUDA;
   mu = mx;
   mb = mw;  // not used without adapters
   if (a.lora && (!make_box_map(&mu, a.u, a.rank, a.T, a.xrows) ||
-                 !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBoxRows)))
+                 !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBox)))
     return MOE_ECUDA;
   return launch_cluster(lora_gemm_kernel<BN, SPLIT>, static_cast<int>(grid), kGemmLThreads, SPLIT ? splits : 1, smem,
                         stream, mx, mw, mu, mb, a);
@@ -944,15 +966,21 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
   a.xbytes = a.xrows * kLRow;
   a.kblocks = (K + kLBK - 1) / kLBK;
   a.mtiles = (T + kLBM - 1) / kLBM;
+  const int64_t tiles256 = static_cast<int64_t>(a.mtiles) * ((N + 255) / 256);
   if (a.lora) {
-    const moe_status st = launch_shrink(a, x, lora_a, sms, cs);
+    const moe_status st = launch_shrink(a, x, lora_a, sms, tiles256 >= sms, cs);
     if (st != MOE_OK) return st;
   }
-  const int64_t tiles256 = static_cast<int64_t>(a.mtiles) * ((N + 255) / 256);
   const int64_t tiles128 = static_cast<int64_t>(a.mtiles) * ((N + 127) / 128);
+  const int64_t tiles64 = static_cast<int64_t>(a.mtiles) * ((N + 63) / 64);
   if (tiles256 >= sms) return launch_gemm<256, false>(a, x, w, lora_b, 1, sms, cs);
-  int splits = kLMaxCluster;
+  // Fewer tiles than SMs: in is split over clusters of up to 4 CTAs (of 8, the
+  // last of 16 clusters found no place until another had ended), and where that
+  // is still too few the tiles are 64 outputs wide.
+  int splits = kLMaxSplit;
   while (splits > 1 && (tiles128 * splits > sms || splits > a.kblocks)) splits >>= 1;
+  if (splits == kLMaxSplit && tiles64 * splits <= sms)
+    return launch_gemm<64, true>(a, x, w, lora_b, splits, sms, cs);
   if (splits > 1) return launch_gemm<128, true>(a, x, w, lora_b, splits, sms, cs);
   return launch_gemm<128, false>(a, x, w, lora_b, 1, sms, cs);
 }
