@@ -461,9 +461,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
 }
 
 // ---------------------------------------------------------------------------
-// u for few tokens: one cluster of CTAs per (adapter, 16 of its rows, 32 of its
-// tokens), K split over the cluster's warps so that all of a row is in flight in
-// one or two rounds of loads. The tensor-core tiles above take 128 tokens
+// u for few tokens: one cluster of CTAs per (adapter, 16 of its rows), which
+// takes its tokens 16 at a time, K split over the cluster's warps so that all of
+// a row is in flight in one or two rounds of loads. The tensor-core tiles above take 128 tokens
 // whether they use the adapter or not; here a token's x row meets only its own
 // adapter.
 // Products: mma.sync, whose 16-row tiles fit a handful of tokens (a
@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 256;
 constexpr int kSmallWarps = kSmallThreads / 32;
-constexpr int kSmallM = 32, kSmallN = 16;
+constexpr int kSmallM = 16, kSmallN = 16;
+constexpr int kSmallTokensPerCta = 64;  // calls of more tokens have more CTAs per adapter, which exit where there is nothing to do
 
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -489,21 +490,20 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (two CTAs per SM: at most 128 registers a thread, which leave a CTA of the projection its own)
-__global__ void __launch_bounds__(kSmallThreads, 2)
+__global__ void __launch_bounds__(kSmallThreads)
     lora_shrink_small_kernel(const LoraArgs a, const uint4 *__restrict__ x, const uint4 *__restrict__ lora_a) {
   __shared__ float part[kSmallWarps][kSmallM][kSmallN + 1];
   __shared__ __align__(16) float red[kSmallM][kSmallN];  // this CTA's sums
-  __shared__ int32_t token[kSmallM];
+  __shared__ int32_t token[kLBM];
   __shared__ int32_t counts[kSmallWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = static_cast<int>(lora_cluster_size()), split = static_cast<int>(lora_cluster_rank());
-  const int ad = blockIdx.x / splits, n0 = blockIdx.y * kSmallN, m0 = blockIdx.z * kSmallM;
+  const int ad = blockIdx.x / splits, n0 = blockIdx.y * kSmallN;
   grid_dependency_wait();
   grid_dependents_launch();  // the projection finds what this kernel's predecessors wrote
-  // this adapter's tokens m0 .. m0 + 31, in token order
+  // this adapter's tokens, in token order
   const int id = tid < a.T ? __ldg(a.adapter + tid) : -1;
-  if ((id < -1 || id >= a.adapters) && blockIdx.x == 0 && n0 == 0 && m0 == 0) latch_error(a.err, MOE_EINVAL);
+  if ((id < -1 || id >= a.adapters) && blockIdx.x == 0 && n0 == 0 && blockIdx.z == 0) latch_error(a.err, MOE_EINVAL);
   const unsigned users = __ballot_sync(0xffffffffu, id == ad);
   if (lane == 0) counts[warp] = __popc(users);
   __syncthreads();
@@ -513,74 +513,71 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     if (w < warp) at += counts[w];
     total += counts[w];
   }
-  if (total <= m0) return;  // the same in every CTA of the cluster
-  if (id == ad && at >= m0 && at < m0 + kSmallM) token[at - m0] = tid;
+  if (id == ad) token[at] = tid;
   __syncthreads();
-  const int nt = min(total - m0, kSmallM);
   const int g = lane >> 2, t4 = lane & 3;
   const int kv = a.K / 8;  // 16-byte vectors of a row
-  const uint4 *xr[4], *ar[2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) xr[i] = i * 8 + g < nt ? x + static_cast<int64_t>(token[i * 8 + g]) * kv : nullptr;
+  const uint4 *ar[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     ar[i] = n0 + i * 8 + g < a.rank ? lora_a + (static_cast<int64_t>(ad) * a.rank + n0 + i * 8 + g) * kv : nullptr;
-  float acc[2][2][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int pieces = (kv + 3) / 4;
+  const int pieces = (kv + 3) / 4, stride = kSmallWarps * splits;
   constexpr int kUnroll = 4;
-  const bool two = nt > 16;
-  const int stride = kSmallWarps * splits;
-  for (int p0 = split * kSmallWarps + warp; p0 < pieces; p0 += stride * kUnroll) {
-    uint4 xv[kUnroll][4], av[kUnroll][2];
+  const float sc = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
+
+  // 16 tokens at a time, the same ones in every CTA of the cluster
+  for (int m0 = blockIdx.z * kSmallM; m0 < total; m0 += gridDim.z * kSmallM) {
+    const int nt = min(total - m0, kSmallM);
+    const uint4 *xr[2];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int v = (p0 + u * stride) * 4 + t4;
-      const bool in = v < kv;
+    for (int i = 0; i < 2; ++i)
+      xr[i] = i * 8 + g < nt ? x + static_cast<int64_t>(token[m0 + i * 8 + g]) * kv : nullptr;
+    float acc[2][4] = {};
+    for (int p0 = split * kSmallWarps + warp; p0 < pieces; p0 += stride * kUnroll) {
+      uint4 xv[kUnroll][2], av[kUnroll][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) av[u][i] = in && ar[i] != nullptr ? __ldg(ar[i] + v) : zero;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int v = (p0 + u * stride) * 4 + t4;
+        const bool in = v < kv;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xv[u][i] = in && xr[i] != nullptr ? __ldg(xr[i] + v) : zero;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        if (mt == 1 && !two) break;
-        const uint4 &lo = xv[u][2 * mt], &hi = xv[u][2 * mt + 1];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mma_m16n8k16(acc[mt][j], lo.x, hi.x, lo.y, hi.y, av[u][j].x, av[u][j].y);
-          mma_m16n8k16(acc[mt][j], lo.z, hi.z, lo.w, hi.w, av[u][j].z, av[u][j].w);
+        for (int i = 0; i < 2; ++i) {
+          av[u][i] = in && ar[i] != nullptr ? __ldg(ar[i] + v) : zero;
+          xv[u][i] = in && xr[i] != nullptr ? __ldg(xr[i] + v) : zero;
         }
       }
-  }
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mma_m16n8k16(acc[j], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, av[u][j].x, av[u][j].y);
+          mma_m16n8k16(acc[j], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][j].z, av[u][j].w);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) part[warp][mt * 16 + (c >> 1) * 8 + g][j * 8 + t4 * 2 + (c & 1)] = acc[mt][j][c];
-  __syncthreads();
-  for (int i = tid; i < kSmallM * kSmallN; i += kSmallThreads) {
-    const int m = i / kSmallN, n = i - m * kSmallN;
-    float f = 0.0f;
+      for (int c = 0; c < 4; ++c) part[warp][(c >> 1) * 8 + g][j * 8 + t4 * 2 + (c & 1)] = acc[j][c];
+    __syncthreads();
+    {
+      const int m = tid / kSmallN, n = tid - m * kSmallN;  // one sum a thread
+      float f = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w) f += part[w][m][n];
-    red[m][n] = f;
-  }
-  lora_cluster_sync();
-  // 8 columns a thread, the cluster's sums in the order of its CTAs
-  const float sc = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
-  const int i = tid * splits + split, m = i >> 1, c = (i & 1) * 8;
-  if (m < nt && n0 + c < a.rank) {
-    float f[8];
-    cluster_sum8(smem_addr(&red[m][c]), splits, f);
+      for (int w = 0; w < kSmallWarps; ++w) f += part[w][m][n];
+      red[m][n] = f;
+    }
+    lora_cluster_sync();
+    // 8 columns a thread, the cluster's sums in the order of its CTAs
+    const int i = tid * splits + split, m = i >> 1, c = (i & 1) * 8;
+    if (m < nt && n0 + c < a.rank) {
+      float f[8];
+      cluster_sum8(smem_addr(&red[m][c]), splits, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= sc;
-    *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(token[m]) * a.rank + n0 + c) = round8(f);
+      for (int j = 0; j < 8; ++j) f[j] *= sc;
+      *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(token[m0 + m]) * a.rank + n0 + c) = round8(f);
+    }
+    lora_cluster_sync();  // no CTA goes on or leaves while another may still read its sums
   }
-  lora_cluster_sync();  // no CTA leaves while another may still read its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -598,6 +595,7 @@ struct GemmShared {
 };
 
 static_assert(kSmallThreads >= kLBM, "a thread per token");
+static_assert(kSmallThreads == kSmallM * kSmallN, "a thread per sum");
 static_assert(sizeof(GemmShared) <= kLStatic && sizeof(ShrinkShared) <= kLStatic, "");
 
 struct LTile {
@@ -671,8 +669,8 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     prefetch_tensormap(&map_b);
   }
   // With adapters the shrink kernel comes before this one: it let this grid
-  // start only after its own dependency wait, so x is there, and only the
-  // producer waits for it, before its first load of u.
+  // start only after its own dependency wait, so x is there, and only the warp
+  // that loads u waits for it.
   if (warp == 1) {
     tmem_alloc(smem_addr(&sh.tmem), kCols);
     tmem_relinquish();
@@ -689,9 +687,8 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     uint32_t it = 0;
     Ring r;
     int lt = 0;
-    bool ok = true, waited = false;
+    bool ok = true;
     const uint32_t ring = smem_addr(smem), fulls = smem_addr(sh.full);
-    uint32_t uphase = 0;  // tiles whose u was loaded
     // asks for the tile's rows of W or of B_a in stage s
     const auto load_w = [&](const CUtensorMap *map, uint32_t s, int row, int k, int cols) {
       const uint32_t sw = ring + s * a.stage + a.xbytes, fb = fulls + s * 8;
@@ -715,29 +712,8 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
       if (!ok) break;
       const int blocks = sh.count[b] * rblocks;
-      // The first B_a tiles are asked for before the wait for u, as far as the
-      // ring goes: no block of the adapters gives its stage back without u. The
-      // tile's u is loaded once: every CTA reads the same few rows, and once per
-      // adapter (64 tokens, 32 adapters of rank 16) they took 0.7 us a block.
-      bool u_asked = false;
-      const auto load_u = [&]() {
-        if (!waited) grid_dependency_wait();  // u is written
-        waited = true;
-        u_asked = true;
-        ok = warp_wait(&sh.uempty, (uphase & 1u) ^ 1u, abort, a.err);
-        if (!ok) return;
-        ++uphase;
-        if (leader) {
-          mbar_arrive_expect_tx(&sh.ufull, static_cast<uint32_t>(rblocks * a.xrows) * kLRow);
-          for (int q = 0; q < rblocks; ++q)
-            tma_load_2d(ubuf + q * a.xbytes, &map_u, q * kLBK, t.t0, smem_addr(&sh.ufull));
-        }
-        __syncwarp();
-      };
-      int ahead = waited ? 0 : a.stages;  // blocks to ask for before u
-      for (int j = split; ok && j < blocks; j += splits, ++it, r.next(a.stages), --ahead) {
-        if (!u_asked && ahead <= 0) load_u();
-        ok = ok && warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+      for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
+        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
         if (!ok) break;
         if (leader) {
           mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(t.cols) * kLRow);
@@ -745,16 +721,12 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         }
         __syncwarp();
       }
-      if (ok && !u_asked && split < blocks) load_u();
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       __syncwarp();
     }
     grid_dependents_launch();  // what comes next may set itself up during the last products and stores
     // the last loads land before the CTA may exit
-    if (leader) {
-      drain_ring(sh.full, r, it, a.stages);
-      if (uphase > 0) mbar_wait_bounded(&sh.ufull, (uphase - 1) & 1u);
-    }
+    if (leader) drain_ring(sh.full, r, it, a.stages);
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer ----
@@ -866,9 +838,10 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(sh.tempty + buf));
     }
   } else if (a.lora) {
-    // ---- the tile's adapters and the rows that do not use each of them ----
+    // ---- the tile's adapters, the rows that do not use each of them, and u ----
     const int m = tid - 192;
     int lt = 0;
+    uint32_t uphase = 0;  // tiles whose u was loaded
     for (int w = first; w < total; w += stride, ++lt) {
       const int b = lt & 1;
       const LTile t = ltile_of<BN>(w, a);
@@ -882,7 +855,24 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       if (m == 0) sh.count[b] = n;
       bar128<2>();
       if (m == 0) mbar_arrive(smem_addr(sh.lfull + b));
+      // The tile's u is loaded once, as soon as it is there: every CTA reads the
+      // same few rows, and once per adapter (64 tokens, 32 adapters of rank 16)
+      // they took 0.7 us a block.
+      if (warp == 6 && split < n * rblocks) {
+        grid_dependency_wait();  // u is written
+        if (warp_wait(&sh.uempty, (uphase & 1u) ^ 1u, abort, a.err)) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.ufull, static_cast<uint32_t>(rblocks * a.xrows) * kLRow);
+            for (int q = 0; q < rblocks; ++q)
+              tma_load_2d(ubuf + q * a.xbytes, &map_u, q * kLBK, t.t0, smem_addr(&sh.ufull));
+          }
+          __syncwarp();
+          ++uphase;
+        }
+      }
     }
+    // the last load lands before the CTA may exit
+    if (warp == 6 && lane == 0 && uphase > 0) mbar_wait_bounded(&sh.ufull, (uphase - 1) & 1u);
   }
   __syncwarp();
   if constexpr (SPLIT) {
@@ -979,16 +969,18 @@ int ring_stages(int stage, int blocks, int bytes) {
 // whole SM, and the shrink kernel before them need not leave any room.
 constexpr int kShrinkRing = 84 * 1024;
 constexpr int kShrinkRingAlone = 192 * 1024;
-constexpr int kSplitRing = 96 * 1024;
+constexpr int kSplitRing = 84 * 1024;
+constexpr int kSplitRingFew = 128 * 1024;  // up to 8 tokens: their shrink CTAs leave SMs enough
+constexpr int kFewTokens = 8;
 
 moe_status launch_shrink_small(const LoraArgs &a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   if (a.adapters > 0x7fffffff / kLMaxCluster) return MOE_EINVAL;
   const int nchunks = (a.rank + kSmallN - 1) / kSmallN;
-  const int64_t busy = static_cast<int64_t>(a.adapters < a.T ? a.adapters : a.T) * nchunks;  // at most, of 32 tokens each
+  const int64_t busy = static_cast<int64_t>(a.adapters < a.T ? a.adapters : a.T) * nchunks;  // clusters with work, at most
   int splits = kLMaxCluster;
   while (splits > 1 && busy * splits > sms) splits >>= 1;
   const dim3 grid(static_cast<unsigned>(a.adapters * splits), static_cast<unsigned>(nchunks),
-                  static_cast<unsigned>((a.T + kSmallM - 1) / kSmallM));
+                  static_cast<unsigned>((a.T + kSmallTokensPerCta - 1) / kSmallTokensPerCta));
   return launch_cluster(lora_shrink_small_kernel, grid, kSmallThreads, splits, 0, stream, a,
                         static_cast<const uint4 *>(x), static_cast<const uint4 *>(lora_a));
 }
@@ -1036,7 +1028,7 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   const int tail = rblocks * a.xbytes + kLBM * kLRow - a.xbytes;
   // BN 256: four stages, or three beside a u of rank above 64. BN 128: three (with six, which keep the shrink
   // kernel's CTAs off the SM, no block came sooner)
-  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, kSplitRing)
+  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, a.T > kFewTokens ? kSplitRing : kSplitRingFew)
                    : (BN > 128 && rblocks <= 1 ? 4 : 3);
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
   if (tiles > 0x3fffffffll / kLMaxSplit) return MOE_EINVAL;
