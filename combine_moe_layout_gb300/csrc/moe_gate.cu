@@ -133,6 +133,28 @@ __device__ __forceinline__ float load_logit(const void *logits, int64_t i) {
 
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
 
+// The two largest keys of a lane and their slots, of the slots that are not
+// gone; equal keys in slot order. Keys of 0 are no values.
+template <int VPL>
+__device__ __forceinline__ void top_two(const uint32_t (&key)[VPL], uint32_t gone, uint32_t *k1, int *s1, uint32_t *k2,
+                                        int *s2) {
+  uint32_t a = 0, b = 0;
+  int sa = 0, sb = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const uint32_t v = (gone >> i) & 1u ? 0u : key[i];
+    const bool over = v > a, second = v > b;
+    b = over ? a : (second ? v : b);
+    sb = over ? sa : (second ? i : sb);
+    a = over ? v : a;
+    sa = over ? i : sa;
+  }
+  *k1 = a;
+  *s1 = sa;
+  *k2 = b;
+  *s2 = sb;
+}
+
 // Which groups stay, as a bit per group (the same in every lane). The warp's
 // values go through shared memory (gs); lanes_per_group lanes share a group and
 // take its group_top largest one by one.
@@ -244,33 +266,38 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   }
   if (__any_sync(0xffffffffu, nan) && lane == 0) latch_error(a.err, MOE_EINVAL);
 
-  // the k choices, one warp maximum each; lane j keeps choice j
+  // The k choices, one warp maximum each; lane j keeps choice j. Every lane
+  // holds its two largest values (k1 >= k2, the lower slot first among equals);
+  // only the lane that is chosen from moves on, and looks through its values
+  // again when both are gone. `gone` marks the slots it has given.
+  uint32_t gone = 0, k1, k2;
+  int s1, s2;
+  top_two<VPL>(key, gone, &k1, &s1, &k2, &s2);
   int my_e = -1;
-  float my_l = -INFINITY;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, k1);
     if (top == 0) break;  // nothing left
-    int cand = 0x7fffffff;
-#pragma unroll
-    for (int i = VPL - 1; i >= 0; --i)
-      if (key[i] == top) cand = expert_of(i, lane);
-    const int e = __reduce_min_sync(0xffffffffu, cand);
-    float lv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (expert_of(i, lane) == e) {
-        lv = l[i];
-        key[i] = 0;
-      }
-    lv = __shfl_sync(0xffffffffu, lv, (e >> 2) & 31);
-    if (lane == j) {
-      my_e = e;
-      my_l = lv;
+    unsigned holders = __ballot_sync(0xffffffffu, k1 == top);
+    int e = expert_of(s1, lane);
+    if (holders & (holders - 1)) {  // equal values in several lanes: the lowest expert
+      const int low = __reduce_min_sync(0xffffffffu, k1 == top ? e : 0x7fffffff);
+      holders = __ballot_sync(0xffffffffu, k1 == top && e == low);
     }
+    const int owner = __ffs(holders) - 1;
+    e = __shfl_sync(0xffffffffu, e, owner);
+    if (lane == j) my_e = e;
+    bool empty = false;
+    if (lane == owner) {
+      gone |= 1u << s1;
+      k1 = k2;
+      s1 = s2;
+      k2 = 0;
+      empty = k1 == 0;
+    }
+    if (__any_sync(0xffffffffu, empty)) top_two<VPL>(key, gone, &k1, &s1, &k2, &s2);
   }
+  float my_l = -INFINITY;
+  if (my_e >= 0) my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
 
   float w = 0.0f;
   if (a.sigmoid) {
@@ -360,14 +387,32 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
 #pragma unroll
     for (int i = 0; i < VPL; ++i) out[i] = -total * (l[i] * inv);
   }
-  if (my_e < 0) d = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(0xffffffffu, my_e, j);
-    const float dj = __shfl_sync(0xffffffffu, d, j);
-    if (e < 0) continue;
+  // the choices' terms, through the warp's row in shared memory (comparing every value with every choice cost as
+  // much as the rest of the kernel)
+  __shared__ __align__(16) float rows[kGateWarps][VPL * 32];
+  float *row = rows[warp];
+  int *mark = reinterpret_cast<int *>(row);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (expert_of(i, lane) == e) out[i] += dj;
+  for (int p = 0; p < VPL / 4; ++p) *reinterpret_cast<float4 *>(row + (p * 32 + lane) * 4) = make_float4(0, 0, 0, 0);
+  __syncwarp();
+  if (my_e >= 0) mark[my_e] = lane;
+  __syncwarp();
+  const bool twice = my_e >= 0 && mark[my_e] != lane;  // an expert named by two entries: their terms add up, in order
+  const bool any_twice = __any_sync(0xffffffffu, twice);
+  if (my_e >= 0) row[my_e] = any_twice ? 0.0f : d;
+  __syncwarp();
+  if (any_twice)
+    for (int j = 0; j < a.k; ++j) {
+      if (lane == j && my_e >= 0) row[my_e] += d;
+      __syncwarp();
+    }
+#pragma unroll
+  for (int p = 0; p < VPL / 4; ++p) {
+    const float4 v = *reinterpret_cast<const float4 *>(row + (p * 32 + lane) * 4);
+    out[4 * p] += v.x;
+    out[4 * p + 1] += v.y;
+    out[4 * p + 2] += v.z;
+    out[4 * p + 3] += v.w;
   }
   const int64_t base = t * a.E;
 #pragma unroll
