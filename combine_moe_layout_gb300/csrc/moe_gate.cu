@@ -52,14 +52,6 @@ struct GateArgs {
   float scale;
 };
 
-// Order-preserving key of a float (larger float, larger key), 0 for "not
-// available" (-inf). -0 and +0 share a key.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (!(v > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -112,11 +104,8 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, i
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (v[c] != v[c]) {
-        *nan = true;
-        v[c] = -INFINITY;
-      }
-      l[4 * p + c] = fminf(v[c], FLT_MAX);
+      *nan |= v[c] != v[c];
+      l[4 * p + c] = fminf(fmaxf(v[c], -INFINITY), FLT_MAX);  // fmaxf of a NaN and -inf is -inf
     }
   }
 }
@@ -133,62 +122,89 @@ __device__ __forceinline__ float load_logit(const void *logits, int64_t i) {
 
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// The two largest keys of a lane and their slots, of the slots that are not
-// gone; equal keys in slot order. Keys of 0 are no values.
-template <int VPL>
-__device__ __forceinline__ void top_two(const uint32_t (&key)[VPL], uint32_t gone, uint32_t *k1, int *s1, uint32_t *k2,
-                                        int *s2) {
-  uint32_t a = 0, b = 0;
-  int sa = 0, sb = 0;
+// Sorts a lane's values, largest first: Batcher's odd-even merge sort.
+template <int N>
+__device__ __forceinline__ void sort_down(float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const uint32_t v = (gone >> i) & 1u ? 0u : key[i];
-    const bool over = v > a, second = v > b;
-    b = over ? a : (second ? v : b);
-    sb = over ? sa : (second ? i : sb);
-    a = over ? v : a;
-    sa = over ? i : sa;
-  }
-  *k1 = a;
-  *s1 = sa;
-  *k2 = b;
-  *s2 = sb;
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        const int first = q % p;
+        if (x >= first && (x - first) % (2 * q) < q && x + q < N && x / (2 * p) == (x + q) / (2 * p)) {
+          const float hi = fmaxf(v[x], v[x + q]), lo = fminf(v[x], v[x + q]);
+          v[x] = hi;
+          v[x + q] = lo;
+        }
+      }
+}
+
+// The largest v of the warp.
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Place of expert e's value among the warp's values in shared memory: a word
+// between the groups keeps equal members of different groups in different banks.
+__device__ __forceinline__ int group_of(const GateArgs &a, int e) {
+  return static_cast<int>(e * a.group_magic >> 32);
 }
 
 // Which groups stay, as a bit per group (the same in every lane). The warp's
-// values go through shared memory (gs); lanes_per_group lanes share a group and
-// take its group_top largest one by one.
+// values go through shared memory (gs); lanes_per_group lanes share a group.
 __device__ __forceinline__ uint32_t kept_groups(const GateArgs &a, const float *gs, int lane) {
   const int lpg = a.lanes_per_group;
   const int grp = lane / lpg, sub = lane - grp * lpg;
   const bool live = grp < a.groups;
-  const float *v = gs + grp * a.group_size;
-  uint64_t taken = 0;  // bit i: value sub + i * lpg (fewer than 64 for 1024 experts)
+  const float *v = gs + grp * (a.group_size + 1);
   float score = 0.0f;
   int found = 0;
-  for (int r = 0; r < a.top; ++r) {
-    float best = -INFINITY;
-    int bi = a.group_size;
-    if (live)
-      for (int i = 0, x = sub; x < a.group_size; ++i, x += lpg)
-        if (!((taken >> i) & 1ull) && v[x] > best) {
-          best = v[x];
-          bi = x;
-        }
-    for (int o = lpg >> 1; o > 0; o >>= 1) {
-      const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (ob > best || (ob == best && oi < bi)) {
-        best = ob;
-        bi = oi;
+  if (a.top <= 2) {  // the usual sizes in one pass: the two largest, lane by lane and then across the group's lanes
+    float b1 = -INFINITY, b2 = -INFINITY;
+    if (live) {
+#pragma unroll 8
+      for (int x = sub; x < a.group_size; x += lpg) {
+        const float y = v[x];
+        b2 = fmaxf(b2, fminf(b1, y));
+        b1 = fmaxf(b1, y);
       }
     }
-    if (best > -INFINITY) {  // members that are not available add nothing
-      score += best;
-      ++found;
+    for (int o = lpg >> 1; o > 0; o >>= 1) {
+      const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+      b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+      b1 = fmaxf(b1, o1);
     }
-    const int d = bi - sub;
-    if (bi < a.group_size && d >= 0 && d % lpg == 0) taken |= 1ull << (d / lpg);
+    found = b1 > -INFINITY;
+    score = a.top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+  } else {  // group_top largest one by one
+    uint64_t taken = 0;  // bit i: value sub + i * lpg (fewer than 64 for 1024 experts)
+    for (int r = 0; r < a.top; ++r) {
+      float best = -INFINITY;
+      int bi = a.group_size;
+      if (live)
+        for (int i = 0, x = sub; x < a.group_size; ++i, x += lpg)
+          if (!((taken >> i) & 1ull) && v[x] > best) {
+            best = v[x];
+            bi = x;
+          }
+      for (int o = lpg >> 1; o > 0; o >>= 1) {
+        const float ob = __shfl_xor_sync(0xffffffffu, best, o);
+        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
+        if (ob > best || (ob == best && oi < bi)) {
+          best = ob;
+          bi = oi;
+        }
+      }
+      if (best > -INFINITY) {  // members that are not available add nothing
+        score += best;
+        ++found;
+      }
+      const int d = bi - sub;
+      if (bi < a.group_size && d >= 0 && d % lpg == 0) taken |= 1ull << (d / lpg);
+    }
   }
   if (!live || found == 0) score = -INFINITY;
   int rank = 0;
@@ -204,7 +220,7 @@ __device__ __forceinline__ uint32_t kept_groups(const GateArgs &a, const float *
 
 template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
-  extern __shared__ float gate_sm[];  // [warps][E], with groups only
+  extern __shared__ float gate_sm[];  // [warps][E + groups], with groups only
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   grid_dependency_wait();
@@ -216,31 +232,20 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   load_row<VPL, BF16, VEC>(a.logits, t, a.E, lane, l, &nan);
 
   float mx = -INFINITY, sum = 1.0f;
-  if (!a.sigmoid) {
+  if (!a.sigmoid && (!a.renorm || a.bias != nullptr || a.groups > 1)) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i]);
     mx = warp_max(mx);
     if (mx == -INFINITY) mx = 0.0f;  // nothing available: every score is 0
-    if (!a.renorm || a.bias != nullptr || a.groups > 1) {
-      sum = 0.0f;
+    sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += expf(l[i] - mx);
-      sum = warp_sum(sum);
-      if (sum == 0.0f) sum = 1.0f;
-    }
+    for (int i = 0; i < VPL; ++i) sum += expf(l[i] - mx);
+    sum = warp_sum(sum);
+    if (sum == 0.0f) sum = 1.0f;
   }
 
-  uint32_t key[VPL];
-  if (a.bias == nullptr && (a.groups <= 1 || a.top == 1)) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = order_key(l[i]);
-    if (a.groups > 1) {
-      float *gs = gate_sm + warp * a.E;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (expert_of(i, lane) < a.E) gs[expert_of(i, lane)] = l[i];
-    }
-  } else {
+  // the values that choose: the logits, or the scores with their bias
+  if (a.bias != nullptr || (a.groups > 1 && a.top > 1)) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = expert_of(i, lane);
@@ -253,51 +258,94 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
           s = -INFINITY;
         }
       }
-      if (a.groups > 1 && e < a.E) gate_sm[warp * a.E + e] = s;
-      key[i] = order_key(a.bias != nullptr ? s : l[i]);
+      if (a.groups > 1 && e < a.E) gate_sm[warp * (a.E + a.groups) + e + group_of(a, e)] = s;
+      if (a.bias != nullptr) l[i] = s;
+    }
+  } else if (a.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = expert_of(i, lane);
+      if (e < a.E) gate_sm[warp * (a.E + a.groups) + e + group_of(a, e)] = l[i];
     }
   }
   if (a.groups > 1) {
     __syncwarp();
-    const uint32_t kept = kept_groups(a, gate_sm + warp * a.E, lane);
+    const uint32_t kept = kept_groups(a, gate_sm + warp * (a.E + a.groups), lane);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (!((kept >> ((expert_of(i, lane) * a.group_magic >> 32) & 31u)) & 1u)) key[i] = 0;
+      if (!((kept >> (group_of(a, expert_of(i, lane)) & 31)) & 1u)) l[i] = -INFINITY;
   }
   if (__any_sync(0xffffffffu, nan) && lane == 0) latch_error(a.err, MOE_EINVAL);
 
-  // The k choices, one warp maximum each; lane j keeps choice j. Every lane
-  // holds its two largest values (k1 >= k2, the lower slot first among equals);
-  // only the lane that is chosen from moves on, and looks through its values
-  // again when both are gone. `gone` marks the slots it has given.
-  uint32_t gone = 0, k1, k2;
-  int s1, s2;
-  top_two<VPL>(key, gone, &k1, &s1, &k2, &s2);
-  int my_e = -1;
-  for (int j = 0; j < a.k; ++j) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, k1);
-    if (top == 0) break;  // nothing left
-    unsigned holders = __ballot_sync(0xffffffffu, k1 == top);
-    int e = expert_of(s1, lane);
-    if (holders & (holders - 1)) {  // equal values in several lanes: the lowest expert
-      const int low = __reduce_min_sync(0xffffffffu, k1 == top ? e : 0x7fffffff);
-      holders = __ballot_sync(0xffffffffu, k1 == top && e == low);
+  // T, the k-th largest (equal ones counted), and how many are larger than T
+  float head[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) head[i] = l[i];
+  sort_down<VPL>(head);
+  float T = INFINITY;
+  int count = 0, over = 0;  // heads taken so far, values > T
+  while (count < a.k) {
+    const float top = redux_max(head[0]);
+    if (top == -INFINITY) break;  // nothing left: all that is available is chosen
+    if (top < T) over = count;    // (a lane may hold equals of T one after the other)
+    T = top;
+    const bool mine = head[0] == top;
+    count += __popc(__ballot_sync(0xffffffffu, mine));
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) head[i] = head[i + 1];
+      head[VPL - 1] = -INFINITY;
     }
-    const int owner = __ffs(holders) - 1;
-    e = __shfl_sync(0xffffffffu, e, owner);
-    if (lane == j) my_e = e;
-    bool empty = false;
-    if (lane == owner) {
-      gone |= 1u << s1;
-      k1 = k2;
-      s1 = s2;
-      k2 = 0;
-      empty = k1 == 0;
-    }
-    if (__any_sync(0xffffffffu, empty)) top_two<VPL>(key, gone, &k1, &s1, &k2, &s2);
   }
-  float my_l = -INFINITY;
-  if (my_e >= 0) my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
+  uint32_t pick = 0;  // this lane's chosen slots
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (l[i] >= T && l[i] > -INFINITY) pick |= 1u << i;
+  count = __reduce_add_sync(0xffffffffu, __popc(pick));  // (a lane's equals of T behind its head were not counted)
+  if (count > a.k) {  // more equals of T than places: the lowest experts of them
+    uint32_t equal = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (l[i] == T) equal |= 1u << i;
+    pick &= ~equal;
+    for (int r = over; r < a.k; ++r) {
+      const int e = equal != 0 ? expert_of(__ffs(equal) - 1, lane) : 0x7fffffff;
+      if (__reduce_min_sync(0xffffffffu, e) == e && equal != 0) {
+        pick |= equal & (0u - equal);
+        equal &= equal - 1;
+      }
+    }
+    count = a.k;
+  }
+  // the chosen experts, one to a lane
+  __shared__ int chosen[kGateWarps][kMaxTopk];
+  for (int base = 0; base < count;) {
+    const unsigned have = __ballot_sync(0xffffffffu, pick != 0);
+    if (have == 0) break;
+    if (pick != 0) {
+      const int at = base + __popc(have & ((1u << lane) - 1u));
+      if (at < kMaxTopk) chosen[warp][at] = expert_of(__ffs(pick) - 1, lane);
+      pick &= pick - 1;
+    }
+    base += __popc(have);
+  }
+  __syncwarp();
+  int my_e = -1;
+  float my_l = -INFINITY, my_v = -INFINITY;
+  if (lane < count) {
+    my_e = chosen[warp][lane];
+    my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
+    my_v = my_l;
+    if (a.bias != nullptr) my_v = (a.sigmoid ? sigmoid_of(my_l) : expf(my_l - mx) / sum) + __ldg(a.bias + my_e);
+  }
+  // and their places: largest first, the lower expert first among equals
+  int place = lane;
+  if (lane < count) place = 0;
+  for (int j = 0; j < count; ++j) {
+    const float v = __shfl_sync(0xffffffffu, my_v, j);
+    const int e = __shfl_sync(0xffffffffu, my_e, j);
+    if (lane < count && (v > my_v || (v == my_v && e < my_e))) ++place;
+  }
 
   float w = 0.0f;
   if (a.sigmoid) {
@@ -315,8 +363,8 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
     w = expf(my_l - mx) / sum;
   }
   if (lane < a.k) {
-    a.idx[t * a.k + lane] = my_e;
-    a.weights[t * a.k + lane] = w * a.scale;
+    a.idx[t * a.k + place] = my_e;
+    a.weights[t * a.k + place] = w * a.scale;
   }
 }
 
@@ -454,8 +502,8 @@ moe_status launch_gate_v(const GateArgs &a, bool bf16, bool vec, bool grad, cuda
   if (blocks > 0x7fffffffll) return MOE_EINVAL;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kGateWarps * 32, 1, 1);
-  // at most 8 warps x 1024 experts x 4 bytes = 32 KB
-  cfg.dynamicSmemBytes = !grad && a.groups > 1 ? static_cast<size_t>(kGateWarps) * a.E * sizeof(float) : 0;
+  // at most 8 warps x (1024 experts + 32 groups) x 4 bytes = 33 KB
+  cfg.dynamicSmemBytes = !grad && a.groups > 1 ? static_cast<size_t>(kGateWarps) * (a.E + a.groups) * sizeof(float) : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   use_pdl(cfg, attr);
