@@ -64,14 +64,24 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The larger of two values, NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// +inf counts as the largest finite value in the scores (the limit of both).
+__device__ __forceinline__ float finite(float l) { return fminf(l, FLT_MAX); }
+
 // Expert of value i of a lane: four neighbours per lane and pass.
 __device__ __forceinline__ int expert_of(int i, int lane) { return ((i >> 2) * 32 + lane) * 4 + (i & 3); }
 
-// A lane's logits of a row. NaN counts as -inf (and is reported), +inf as the
-// largest finite value (the limit of both scores).
+// A lane's logits of a row. NaN counts as -inf (and is reported).
 template <int VPL, bool BF16, bool VEC>
 __device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, int lane, float (&l)[VPL], bool *nan) {
   const int64_t base = t * E;
+  float worst = -INFINITY;
 #pragma unroll
   for (int p = 0; p < VPL / 4; ++p) {
     const int e0 = (p * 32 + lane) * 4;
@@ -102,12 +112,11 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, i
             v[c] = static_cast<const float *>(logits)[base + e0 + c];
         }
     }
+    worst = max_nan(worst, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      *nan |= v[c] != v[c];
-      l[4 * p + c] = fminf(fmaxf(v[c], -INFINITY), FLT_MAX);  // fmaxf of a NaN and -inf is -inf
-    }
+    for (int c = 0; c < 4; ++c) l[4 * p + c] = fmaxf(v[c], -INFINITY);  // -inf for a NaN
   }
+  *nan = worst != worst;
 }
 
 template <bool BF16>
@@ -117,14 +126,19 @@ __device__ __forceinline__ float load_logit(const void *logits, int64_t i) {
     v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(logits)[i]) << 16);
   else
     v = static_cast<const float *>(logits)[i];
-  return v != v ? -INFINITY : fminf(v, FLT_MAX);
+  return fmaxf(v, -INFINITY);
 }
 
-__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }  // 1 for +inf
+
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
 
 // Sorts a lane's values, largest first: Batcher's odd-even merge sort.
-template <int N>
-__device__ __forceinline__ void sort_down(float (&v)[N]) {
+template <int N, class V>
+__device__ __forceinline__ void sort_down(V (&v)[N]) {
 #pragma unroll
   for (int p = 1; p < N; p *= 2)
 #pragma unroll
@@ -133,7 +147,7 @@ __device__ __forceinline__ void sort_down(float (&v)[N]) {
       for (int x = 0; x < N; ++x) {
         const int first = q % p;
         if (x >= first && (x - first) % (2 * q) < q && x + q < N && x / (2 * p) == (x + q) / (2 * p)) {
-          const float hi = fmaxf(v[x], v[x + q]), lo = fminf(v[x], v[x + q]);
+          const V hi = larger(v[x], v[x + q]), lo = smaller(v[x], v[x + q]);
           v[x] = hi;
           v[x + q] = lo;
         }
@@ -234,12 +248,12 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   float mx = -INFINITY, sum = 1.0f;
   if (!a.sigmoid && (!a.renorm || a.bias != nullptr || a.groups > 1)) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i]);
+    for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, finite(l[i]));
     mx = warp_max(mx);
     if (mx == -INFINITY) mx = 0.0f;  // nothing available: every score is 0
     sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += expf(l[i] - mx);
+    for (int i = 0; i < VPL; ++i) sum += expf(finite(l[i]) - mx);
     sum = warp_sum(sum);
     if (sum == 0.0f) sum = 1.0f;
   }
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
       const int e = expert_of(i, lane);
       float s = -INFINITY;
       if (e < a.E && l[i] > -INFINITY) {
-        s = a.sigmoid ? sigmoid_of(l[i]) : expf(l[i] - mx) / sum;
+        s = a.sigmoid ? sigmoid_of(l[i]) : expf(finite(l[i]) - mx) / sum;
         if (a.bias != nullptr) s += __ldg(a.bias + e);
         if (s != s) {
           nan = true;
@@ -277,75 +291,157 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   }
   if (__any_sync(0xffffffffu, nan) && lane == 0) latch_error(a.err, MOE_EINVAL);
 
-  // T, the k-th largest (equal ones counted), and how many are larger than T
-  float head[VPL];
+  // the score of a logit as the choice sees it
+  const auto choosing = [&](float logit, int e) {
+    if (a.bias == nullptr) return logit;
+    return (a.sigmoid ? sigmoid_of(logit) : expf(finite(logit) - mx) / sum) + __ldg(a.bias + e);
+  };
+  int my_e = -1, place = lane;
+  float my_l = -INFINITY;
+  if (BF16 && a.bias == nullptr) {
+    // bf16 values leave room for their expert in one 32-bit key: the value's
+    // order above, the expert counted down below, so that no two are equal
+    uint32_t head[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) head[i] = l[i];
-  sort_down<VPL>(head);
-  float T = INFINITY;
-  int count = 0, over = 0;  // heads taken so far, values > T
-  while (count < a.k) {
-    const float top = redux_max(head[0]);
-    if (top == -INFINITY) break;  // nothing left: all that is available is chosen
-    if (top < T) over = count;    // (a lane may hold equals of T one after the other)
-    T = top;
-    const bool mine = head[0] == top;
-    count += __popc(__ballot_sync(0xffffffffu, mine));
-    if (mine) {
-#pragma unroll
-      for (int i = 0; i + 1 < VPL; ++i) head[i] = head[i + 1];
-      head[VPL - 1] = -INFINITY;
+    for (int i = 0; i < VPL; ++i) {
+      const uint32_t u = __float_as_uint(l[i] + 0.0f);  // -0 as +0
+      const uint32_t order = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+      head[i] = l[i] > -INFINITY ? (order & 0xffff0000u) | (0xffffu - expert_of(i, lane)) : 0u;
     }
-  }
-  uint32_t pick = 0;  // this lane's chosen slots
+    sort_down<VPL>(head);
+    uint32_t key = 0;
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, head[0]);
+      if (top == 0) break;  // nothing left
+      if (lane == j) key = top;
+      const bool from = head[0] == top;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (l[i] >= T && l[i] > -INFINITY) pick |= 1u << i;
-  count = __reduce_add_sync(0xffffffffu, __popc(pick));  // (a lane's equals of T behind its head were not counted)
-  if (count > a.k) {  // more equals of T than places: the lowest experts of them
-    uint32_t equal = 0;
+      for (int i = 0; i < VPL; ++i) head[i] = from ? (i + 1 < VPL ? head[i + 1] : 0u) : head[i];
+    }
+    if (key != 0) {
+      my_e = static_cast<int>(0xffffu - (key & 0xffffu));
+      const uint32_t order = key & 0xffff0000u;
+      my_l = __uint_as_float((order & 0x80000000u) != 0 ? order ^ 0x80000000u : ~(order | 0xffffu));  // a bf16 value's low half is 0
+    }
+  } else {
+    // The largest head of the sorted lists, k times; lane j keeps the j-th largest
+    // value. Of each list only the first kDepth values move up (a +inf stands for
+    // what is behind them): that a lane holds more of the k, or that two values
+    // are equal, is found out and left to the slow way below.
+    constexpr int kDepth = VPL < 4 ? VPL : 4;
+    float head[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (l[i] == T) equal |= 1u << i;
-    pick &= ~equal;
-    for (int r = over; r < a.k; ++r) {
-      const int e = equal != 0 ? expert_of(__ffs(equal) - 1, lane) : 0x7fffffff;
-      if (__reduce_min_sync(0xffffffffu, e) == e && equal != 0) {
-        pick |= equal & (0u - equal);
-        equal &= equal - 1;
+    for (int i = 0; i < VPL; ++i) head[i] = l[i];
+    sort_down<VPL>(head);
+    float keep[kDepth];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) keep[i] = head[i];
+    const float behind = VPL > kDepth && head[VPL > kDepth ? kDepth : 0] > -INFINITY ? INFINITY : -INFINITY;
+    float mine = -INFINITY, T = INFINITY;
+    unsigned equal_heads = 0;
+    bool slow = false;
+    int count = 0;
+    for (; count < a.k; ++count) {
+      const float top = redux_max(keep[0]);
+      if (!(fabsf(top) < INFINITY)) {
+        slow = top > 0.0f;  // else nothing is left
+        break;
+      }
+      const bool from = keep[0] == top;
+      const unsigned holders = __ballot_sync(0xffffffffu, from);
+      equal_heads |= holders & (holders - 1);
+      slow |= top == T;
+      if (lane == count) mine = top;
+      T = top;
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) keep[i] = from ? (i + 1 < kDepth ? keep[i + 1] : behind) : keep[i];
+    }
+    slow |= equal_heads != 0 || __any_sync(0xffffffffu, count > 0 && keep[0] >= T);
+
+    __shared__ int chosen[kGateWarps][kMaxTopk];
+    if (!slow) {
+      // what is not below T, up to one value of every lane at a time: a value's place is the number of larger ones
+      uint32_t pick = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (l[i] >= T) pick |= 1u << i;
+      while (__any_sync(0xffffffffu, pick != 0)) {
+        const int e = expert_of(__ffs(pick) - 1, lane);
+        float v = INFINITY;
+        if (pick != 0) v = choosing(load_logit<BF16>(a.logits, t * a.E + e), e);
+        int at = 0;
+#pragma unroll
+        for (int step = kMaxTopk / 2; step > 0; step /= 2)
+          if (__shfl_sync(0xffffffffu, mine, at + step - 1) > v) at += step;
+        if (pick != 0) chosen[warp][at] = e;
+        pick &= pick - 1;
+      }
+      __syncwarp();
+      if (lane < count) {
+        my_e = chosen[warp][lane];
+        my_l = a.bias == nullptr ? mine : load_logit<BF16>(a.logits, t * a.E + my_e);
+      }
+    } else {
+      // any values: T with its equals counted, the lowest experts among them, and the order by comparing
+      int over = 0;  // values > T
+      T = INFINITY;
+      for (count = 0; count < a.k;) {
+        const float top = redux_max(head[0]);
+        if (top == -INFINITY) break;
+        if (top < T) over = count;  // (a lane may hold equals of T one after the other)
+        T = top;
+        const bool from = head[0] == top;
+        count += __popc(__ballot_sync(0xffffffffu, from));
+        if (from) {
+#pragma unroll
+          for (int i = 0; i + 1 < VPL; ++i) head[i] = head[i + 1];
+          head[VPL - 1] = -INFINITY;
+        }
+      }
+      uint32_t pick = 0, equal = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (l[i] >= T) pick |= 1u << i;
+        if (l[i] == T) equal |= 1u << i;
+      }
+      count = __reduce_add_sync(0xffffffffu, __popc(pick));  // (a lane's equals of T behind its head were not counted)
+      if (count > a.k) {
+        pick &= ~equal;
+        for (int r = over; r < a.k; ++r) {
+          const int e = equal != 0 ? expert_of(__ffs(equal) - 1, lane) : 0x7fffffff;
+          if (__reduce_min_sync(0xffffffffu, e) == e && equal != 0) {
+            pick |= equal & (0u - equal);
+            equal &= equal - 1;
+          }
+        }
+        count = a.k;
+      }
+      for (int base = 0; base < count;) {
+        const unsigned have = __ballot_sync(0xffffffffu, pick != 0);
+        if (have == 0) break;
+        if (pick != 0) {
+          const int at = base + __popc(have & ((1u << lane) - 1u));
+          if (at < kMaxTopk) chosen[warp][at] = expert_of(__ffs(pick) - 1, lane);
+          pick &= pick - 1;
+        }
+        base += __popc(have);
+      }
+      __syncwarp();
+      float my_v = -INFINITY;
+      if (lane < count) {
+        my_e = chosen[warp][lane];
+        my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
+        my_v = choosing(my_l, my_e);
+        place = 0;
+      }
+      for (int j = 0; j < count; ++j) {
+        const float v = __shfl_sync(0xffffffffu, my_v, j);
+        const int e = __shfl_sync(0xffffffffu, my_e, j);
+        if (lane < count && (v > my_v || (v == my_v && e < my_e))) ++place;
       }
     }
-    count = a.k;
   }
-  // the chosen experts, one to a lane
-  __shared__ int chosen[kGateWarps][kMaxTopk];
-  for (int base = 0; base < count;) {
-    const unsigned have = __ballot_sync(0xffffffffu, pick != 0);
-    if (have == 0) break;
-    if (pick != 0) {
-      const int at = base + __popc(have & ((1u << lane) - 1u));
-      if (at < kMaxTopk) chosen[warp][at] = expert_of(__ffs(pick) - 1, lane);
-      pick &= pick - 1;
-    }
-    base += __popc(have);
-  }
-  __syncwarp();
-  int my_e = -1;
-  float my_l = -INFINITY, my_v = -INFINITY;
-  if (lane < count) {
-    my_e = chosen[warp][lane];
-    my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
-    my_v = my_l;
-    if (a.bias != nullptr) my_v = (a.sigmoid ? sigmoid_of(my_l) : expf(my_l - mx) / sum) + __ldg(a.bias + my_e);
-  }
-  // and their places: largest first, the lower expert first among equals
-  int place = lane;
-  if (lane < count) place = 0;
-  for (int j = 0; j < count; ++j) {
-    const float v = __shfl_sync(0xffffffffu, my_v, j);
-    const int e = __shfl_sync(0xffffffffu, my_e, j);
-    if (lane < count && (v > my_v || (v == my_v && e < my_e))) ++place;
-  }
+  my_l = finite(my_l);
 
   float w = 0.0f;
   if (a.sigmoid) {
@@ -385,7 +481,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
       my_e = -1;
     } else {
       g = a.gw[t * a.k + lane] * a.scale;
-      my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
+      my_l = finite(load_logit<BF16>(a.logits, t * a.E + my_e));
     }
   }
   float out[VPL];
@@ -419,7 +515,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
     load_row<VPL, BF16, VEC>(a.logits, t, a.E, lane, l, &nan);
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i]);
+    for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i] = finite(l[i]));
     mx = warp_max(mx);
     if (mx == -INFINITY) mx = 0.0f;
     float sum = 0.0f;

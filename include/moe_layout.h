@@ -412,7 +412,8 @@ typedef struct {
  *   sum when renormalize (0 where that sum is 0).
  * An expert whose logit (or s + bias) is -inf is never chosen; when fewer than k
  * are left the remaining entries are -1 with weight 0, the masked choices of
- * moe_layout and moe_sort. A logit of +inf counts as the largest finite float.
+ * moe_layout and moe_sort. A logit of +inf counts as the largest finite float in
+ * the scores.
  *   logits [R][T][E] float or bfloat16; bias [E] float or NULL (read);
  *   topk_idx [R][T][k] int32, topk_weights [R][T][k] float (written).
  * E at most 1024. Host errors: MOE_EINVAL (also keep_groups * E / num_groups < k,
