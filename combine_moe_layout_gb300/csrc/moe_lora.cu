@@ -15,8 +15,9 @@
 //
 // Two kernels:
 //   lora_shrink_kernel  u[t] = s_a x[t] A_a^T. A tile is 128 tokens against the
-//     stacked rows of up to 256 / rank adapters that occur among them: a token's
-//     own columns are picked in the epilogue. in is split over a cluster of CTAs whose partial sums meet in
+//     stacked rows of up to 128 / rank adapters that occur among them (or one
+//     adapter's, if it has more): a token's own columns are picked in the
+//     epilogue. in is split over a cluster of CTAs whose partial sums meet in
 //     distributed shared memory in a fixed order.
 //   lora_gemm_kernel    the projection with its extra K blocks. Tiles of 128
 //     tokens x BN outputs; TMA brings x and W (then u and B_a) tiles, one lane
@@ -47,7 +48,7 @@ constexpr int kLStatic = 8192;      // room for a kernel's static shared memory
 constexpr int kLBytesPerCol = 228 * 1024 / 512;  // shared memory that goes with one tensor-memory column
 constexpr int kShrinkThreads = 192;
 constexpr int kGemmLThreads = 320;
-constexpr int kShrinkCols = 256;    // adapter rows of a shrink tile
+constexpr int kShrinkCols = 128;    // adapter rows of a shrink tile (or one adapter's, if it has more)
 constexpr int kLMaxCluster = 8;    // of the shrink kernel
 constexpr int kLMaxSplit = 4;      // of the projection
 
@@ -60,9 +61,10 @@ struct LoraArgs {
   int T, K, N, rank, adapters;
   int xrows;           // rows of an x box (a multiple of 8, at most 128)
   int xbytes;          // bytes of an x tile in a stage (a multiple of 1024)
-  int stage, stages;   // bytes and number of the ring's stages
+  int stage, stages;   // bytes and number of the ring's stages (shrink: the most of them)
   int kblocks;
   // shrink
+  int ring;              // bytes of the ring
   int per_pass, groups;  // adapters of one pass over K, and the CTAs that share a tile's passes
   uint32_t cols;         // tensor-memory columns
   // projection
@@ -373,6 +375,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
   const int rows = min(kLBM, a.T - t0), vecs = a.rank / 8;
   float *red = reinterpret_cast<float *>(smem);  // [128][rank]: this split's sums, once the ring is idle
+  // the ring as this tile's adapters fill it: most tiles of prompts have one or two, and more stages for it
+  const int stage = a.xbytes + ((min(sh.n, a.per_pass) * a.rank + 15) & ~15) * kLRow;
+  const int stages = min(a.stages, a.ring / stage);
   Ring r;
   uint32_t it = 0, ph = 0;
 
@@ -381,10 +386,10 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const int nact = min(sh.n - first, a.per_pass);
     if (warp == 0) {
       const uint32_t bytes = static_cast<uint32_t>(a.xrows + nact * a.rank) * kLRow;
-      for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(a.stages)) {
+      for (int kb = kb0; kb < kb1; ++kb, ++it, r.next(stages)) {
         if (!warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err)) break;
         if (leader) {
-          const uint32_t sx = smem_addr(smem) + r.s * a.stage, sa = sx + a.xbytes, fb = smem_addr(sh.full) + r.s * 8;
+          const uint32_t sx = smem_addr(smem) + r.s * stage, sa = sx + a.xbytes, fb = smem_addr(sh.full) + r.s * 8;
           mbar_arrive_expect_tx(sh.full + r.s, bytes);
           tma_load_2d(sx, &map_x, kb * kLBK, t0, fb);
           for (int i = 0; i < nact; ++i)
@@ -392,14 +397,14 @@ __global__ void __launch_bounds__(kShrinkThreads)
         }
         __syncwarp();
       }
-      if (leader) drain_ring(sh.full, r, it, a.stages);
+      if (leader) drain_ring(sh.full, r, it, stages);
       __syncwarp();
     } else if (warp == 1) {
       const uint32_t idesc = idesc_bf16(kLBM, (nact * a.rank + 15) & ~15);
-      const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
+      const uint32_t xlo = desc_lo(smem_addr(smem)), step = stage >> 4, xstep = a.xbytes >> 4;
       const uint32_t empty = smem_addr(sh.empty);
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, r.next(a.stages)) {
+      for (int kb = kb0; kb < kb1; ++kb, r.next(stages)) {
         ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
         if (!ok) break;
         tc_fence_after();
@@ -964,11 +969,9 @@ int ring_stages(int stage, int blocks, int bytes) {
   return n < 3 ? 3 : n;
 }
 
-// Rings of CTAs that are to share an SM: a shrink CTA and one of the
-// projection, or two of the projection. The projection's 256-wide tiles take a
-// whole SM, and the shrink kernel before them need not leave any room.
+// Rings of CTAs that are to share an SM: two shrink CTAs, one and a CTA of the
+// projection, or two of the projection.
 constexpr int kShrinkRing = 84 * 1024;
-constexpr int kShrinkRingAlone = 192 * 1024;
 constexpr int kSplitRing = 84 * 1024;
 constexpr int kSplitRingFew = 128 * 1024;  // up to 8 tokens: their shrink CTAs leave SMs enough
 constexpr int kFewTokens = 8;
@@ -985,27 +988,28 @@ moe_status launch_shrink_small(const LoraArgs &a, const void *x, const void *lor
                         static_cast<const uint4 *>(x), static_cast<const uint4 *>(lora_a));
 }
 
-moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, bool alone, cudaStream_t stream) {
+moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   if (a.T <= kLBM) return launch_shrink_small(a, x, lora_a, sms, stream);
   const int most = a.adapters < a.T ? (a.adapters < kLBM ? a.adapters : kLBM) : (a.T < kLBM ? a.T : kLBM);
+  // up to two CTAs an SM (8192 tokens: the whole call takes 184 us so, 189 us with one)
   int splits = kLMaxCluster;
-  while (splits > 1 && (a.mtiles * splits > sms || splits > a.kblocks)) splits >>= 1;
+  while (splits > 1 && (a.mtiles * splits > 2 * sms || splits > a.kblocks)) splits >>= 1;
   // few tokens: their adapters are spread over the SMs that are left
   const int spread = sms / (a.mtiles * splits) > 1 ? sms / (a.mtiles * splits) : 1;
   a.per_pass = (most + spread - 1) / spread;
-  if (a.per_pass > kShrinkCols / a.rank) a.per_pass = kShrinkCols / a.rank;
+  if (a.per_pass > kShrinkCols / a.rank) a.per_pass = a.rank > kShrinkCols ? 1 : kShrinkCols / a.rank;
   a.groups = (most + a.per_pass - 1) / a.per_pass;
   if (a.groups > spread) a.groups = spread;
   int n = (a.per_pass * a.rank + 15) & ~15;
   a.cols = 32;
   while (static_cast<int>(a.cols) < n) a.cols <<= 1;
-  // the adapters' rows end on whole 1024-byte swizzle groups, and the MMA's last
-  // 16-row step may read one group past them
-  a.stage = a.xbytes + n * kLRow;
-  a.stages = ring_stages(a.stage, (a.kblocks + splits - 1) / splits, alone ? kShrinkRingAlone : kShrinkRing);
+  // room for two stages of the widest tile; narrower ones have up to kLMaxStages
+  a.ring = 2 * (a.xbytes + n * kLRow);
+  if (a.ring < kShrinkRing) a.ring = kShrinkRing;
+  a.stages = kLMaxStages;
   // the products take 128 rows from the x tile's place also where the tile has
   // fewer: what follows it inside the allocation is read then
-  int smem = 1024 + a.stages * a.stage + kLBM * kLRow - a.xbytes;
+  int smem = 1024 + a.ring + kLBM * kLRow - a.xbytes;
   const int red = 1024 + kLBM * a.rank * 4;
   if (smem < red) smem = red;
   smem = with_columns(smem, static_cast<int>(a.cols));
@@ -1097,7 +1101,7 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
   a.mtiles = (T + kLBM - 1) / kLBM;
   const int64_t tiles256 = static_cast<int64_t>(a.mtiles) * ((N + 255) / 256);
   if (a.lora) {
-    const moe_status st = launch_shrink(a, x, lora_a, sms, tiles256 >= sms, cs);
+    const moe_status st = launch_shrink(a, x, lora_a, sms, cs);
     if (st != MOE_OK) return st;
   }
   const int64_t tiles128 = static_cast<int64_t>(a.mtiles) * ((N + 127) / 128);

@@ -87,6 +87,7 @@ def check(T, K, N, r, A, mix, seed=0, scales=True, num_sms=0):
     (1, 512, 512, 8, 1), (1, 4096, 4096, 16, 8), (2, 8, 8, 8, 3), (5, 72, 136, 24, 2), (31, 1000, 264, 64, 40),
     (64, 7168, 2048, 16, 32), (65, 200, 520, 40, 5), (127, 640, 384, 128, 7), (128, 512, 256, 256, 4),
     (129, 512, 256, 8, 200), (300, 328, 1032, 72, 9), (389, 2056, 4104, 24, 12), (513, 128, 4096, 16, 3),
+    (200, 136, 264, 256, 5), (260, 1032, 72, 128, 30), (1000, 64, 128, 8, 1000), (16, 4096, 14336, 32, 3),
 ])
 def test_against_the_formula(T, K, N, r, A, mix):
     check(T, K, N, r, A, mix)
