@@ -1,9 +1,13 @@
-"""One dispatch/combine step through the C ABI, with torch for device memory.
+"""Steps through the C ABI, with torch for device memory.
 
 ``MoeStep`` owns the device buffers of one problem size and runs
 layout -> dispatch -> experts -> combine on a stream. The experts are the
 synthetic ones of the workloads: identity for bf16 steps (combine reads the
 receive buffer itself) and ``moe_expert_stub`` for fp8 steps.
+
+``LocalMoe`` is an MoE layer of one device that is no part of an EP group: router,
+token sort, expert stage and the way back, the gradients of all but the experts,
+and a projection shared by all requests with each request's low-rank adapter.
 """
 from __future__ import annotations
 
@@ -138,3 +142,86 @@ class MoeStep:
 
     def error(self, stream=None) -> int:
         return B.moe_get_error(self.buf.err, stream)
+
+
+class LocalMoe:
+    """An MoE layer of one device.
+
+    forward: logits -> moe_gate -> moe_sort -> expert stage -> moe_unsort. backward takes the gradient of the
+    output back through moe_unsort_grad, the caller's expert gradient, moe_sort_grad and moe_gate_grad. shared runs
+    the projection beside the experts with the adapters of the batch's requests. Every buffer is allocated once.
+
+    tokens x hidden bf16 rows, num_experts experts of width inter (a multiple of 128 when the expert stage runs)."""
+
+    def __init__(self, tokens: int, hidden: int, num_experts: int, topk: int, opts: B.MoeGateOpts, device="cuda",
+                 inter: int = 0):
+        self.desc = B.MoeDesc(1, tokens, hidden, num_experts, topk, max(tokens, 1), B.MOE_BF16, 0)
+        self.opts, self.inter = opts, inter
+        n, dev = tokens * topk, torch.device(device)
+
+        def rows(count, width):
+            return torch.empty((count, width), dtype=torch.bfloat16, device=dev)
+
+        def ints(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=dev)
+
+        self.topk_idx, self.tok_packed = ints(tokens, topk), ints(tokens, topk)
+        self.region_offsets = ints(num_experts + 1)
+        self.topk_weights = torch.empty((tokens, topk), device=dev)
+        self.packed_x, self.packed_y, self.out = rows(n, hidden), rows(n, hidden), rows(tokens, hidden)
+        self.h = rows(n, inter) if inter else None
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.grad_y, self.grad_x = None, None  # allocated by the first backward
+        self.u = self.shared_out = None        # by the first shared
+
+    def route(self, logits, bias=None, stream=None):
+        B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err, stream)
+
+    def sort(self, x, stream=None):
+        B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed,
+                   self.err, stream)
+
+    def experts(self, weights, stream=None):
+        """The expert stage on the sorted rows (weights: workloads.ExpertWeights)."""
+        B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up,
+                             self.h, self.err, stream)
+        B.moe_expert_down(self.desc, self.inter, self.region_offsets, self.h, weights.w_down, self.packed_y, self.err,
+                          stream)
+
+    def unsort(self, stream=None):
+        B.moe_unsort(self.desc, self.packed_y, self.tok_packed, self.topk_weights, self.out, self.err, stream)
+        return self.out
+
+    def forward(self, x, logits, weights, bias=None, stream=None):
+        """x [tokens][hidden], logits [tokens][num_experts] -> the routed experts' output [tokens][hidden]."""
+        self.route(logits, bias, stream)
+        self.sort(x, stream)
+        self.experts(weights, stream)
+        return self.unsort(stream)
+
+    def backward(self, grad_out, logits, expert_grad, stream=None):
+        """The gradients of x and of the logits. expert_grad(packed_x, region_offsets, grad_y) is the caller's
+        gradient of the experts: from the gradient of packed_y to that of packed_x, row by row."""
+        if self.grad_y is None:
+            self.grad_y, self.grad_x = torch.zeros_like(self.packed_y), torch.empty_like(self.out)
+            self.grad_weights, self.grad_logits = torch.empty_like(self.topk_weights), torch.empty_like(logits)
+        B.moe_unsort_grad(self.desc, self.packed_y, self.tok_packed, self.topk_weights, grad_out, self.grad_y,
+                          self.grad_weights, self.err, stream)
+        grad_packed = expert_grad(self.packed_x, self.region_offsets, self.grad_y)
+        B.moe_sort_grad(self.desc, grad_packed, self.tok_packed, self.grad_x, self.err, stream)
+        B.moe_gate_grad(self.desc, self.opts, logits, self.topk_idx, self.grad_weights, self.grad_logits, self.err,
+                        stream)
+        return self.grad_x, self.grad_logits
+
+    def shared(self, x, w, lora_a, lora_b, scales, adapter, stream=None):
+        """x w^T [tokens][out] with each token's adapter beside it (moe_lora_linear)."""
+        A, rank, _ = lora_a.shape
+        if self.u is None:
+            self.u = torch.empty((x.shape[0], rank), dtype=torch.bfloat16, device=x.device)
+            self.shared_out = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
+        desc = B.MoeLoraDesc(x.shape[0], x.shape[1], w.shape[0], rank, A, 0)
+        B.moe_lora_linear(desc, x, w, lora_a, lora_b, scales, adapter, self.u, self.shared_out, self.err, stream)
+        return self.shared_out
+
+    def error(self, stream=None) -> int:
+        return B.moe_get_error(self.err, stream)
