@@ -84,7 +84,11 @@ __device__ __forceinline__ uint32_t lora_cluster_size() {
   return r;
 }
 
+// The cluster barrier, the named barriers and the tensor-memory loads below are
+// instructions of a whole warp: a warp that comes from a branch or a loop that
+// its lanes left at different times is brought together first.
 __device__ __forceinline__ void lora_cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -129,6 +133,7 @@ __device__ __forceinline__ void cluster_sum8(uint32_t saddr, int ctas, float (&f
 
 template <int ID>
 __device__ __forceinline__ void bar128() {
+  __syncwarp();
   asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
 }
 
@@ -136,6 +141,7 @@ __device__ __forceinline__ void bar128() {
 template <int ID>
 __device__ __forceinline__ bool bar128_and(bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
@@ -150,6 +156,7 @@ __device__ __forceinline__ bool bar128_and(bool v) {
 // 8 consecutive fp32 accumulator columns of this thread's row.
 __device__ __forceinline__ void tmem_load8_wait(uint32_t taddr, float (&f)[8]) {
   uint32_t r[8];
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
@@ -338,10 +345,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int group = item / a.mtiles, mt = item - group * a.mtiles;
   const int t0 = mt * kLBM;
 
-  if (warp == 1) {
-    tmem_alloc(smem_addr(&sh.tmem), a.cols);
-    tmem_relinquish();
-  }
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(sh.full + s, 1);
@@ -355,10 +358,17 @@ __global__ void __launch_bounds__(kShrinkThreads)
     prefetch_tensormap(&map_a);
   }
   grid_dependency_wait();
-  // the projection's CTAs may come: they find what this kernel's predecessors wrote, and by the rule on shared
-  // memory they leave every CTA of this kernel its tensor memory
+  // The projection's CTAs may come: they find what this kernel's predecessors wrote, and by the rule on shared
+  // memory they leave every CTA of this kernel its tensor memory. (The projection in turn lets nothing start before
+  // it ends: with the next call's shrink kernel beside a projection of several 128-wide tiles a CTA, calls of 2500
+  // tokens and 520 inputs faulted, for a reason that reading did not show.)
   grid_dependents_launch();
   int slot = -1;
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&sh.tmem), a.cols);
+    tmem_relinquish();
+  }
   if (warp >= 2) {
     bool bad = false;
     const int n = tile_adapters<1>(a, t0, tid - 64, sh.scratch, sh.list, &slot, &bad);
@@ -369,6 +379,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  __syncwarp();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const bool leader = elect_one();  // used by warps 0 and 1
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
@@ -462,6 +473,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     tc_fence_after();
   }
   __syncthreads();
+  __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, a.cols);
 }
 
@@ -676,6 +688,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   // With adapters the shrink kernel comes before this one: it let this grid
   // start only after its own dependency wait, so x is there, and only the warp
   // that loads u waits for it.
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(smem_addr(&sh.tmem), kCols);
     tmem_relinquish();
@@ -729,7 +742,6 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       __syncwarp();
     }
-    grid_dependents_launch();  // what comes next may set itself up during the last products and stores
     // the last loads land before the CTA may exit
     if (leader) drain_ring(sh.full, r, it, a.stages);
     __syncwarp();
@@ -825,11 +837,11 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         __nv_bfloat16 *row = a.y + static_cast<int64_t>(valid ? t.t0 + m : 0) * a.N + t.n0;
         for (int c = 0; c < t.cols; c += 32) {
           uint32_t r[32];
+          __syncwarp();
           tmem_load32_wait(tb + c, r);
-          if (!valid) continue;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            if (t.n0 + c + v * 8 < a.N) {
+            if (valid && t.n0 + c + v * 8 < a.N) {
               float f[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[v * 8 + j]);
@@ -903,6 +915,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
@@ -1022,6 +1035,38 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
   return launch_cluster(lora_shrink_kernel, dim3(static_cast<unsigned>(grid)), kShrinkThreads, splits, smem, stream, mx, ma, a);
 }
 
+// The projection's tiles: their width and the CTAs that share one's K, by the
+// time they are expected to take: waves of CTAs x K blocks of one x the time of
+// a block (measured beside other CTAs: 0.20, 0.30 and 0.33 us for 64, 128 and
+// 256 outputs; a wide tile has more products for the bytes that it loads), then
+// the sum over a cluster (3 us), and what the last tile's stores take, with,
+// for 256-wide tiles, the shrink kernel that their CTAs have to let finish
+// first (1.2 and 5 us). Only 256-wide tiles come several to a CTA. Widths of 64
+// only pay where 128 tokens or fewer leave SMs idle. Measured against 128-wide tiles throughout: 1500 tokens 4096 ->
+// 2048 41 to 36.5 us, 700 tokens 4104 -> 2056 31 to 29 us; against 256-wide
+// ones: 389 tokens 2056 -> 4104 23.6 to 20.6 us.
+int tile_width(const LoraArgs &a, int sms, int *splits) {
+  constexpr int kWidths[3] = {64, 128, 256};
+  constexpr int kBlockNs[3] = {200, 300, 330}, kEndNs[3] = {1200, 1200, 5000};
+  constexpr int kSumNs = 3000;
+  int64_t best = INT64_MAX;
+  int width = 256;
+  *splits = 1;
+  for (int i = 0; i < 3; ++i)
+    for (int s = 1; s <= kLMaxSplit; s *= 2) {
+      if (s > a.kblocks || (kWidths[i] == 64 && (a.mtiles > 1 || s == 1))) continue;
+      const int64_t ctas = static_cast<int64_t>(a.mtiles) * ((a.N + kWidths[i] - 1) / kWidths[i]) * s;
+      if ((s > 1 || kWidths[i] < 256) && ctas > sms) continue;
+      const int64_t ns = (ctas + sms - 1) / sms * ((a.kblocks + s - 1) / s) * kBlockNs[i] + kEndNs[i] + (s > 1 ? kSumNs : 0);
+      if (ns < best) {
+        best = ns;
+        width = kWidths[i];
+        *splits = s;
+      }
+    }
+  return width;
+}
+
 template <int BN, bool SPLIT>
 moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lora_b, int splits, int sms,
                        cudaStream_t stream) {
@@ -1030,10 +1075,11 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   const int rblocks = a.lora ? (a.rank + kLBK - 1) / kLBK : 0;
   // what follows the ring: u, and the rest of the 128 rows of x that the products take (as in the shrink kernel)
   const int tail = rblocks * a.xbytes + kLBM * kLRow - a.xbytes;
-  // BN 256: four stages, or three beside a u of rank above 64. BN 128: three (with six, which keep the shrink
-  // kernel's CTAs off the SM, no block came sooner)
-  a.stages = SPLIT ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, a.T > kFewTokens ? kSplitRing : kSplitRingFew)
-                   : (BN > 128 && rblocks <= 1 ? 4 : 3);
+  // BN 256: four stages, or three beside a u of rank above 64. BN 128 over whole tiles: three (with six, which keep
+  // the shrink kernel's CTAs off the SM, no block came sooner)
+  a.stages = BN > 128 ? (rblocks <= 1 ? 4 : 3)
+             : SPLIT  ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, a.T > kFewTokens ? kSplitRing : kSplitRingFew)
+                      : 3;
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
   if (tiles > 0x3fffffffll / kLMaxSplit) return MOE_EINVAL;
   a.whole = a.total = static_cast<int>(tiles);
@@ -1099,21 +1145,18 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
   a.xbytes = a.xrows * kLRow;
   a.kblocks = (K + kLBK - 1) / kLBK;
   a.mtiles = (T + kLBM - 1) / kLBM;
-  const int64_t tiles256 = static_cast<int64_t>(a.mtiles) * ((N + 255) / 256);
   if (a.lora) {
     const moe_status st = launch_shrink(a, x, lora_a, sms, cs);
     if (st != MOE_OK) return st;
   }
-  const int64_t tiles128 = static_cast<int64_t>(a.mtiles) * ((N + 127) / 128);
-  const int64_t tiles64 = static_cast<int64_t>(a.mtiles) * ((N + 63) / 64);
-  if (tiles256 >= sms) return launch_gemm<256, false>(a, x, w, lora_b, 1, sms, cs);
-  // Fewer tiles than SMs: in is split over clusters of up to 4 CTAs (of 8, the
-  // last of 16 clusters found no place until another had ended), and where that
-  // is still too few the tiles are 64 outputs wide.
-  int splits = kLMaxSplit;
-  while (splits > 1 && (tiles128 * splits > sms || splits > a.kblocks)) splits >>= 1;
-  if (splits == kLMaxSplit && tiles64 * splits <= sms)
-    return launch_gemm<64, true>(a, x, w, lora_b, splits, sms, cs);
+  int splits = 1;
+  switch (tile_width(a, sms, &splits)) {
+    case 256:
+      return splits > 1 ? launch_gemm<256, true>(a, x, w, lora_b, splits, sms, cs)
+                        : launch_gemm<256, false>(a, x, w, lora_b, 1, sms, cs);
+    case 64: return launch_gemm<64, true>(a, x, w, lora_b, splits, sms, cs);
+    default: break;
+  }
   if (splits > 1) return launch_gemm<128, true>(a, x, w, lora_b, splits, sms, cs);
   return launch_gemm<128, false>(a, x, w, lora_b, 1, sms, cs);
 }
