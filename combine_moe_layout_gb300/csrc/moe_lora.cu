@@ -359,9 +359,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   grid_dependency_wait();
   // The projection's CTAs may come: they find what this kernel's predecessors wrote, and by the rule on shared
-  // memory they leave every CTA of this kernel its tensor memory. (The projection in turn lets nothing start before
-  // it ends: with the next call's shrink kernel beside a projection of several 128-wide tiles a CTA, calls of 2500
-  // tokens and 520 inputs faulted, for a reason that reading did not show.)
+  // memory they leave every CTA of this kernel its tensor memory. (A projection of several tiles a CTA in turn lets
+  // nothing start before it ends: with this kernel, which then claimed tensor memory before its wait, beside one of
+  // 128-wide tiles, calls of 2500 tokens and 520 inputs faulted, for a reason that reading did not show.)
   grid_dependents_launch();
   int slot = -1;
   __syncwarp();
@@ -742,6 +742,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       __syncwarp();
     }
+    if (SPLIT) grid_dependents_launch();  // what comes next may be on its way during the last products and sums
     // the last loads land before the CTA may exit
     if (leader) drain_ring(sh.full, r, it, a.stages);
     __syncwarp();
