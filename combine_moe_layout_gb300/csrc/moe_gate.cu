@@ -291,154 +291,112 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   }
   if (__any_sync(0xffffffffu, nan) && lane == 0) latch_error(a.err, MOE_EINVAL);
 
-  // the score of a logit as the choice sees it
-  const auto choosing = [&](float logit, int e) {
-    if (a.bias == nullptr) return logit;
-    return (a.sigmoid ? sigmoid_of(logit) : expf(finite(logit) - mx) / sum) + __ldg(a.bias + e);
-  };
-  int my_e = -1, place = lane;
+  // Most rows: keys that hold a value's order above and, in their last bits, its
+  // expert counted down, so that no two are equal. A lane's keys are sorted, and
+  // the largest head of the 32 lists is taken k times: the experts in their
+  // order. bf16 values lose nothing to the expert's bits; others may agree in
+  // all bits above them (about 1 row in 200 of N(0, 1) logits at 256 experts),
+  // which shows in neighbours of the chosen and goes the slow way.
+  constexpr uint32_t kExperts = VPL * 32 - 1;  // the expert's bits
+  int my_e = -1, place = lane, count = 0;
   float my_l = -INFINITY;
-  if (BF16 && a.bias == nullptr) {
-    // bf16 values leave room for their expert in one 32-bit key: the value's
-    // order above, the expert counted down below, so that no two are equal
+  bool slow = false;
+  {
     uint32_t head[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const uint32_t u = __float_as_uint(l[i] + 0.0f);  // -0 as +0
       const uint32_t order = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-      head[i] = l[i] > -INFINITY ? (order & 0xffff0000u) | (0xffffu - expert_of(i, lane)) : 0u;
+      head[i] = l[i] > -INFINITY ? (order & ~kExperts) | (kExperts - expert_of(i, lane)) : 0u;
     }
     sort_down<VPL>(head);
-    uint32_t key = 0;
-    for (int j = 0; j < a.k; ++j) {
+    uint32_t key = 0, last = 0;
+    for (; count < a.k; ++count) {
       const uint32_t top = __reduce_max_sync(0xffffffffu, head[0]);
       if (top == 0) break;  // nothing left
-      if (lane == j) key = top;
+      slow |= (top ^ last) <= kExperts;
+      last = top;
+      if (lane == count) key = top;
       const bool from = head[0] == top;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) head[i] = from ? (i + 1 < VPL ? head[i + 1] : 0u) : head[i];
     }
-    if (key != 0) {
-      my_e = static_cast<int>(0xffffu - (key & 0xffffu));
-      const uint32_t order = key & 0xffff0000u;
-      my_l = __uint_as_float((order & 0x80000000u) != 0 ? order ^ 0x80000000u : ~(order | 0xffffu));  // a bf16 value's low half is 0
-    }
+    if (key != 0) my_e = static_cast<int>(kExperts - (key & kExperts));
+    if (BF16 && a.bias == nullptr)
+      slow = false;
+    else
+      slow |= __any_sync(0xffffffffu, head[0] != 0 && (head[0] ^ last) <= kExperts);
+  }
+  if (!slow) {
+    if (my_e >= 0) my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
   } else {
-    // The largest head of the sorted lists, k times; lane j keeps the j-th largest
-    // value. Of each list only the first kDepth values move up (a +inf stands for
-    // what is behind them): that a lane holds more of the k, or that two values
-    // are equal, is found out and left to the slow way below.
-    constexpr int kDepth = VPL < 4 ? VPL : 4;
+    // the score of a logit as the choice sees it
+    const auto choosing = [&](float logit, int e) {
+      if (a.bias == nullptr) return logit;
+      return (a.sigmoid ? sigmoid_of(logit) : expf(finite(logit) - mx) / sum) + __ldg(a.bias + e);
+    };
+    __shared__ int chosen[kGateWarps][kMaxTopk];
     float head[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) head[i] = l[i];
     sort_down<VPL>(head);
-    float keep[kDepth];
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) keep[i] = head[i];
-    const float behind = VPL > kDepth && head[VPL > kDepth ? kDepth : 0] > -INFINITY ? INFINITY : -INFINITY;
-    float mine = -INFINITY, T = INFINITY;
-    unsigned equal_heads = 0;
-    bool slow = false;
-    int count = 0;
-    for (; count < a.k; ++count) {
-      const float top = redux_max(keep[0]);
-      if (!(fabsf(top) < INFINITY)) {
-        slow = top > 0.0f;  // else nothing is left
-        break;
-      }
-      const bool from = keep[0] == top;
-      const unsigned holders = __ballot_sync(0xffffffffu, from);
-      equal_heads |= holders & (holders - 1);
-      slow |= top == T;
-      if (lane == count) mine = top;
+    my_e = -1;
+    // any values: T with its equals counted, the lowest experts among them, and the order by comparing
+    int over = 0;  // values > T
+    float T = INFINITY;
+    for (count = 0; count < a.k;) {
+      const float top = redux_max(head[0]);
+      if (top == -INFINITY) break;
+      if (top < T) over = count;  // (a lane may hold equals of T one after the other)
       T = top;
+      const bool from = head[0] == top;
+      count += __popc(__ballot_sync(0xffffffffu, from));
+      if (from) {
 #pragma unroll
-      for (int i = 0; i < kDepth; ++i) keep[i] = from ? (i + 1 < kDepth ? keep[i + 1] : behind) : keep[i];
+        for (int i = 0; i + 1 < VPL; ++i) head[i] = head[i + 1];
+        head[VPL - 1] = -INFINITY;
+      }
     }
-    slow |= equal_heads != 0 || __any_sync(0xffffffffu, count > 0 && keep[0] >= T);
-
-    __shared__ int chosen[kGateWarps][kMaxTopk];
-    if (!slow) {
-      // what is not below T, up to one value of every lane at a time: a value's place is the number of larger ones
-      uint32_t pick = 0;
+    uint32_t pick = 0, equal = 0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (l[i] >= T) pick |= 1u << i;
-      while (__any_sync(0xffffffffu, pick != 0)) {
-        const int e = expert_of(__ffs(pick) - 1, lane);
-        float v = INFINITY;
-        if (pick != 0) v = choosing(load_logit<BF16>(a.logits, t * a.E + e), e);
-        int at = 0;
-#pragma unroll
-        for (int step = kMaxTopk / 2; step > 0; step /= 2)
-          if (__shfl_sync(0xffffffffu, mine, at + step - 1) > v) at += step;
-        if (pick != 0) chosen[warp][at] = e;
+    for (int i = 0; i < VPL; ++i) {
+      if (l[i] >= T) pick |= 1u << i;
+      if (l[i] == T) equal |= 1u << i;
+    }
+    count = __reduce_add_sync(0xffffffffu, __popc(pick));  // (a lane's equals of T behind its head were not counted)
+    if (count > a.k) {
+      pick &= ~equal;
+      for (int r = over; r < a.k; ++r) {
+        const int e = equal != 0 ? expert_of(__ffs(equal) - 1, lane) : 0x7fffffff;
+        if (__reduce_min_sync(0xffffffffu, e) == e && equal != 0) {
+          pick |= equal & (0u - equal);
+          equal &= equal - 1;
+        }
+      }
+      count = a.k;
+    }
+    for (int base = 0; base < count;) {
+      const unsigned have = __ballot_sync(0xffffffffu, pick != 0);
+      if (have == 0) break;
+      if (pick != 0) {
+        const int at = base + __popc(have & ((1u << lane) - 1u));
+        if (at < kMaxTopk) chosen[warp][at] = expert_of(__ffs(pick) - 1, lane);
         pick &= pick - 1;
       }
-      __syncwarp();
-      if (lane < count) {
-        my_e = chosen[warp][lane];
-        my_l = a.bias == nullptr ? mine : load_logit<BF16>(a.logits, t * a.E + my_e);
-      }
-    } else {
-      // any values: T with its equals counted, the lowest experts among them, and the order by comparing
-      int over = 0;  // values > T
-      T = INFINITY;
-      for (count = 0; count < a.k;) {
-        const float top = redux_max(head[0]);
-        if (top == -INFINITY) break;
-        if (top < T) over = count;  // (a lane may hold equals of T one after the other)
-        T = top;
-        const bool from = head[0] == top;
-        count += __popc(__ballot_sync(0xffffffffu, from));
-        if (from) {
-#pragma unroll
-          for (int i = 0; i + 1 < VPL; ++i) head[i] = head[i + 1];
-          head[VPL - 1] = -INFINITY;
-        }
-      }
-      uint32_t pick = 0, equal = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (l[i] >= T) pick |= 1u << i;
-        if (l[i] == T) equal |= 1u << i;
-      }
-      count = __reduce_add_sync(0xffffffffu, __popc(pick));  // (a lane's equals of T behind its head were not counted)
-      if (count > a.k) {
-        pick &= ~equal;
-        for (int r = over; r < a.k; ++r) {
-          const int e = equal != 0 ? expert_of(__ffs(equal) - 1, lane) : 0x7fffffff;
-          if (__reduce_min_sync(0xffffffffu, e) == e && equal != 0) {
-            pick |= equal & (0u - equal);
-            equal &= equal - 1;
-          }
-        }
-        count = a.k;
-      }
-      for (int base = 0; base < count;) {
-        const unsigned have = __ballot_sync(0xffffffffu, pick != 0);
-        if (have == 0) break;
-        if (pick != 0) {
-          const int at = base + __popc(have & ((1u << lane) - 1u));
-          if (at < kMaxTopk) chosen[warp][at] = expert_of(__ffs(pick) - 1, lane);
-          pick &= pick - 1;
-        }
-        base += __popc(have);
-      }
-      __syncwarp();
-      float my_v = -INFINITY;
-      if (lane < count) {
-        my_e = chosen[warp][lane];
-        my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
-        my_v = choosing(my_l, my_e);
-        place = 0;
-      }
-      for (int j = 0; j < count; ++j) {
-        const float v = __shfl_sync(0xffffffffu, my_v, j);
-        const int e = __shfl_sync(0xffffffffu, my_e, j);
-        if (lane < count && (v > my_v || (v == my_v && e < my_e))) ++place;
-      }
+      base += __popc(have);
+    }
+    __syncwarp();
+    float my_v = -INFINITY;
+    if (lane < count) {
+      my_e = chosen[warp][lane];
+      my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
+      my_v = choosing(my_l, my_e);
+      place = 0;
+    }
+    for (int j = 0; j < count; ++j) {
+      const float v = __shfl_sync(0xffffffffu, my_v, j);
+      const int e = __shfl_sync(0xffffffffu, my_e, j);
+      if (lane < count && (v > my_v || (v == my_v && e < my_e))) ++place;
     }
   }
   my_l = finite(my_l);

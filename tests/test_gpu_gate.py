@@ -194,6 +194,23 @@ def test_close_and_saturated_logits_keep_their_order():
     assert status == B.MOE_OK and idx[0].tolist() == [5, 11, 10, 9] and w[0].tolist() == [1.0, 0.0, 0.0, 0.0]
 
 
+def test_values_that_differ_in_their_last_bits_only():
+    """fp32 logits that agree in all but the lowest few bits, among the chosen, across the k-th place and below it, and
+    many equal ones: the order is still the logits', ties to the lowest expert."""
+    require_gpu()
+    for E in (40, 256, 700, 1024):
+        g = torch.Generator().manual_seed(E)
+        l = torch.randn((60, E), generator=g)
+        base = torch.tensor([3.0, -0.5])[torch.arange(60) % 2]
+        near = (base[:, None].view(-1, 1).expand(60, 12).contiguous().view(torch.int32)
+                + torch.randint(0, 6, (60, 12), generator=g, dtype=torch.int32)).view(torch.float32)
+        at = torch.argsort(torch.rand((60, E), generator=g), 1)[:, :12]
+        l.scatter_(1, at, near)
+        l[::2] = torch.where(torch.rand((30, E), generator=g) < 0.3, l[::2], torch.full_like(l[::2], -4.0))
+        for k in (1, 5, 16):
+            check(l.cuda(), opts("sigmoid", True), k)
+
+
 @pytest.mark.parametrize("groups", [0, 4])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_bias_selects_and_does_not_weigh(score, groups):
