@@ -52,22 +52,16 @@ struct GateArgs {
   float scale;
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The larger of two values, NaN if either is one.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest of three values, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -112,11 +106,15 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, i
             v[c] = static_cast<const float *>(logits)[base + e0 + c];
         }
     }
-    worst = max_nan(worst, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])));
+    worst = max_nan(max_nan(worst, v[0], v[1]), v[2], v[3]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) l[4 * p + c] = fmaxf(v[c], -INFINITY);  // -inf for a NaN
+    for (int c = 0; c < 4; ++c) l[4 * p + c] = v[c];
   }
   *nan = worst != worst;
+  if (*nan) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = fmaxf(l[i], -INFINITY);  // -inf for a NaN
+  }
 }
 
 template <bool BF16>
@@ -152,6 +150,30 @@ __device__ __forceinline__ void sort_down(V (&v)[N]) {
           v[x + q] = lo;
         }
       }
+}
+
+// The D largest of a lane's values, largest first: fours are sorted, and two
+// sorted lists of four are joined by taking the larger of opposite ends, which
+// are the four largest as a bitonic sequence, and sorting that.
+template <int N, int D>
+__device__ __forceinline__ void largest_of(const uint32_t (&v)[N], uint32_t (&head)[D]) {
+  static_assert(D == 4 && N % 4 == 0, "lists of four");
+#pragma unroll
+  for (int b = 0; b < N; b += 4) {
+    uint32_t q[4] = {v[b], v[b + 1], v[b + 2], v[b + 3]};
+    sort_down<4>(q);
+    if (b == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) head[i] = q[i];
+      continue;
+    }
+    const uint32_t b0 = max(head[0], q[3]), b1 = max(head[1], q[2]), b2 = max(head[2], q[1]), b3 = max(head[3], q[0]);
+    const uint32_t a0 = max(b0, b2), a2 = min(b0, b2), a1 = max(b1, b3), a3 = min(b1, b3);
+    head[0] = max(a0, a1);
+    head[1] = min(a0, a1);
+    head[2] = max(a2, a3);
+    head[3] = min(a2, a3);
+  }
 }
 
 // The largest v of the warp.
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   if (!a.sigmoid && (!a.renorm || a.bias != nullptr || a.groups > 1)) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, finite(l[i]));
-    mx = warp_max(mx);
+    mx = redux_max(mx);
     if (mx == -INFINITY) mx = 0.0f;  // nothing available: every score is 0
     sum = 0.0f;
 #pragma unroll
@@ -292,40 +314,47 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   if (__any_sync(0xffffffffu, nan) && lane == 0) latch_error(a.err, MOE_EINVAL);
 
   // Most rows: keys that hold a value's order above and, in their last bits, its
-  // expert counted down, so that no two are equal. A lane's keys are sorted, and
-  // the largest head of the 32 lists is taken k times: the experts in their
-  // order. bf16 values lose nothing to the expert's bits; others may agree in
-  // all bits above them (about 1 row in 200 of N(0, 1) logits at 256 experts),
-  // which shows in neighbours of the chosen and goes the slow way.
+  // expert counted down, so that no two are equal. A lane keeps its four largest
+  // keys in order, and the largest head of the 32 lists is taken k times: the
+  // experts in their order. bf16 values lose nothing to the expert's bits; others
+  // may agree in all bits above them (about 1 row in 200 of N(0, 1) logits at 256
+  // experts), which shows in neighbours of the chosen and goes the slow way, as
+  // does a row with four of its chosen experts in one lane that holds more.
   constexpr uint32_t kExperts = VPL * 32 - 1;  // the expert's bits
-  int my_e = -1, place = lane, count = 0;
+  constexpr uint32_t kNone = 0x007fffffu;      // the largest key of -inf
+  int my_e = -1, place = lane;
   float my_l = -INFINITY;
   bool slow = false;
   {
-    uint32_t head[VPL];
+    uint32_t keys[VPL], head[4];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const uint32_t u = __float_as_uint(l[i] + 0.0f);  // -0 as +0
       const uint32_t order = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-      head[i] = l[i] > -INFINITY ? (order & ~kExperts) | (kExperts - expert_of(i, lane)) : 0u;
+      keys[i] = (order & ~kExperts) | (kExperts - expert_of(i, lane));
     }
-    sort_down<VPL>(head);
+    largest_of(keys, head);
     uint32_t key = 0, last = 0;
-    for (; count < a.k; ++count) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, head[0]);
-      if (top == 0) break;  // nothing left
-      slow |= (top ^ last) <= kExperts;
-      last = top;
-      if (lane == count) key = top;
-      const bool from = head[0] == top;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) head[i] = from ? (i + 1 < VPL ? head[i + 1] : 0u) : head[i];
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+      last = __reduce_max_sync(0xffffffffu, head[0]);
+      if (lane == j) key = last;
+      if (head[0] == last) {
+        head[0] = head[1];
+        head[1] = head[2];
+        head[2] = head[3];
+        head[3] = 0;
+      }
     }
-    if (key != 0) my_e = static_cast<int>(kExperts - (key & kExperts));
-    if (BF16 && a.bias == nullptr)
-      slow = false;
-    else
-      slow |= __any_sync(0xffffffffu, head[0] != 0 && (head[0] ^ last) <= kExperts);
+    if (key > kNone) my_e = static_cast<int>(kExperts - (key & kExperts));
+    // a chosen value too near to the one before it or to the best of those left, or a lane that ran out
+    if (!BF16 || a.bias != nullptr) {
+      const uint32_t before = __shfl_up_sync(0xffffffffu, key, 1);
+      slow = (lane > 0 && key > kNone && (key ^ before) <= kExperts) ||
+             (head[0] > kNone && (head[0] ^ last) <= kExperts);
+    }
+    if (VPL > 4) slow |= head[0] == 0;
+    slow = __any_sync(0xffffffffu, slow);
   }
   if (!slow) {
     if (my_e >= 0) my_l = load_logit<BF16>(a.logits, t * a.E + my_e);
@@ -342,9 +371,9 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
     sort_down<VPL>(head);
     my_e = -1;
     // any values: T with its equals counted, the lowest experts among them, and the order by comparing
-    int over = 0;  // values > T
+    int over = 0, count = 0;  // values > T, and values taken
     float T = INFINITY;
-    for (count = 0; count < a.k;) {
+    while (count < a.k) {
       const float top = redux_max(head[0]);
       if (top == -INFINITY) break;
       if (top < T) over = count;  // (a lane may hold equals of T one after the other)
@@ -409,7 +438,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
       w = s > 0.0f ? w / s : 0.0f;
     }
   } else if (a.renorm) {
-    const float m = warp_max(my_l);
+    const float m = redux_max(my_l);
     if (my_e >= 0) w = expf(my_l - m);
     const float s = warp_sum(w);
     w = s > 0.0f ? w / s : 0.0f;
@@ -458,7 +487,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
 #pragma unroll
     for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
   } else if (a.renorm) {
-    const float m = warp_max(my_l);
+    const float m = redux_max(my_l);
     const float p = my_l > -INFINITY ? expf(my_l - m) : 0.0f;
     const float total = warp_sum(p);
     if (total > 0.0f) {
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i] = finite(l[i]));
-    mx = warp_max(mx);
+    mx = redux_max(mx);
     if (mx == -INFINITY) mx = 0.0f;
     float sum = 0.0f;
 #pragma unroll

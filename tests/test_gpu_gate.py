@@ -211,6 +211,24 @@ def test_values_that_differ_in_their_last_bits_only():
             check(l.cuda(), opts("sigmoid", True), k)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [100, 256, 1024])
+def test_the_chosen_are_neighbours(E, dtype):
+    """The largest logits lie next to one another and a fixed distance apart, so that one lane holds many of them."""
+    require_gpu()
+    g = torch.Generator().manual_seed(E)
+    l = torch.rand((5, E), generator=g).sub_(9).to(dtype)
+    high = torch.arange(16) / 8 + 1
+    l[0, 4:20] = high.to(dtype)
+    l[1, torch.arange(16) // 4 * (E // 4 // 4 * 4) + torch.arange(16) % 4] = high.to(dtype)
+    l[2, torch.arange(4) + 8] = high[:4].to(dtype)
+    l[3, :] = float("-inf")
+    l[3, 8:13] = high[:5].to(dtype)
+    l[4, [8, 9, 10, 11, E - 1]] = high[:5].to(dtype)
+    for k in (1, 4, 5, 8, 16):
+        check(l.cuda(), opts("sigmoid", True, bf16=dtype == torch.bfloat16), k)
+
+
 @pytest.mark.parametrize("groups", [0, 4])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_bias_selects_and_does_not_weigh(score, groups):
