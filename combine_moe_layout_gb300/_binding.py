@@ -436,13 +436,13 @@ class PartBuffers:
         t = MoeParts()
         t.num_parts = self.num_parts
         for g in range(self.num_parts):
-            t.recv_x[g] = _ptr(self.recv_x[g]).value
-            t.recv_meta[g] = _ptr(self.recv_meta[g]).value
-            t.flags[g] = _ptr(self.flags[g]).value
+            t.recv_x[g] = _ptr(self.recv_x[g])
+            t.recv_meta[g] = _ptr(self.recv_meta[g])
+            t.flags[g] = _ptr(self.flags[g])
             if self.recv_scales is not None:
-                t.recv_scales[g] = _ptr(self.recv_scales[g]).value
+                t.recv_scales[g] = _ptr(self.recv_scales[g])
             if self.expert_out is not None:
-                t.expert_out[g] = _ptr(self.expert_out[g]).value
+                t.expert_out[g] = _ptr(self.expert_out[g])
         return t
 
 
