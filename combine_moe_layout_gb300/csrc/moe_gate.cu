@@ -22,8 +22,17 @@
 //
 // Both kernels take one warp per token: a lane holds E/32 logits in registers
 // (groups of four neighbours, so a row is read with 16-byte (fp32) or 8-byte
-// (bf16) loads) and a choice is one warp maximum over order-preserving integer
-// keys and one warp minimum over the indices that hold it.
+// (bf16) loads) and a choice is one warp maximum over integer keys that hold the
+// order of a logit and its expert.
+//
+// Measured, 32768 tokens of 256 fp32 logits, k = 8, renormalised softmax: the
+// gate takes 18.5 us (36 MB, 1.9 TB/s). It is bound by integer instructions
+// (their pipe is busy for more than 80% of the time), so what counts is how few
+// a choice takes: with a maximum over all of a lane's values for each choice it
+// took 36 us, with lists of four sorted keys a lane 18.5 us. The gradient takes
+// 11.8 us (44 MB with the chosen logits' sectors, 3.7 TB/s), bound by its reads
+// one after the other (ids, then the chosen logits) and the launch. One token:
+// 4.4 us a call, which is its launch.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -451,6 +460,9 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   }
 }
 
+// The gradient's row is zero (renormalised softmax and sigmoid) or -s_e times
+// one number (plain softmax), but for the k chosen. A renormalised row needs the
+// chosen logits only, so the other E - k are not read.
 template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

