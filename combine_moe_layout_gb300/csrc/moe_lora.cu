@@ -107,10 +107,11 @@ __device__ __forceinline__ float4 peer_load(uint32_t saddr, uint32_t rank) {
 // The sum over the cluster's CTAs, in their order, of 8 floats at this
 // shared-memory address. All loads are issued before the first is used: one
 // after the other they take a quarter of a microsecond each.
+template <int MAX>
 __device__ __forceinline__ void cluster_sum8(uint32_t saddr, int ctas, float (&f)[8]) {
-  float4 lo[kLMaxCluster], hi[kLMaxCluster];
+  float4 lo[MAX], hi[MAX];
 #pragma unroll
-  for (int p = 0; p < kLMaxCluster; ++p)
+  for (int p = 0; p < MAX; ++p)
     if (p < ctas) {
       lo[p] = peer_load(saddr, p);
       hi[p] = peer_load(saddr + 16, p);
@@ -118,7 +119,7 @@ __device__ __forceinline__ void cluster_sum8(uint32_t saddr, int ctas, float (&f
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = 0.0f;
 #pragma unroll
-  for (int p = 0; p < kLMaxCluster; ++p)
+  for (int p = 0; p < MAX; ++p)
     if (p < ctas) {
       f[0] += lo[p].x;
       f[1] += lo[p].y;
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       if (p < 0 || p >= nact) continue;
       const float sc = a.scales != nullptr ? __ldg(a.scales + sh.list[first + p]) : 1.0f;
       float f[8];
-      cluster_sum8(smem_addr(red + m * a.rank + c), splits, f);
+      cluster_sum8<kLMaxCluster>(smem_addr(red + m * a.rank + c), splits, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= sc;
       *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(t0 + m) * a.rank + c) = round8(f);
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     const int i = tid * splits + split, m = i >> 1, c = (i & 1) * 8;
     if (m < nt && n0 + c < a.rank) {
       float f[8];
-      cluster_sum8(smem_addr(&red[m][c]), splits, f);
+      cluster_sum8<kLMaxCluster>(smem_addr(&red[m][c]), splits, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= sc;
       *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(token[m0 + m]) * a.rank + n0 + c) = round8(f);
@@ -916,7 +917,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         const int q = i / vecs, m = q * splits + split, c = (i - q * vecs) * 8;
         if (t.n0 + c >= a.N) continue;
         float f[8];
-        cluster_sum8(smem_addr(reinterpret_cast<float *>(smem) + m * kRedPitch + c), splits, f);
+        cluster_sum8<kLMaxSplit>(smem_addr(reinterpret_cast<float *>(smem) + m * kRedPitch + c), splits, f);
         *reinterpret_cast<uint4 *>(a.y + static_cast<int64_t>(t.t0 + m) * a.N + t.n0 + c) = round8(f);
       }
     }
@@ -1000,6 +1001,11 @@ constexpr int kShrinkRing = 84 * 1024;
 constexpr int kSplitRing = 84 * 1024;
 constexpr int kSplitRingFew = 128 * 1024;  // up to 8 tokens: their shrink CTAs leave SMs enough
 constexpr int kFewTokens = 8;
+// Few tokens' shrink CTAs, where there are no more of them than SMs: one an SM,
+// beside a CTA of the projection. They come while the last call's projection is
+// ending; two of them on an SM that it does not use would leave no registers for
+// the next projection's CTA there, whose cluster then starts when they end.
+constexpr int kSmallAlone = 104 * 1024;
 
 moe_status launch_shrink_small(const LoraArgs &a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   if (a.adapters > 0x7fffffff / kLMaxCluster) return MOE_EINVAL;
@@ -1009,7 +1015,8 @@ moe_status launch_shrink_small(const LoraArgs &a, const void *x, const void *lor
   while (splits > 1 && busy * splits > sms) splits >>= 1;
   const dim3 grid(static_cast<unsigned>(a.adapters * splits), static_cast<unsigned>(nchunks),
                   static_cast<unsigned>((a.T + kSmallTokensPerCta - 1) / kSmallTokensPerCta));
-  return launch_cluster(lora_shrink_small_kernel, grid, kSmallThreads, splits, 0, stream, a,
+  const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y * grid.z;
+  return launch_cluster(lora_shrink_small_kernel, grid, kSmallThreads, splits, ctas <= sms ? kSmallAlone : 0, stream, a,
                         static_cast<const uint4 *>(x), static_cast<const uint4 *>(lora_a));
 }
 
