@@ -92,6 +92,23 @@ __device__ __forceinline__ void lora_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void lora_cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void lora_cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Writes v at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ void peer_store(uint32_t saddr, uint32_t rank, float v) {
+  uint32_t p;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(saddr), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(p), "f"(v) : "memory");
+}
+
 // 16 bytes at this shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ float4 peer_load(uint32_t saddr, uint32_t rank) {
   uint32_t p;
@@ -485,23 +502,31 @@ __global__ void __launch_bounds__(kShrinkThreads)
 
 // ---------------------------------------------------------------------------
 // u for few tokens: one cluster of CTAs per (adapter, 16 of its rows), which
-// takes its tokens 16 at a time, K split over the cluster's warps so that all of
-// a row is in flight in one or two rounds of loads. The tensor-core tiles above
-// take 128 tokens whether they use the adapter or not; here a token's x row
+// takes its tokens 16 at a time, K split over the cluster. The tensor-core tiles
+// above take 128 tokens whether they use the adapter or not; here a token's x row
 // meets only its own adapter.
+// Bound by the latency of the loads, beside the projection's stream of W: a CTA
+// asks for all of its rows' pieces at once, with one bulk copy a row into shared
+// memory (two halves in turn where they do not fit). Loading them to registers,
+// in two rounds, took 6 us at the sizes below, and takes 4 us so.
 // Products: mma.sync, whose 16-row tiles fit a handful of tokens (a
 // tensor-memory accumulator would cost a claim, a commit and a read back for
-// them). Fragments come straight from global memory with 16-byte loads: lane
-// (g, t) loads elements 8t .. 8t + 7 of a 32-wide K piece of row g and gives
-// them to two k = 16 steps as its elements (2t, 2t + 1) and (2t + 8, 2t + 9) of
-// each; x and A_a are permuted alike, so the sum is the same.
-// Measured beside the projection of 64 tokens (7168 -> 2048, 32 adapters of
-// rank 16): the call takes 21.6 us with the tensor-memory kernel and 19.5 us with
-// this one.
+// them). Lane (g, t) reads elements 8t .. 8t + 7 of a 32-wide K piece of row g
+// and gives them to two k = 16 steps as its elements (2t, 2t + 1) and (2t + 8,
+// 2t + 9) of each; x and A_a are permuted alike, so the sum is the same. Rows lie
+// 64 bytes past a multiple of 128 apart, so that eight lanes' reads meet every
+// bank once.
+// Sums: every CTA of the cluster sends its part of a sum to the CTA that owns it
+// and the owner adds them in the order of the CTAs. What it receives has two
+// places in turn, so one cluster barrier a pass is enough.
+// 64 tokens (7168 -> 2048, 32 adapters of rank 16): the call takes 21.6 us with
+// the tensor-memory kernel, 19.5 us with loads to registers and sums read from
+// the other CTAs, 17.3 us with this one.
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 256;
 constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kSmallM = 16, kSmallN = 16;
+constexpr int kSmallPad = 64;  // bytes between rows in shared memory
 constexpr int kSmallTokensPerCta = 64;  // calls of more tokens have more CTAs per adapter, which exit where there is nothing to do
 
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -513,15 +538,26 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// K elements (a multiple of 64) of which `bytes` hold `rows` rows.
+__host__ __device__ constexpr int small_chunk(int bytes, int rows) { return (bytes / rows - kSmallPad) / 128 * 64; }
+
 __global__ void __launch_bounds__(kSmallThreads)
-    lora_shrink_small_kernel(const LoraArgs a, const uint4 *__restrict__ x, const uint4 *__restrict__ lora_a) {
+    lora_shrink_small_kernel(const LoraArgs a, const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__restrict__ lora_a) {
+  extern __shared__ __align__(128) uint8_t small_rows[];  // a.ring bytes: rows of A_a, then of x
   __shared__ float part[kSmallWarps][kSmallM][kSmallN + 1];
-  __shared__ __align__(16) float red[kSmallM][kSmallN];  // this CTA's sums
+  __shared__ __align__(16) float recv[2][kLMaxCluster][kSmallM * kSmallN];  // the parts of the sums that this CTA owns
   __shared__ int32_t token[kLBM];
   __shared__ int32_t counts[kSmallWarps];
+  __shared__ uint64_t full[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = static_cast<int>(lora_cluster_size()), split = static_cast<int>(lora_cluster_rank());
   const int ad = blockIdx.x / splits, n0 = blockIdx.y * kSmallN;
+  if (tid == 0) {
+    mbar_init(full, 1);
+    mbar_init(full + 1, 1);
+    fence_mbar_init();
+  }
+  lora_cluster_arrive();  // the others may be written to once they have started
   grid_dependency_wait();
   grid_dependents_launch();  // the projection finds what this kernel's predecessors wrote
   // this adapter's tokens, in token order
@@ -538,44 +574,74 @@ __global__ void __launch_bounds__(kSmallThreads)
   }
   if (id == ad) token[at] = tid;
   __syncthreads();
-  const int g = lane >> 2, t4 = lane & 3;
-  const int kv = a.K / 8;  // 16-byte vectors of a row
-  const uint4 *ar[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    ar[i] = n0 + i * 8 + g < a.rank ? lora_a + (static_cast<int64_t>(ad) * a.rank + n0 + i * 8 + g) * kv : nullptr;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int pieces = (kv + 3) / 4, stride = kSmallWarps * splits;
-  constexpr int kUnroll = 4;
-  const float sc = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
 
-  // 16 tokens at a time, the same ones in every CTA of the cluster
-  for (int m0 = blockIdx.z * kSmallM; m0 < total; m0 += gridDim.z * kSmallM) {
+  // this CTA's K elements, its passes of 16 tokens (the same in every CTA of the cluster) and the steps of a pass
+  const int pieces = (a.K + 31) / 32;
+  const int e0 = static_cast<int>(static_cast<int64_t>(pieces) * split / splits) * 32;
+  const int len = max(min(static_cast<int>(static_cast<int64_t>(pieces) * (split + 1) / splits) * 32, a.K) - e0, 0);
+  const int first = blockIdx.z * kSmallM, every = gridDim.z * kSmallM;
+  const int passes = total > first ? (total - first + every - 1) / every : 0;
+  const int nr = min(kSmallN, a.rank - n0);                  // rows of A_a
+  const int most = nr + min(kSmallM, max(total - first, 0));  // and of x
+  const bool whole = passes == 1 && len <= small_chunk(a.ring, most);
+  const int chunk = whole ? (len + 63) / 64 * 64 : small_chunk(a.ring / 2, most);
+  const int chunks = len > 0 ? (len + chunk - 1) / chunk : 0, steps = passes * chunks;
+  const int pitch = chunk * 2 + kSmallPad;
+  // asks for step s into half s & 1 (warp 0)
+  const auto load = [&](int s) {
+    const int m0 = first + s / chunks * every, o = s % chunks * chunk;
     const int nt = min(total - m0, kSmallM);
-    const uint4 *xr[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      xr[i] = i * 8 + g < nt ? x + static_cast<int64_t>(token[m0 + i * 8 + g]) * kv : nullptr;
+    const uint32_t bytes = static_cast<uint32_t>(min(chunk, len - o)) * 2;
+    uint8_t *dst = small_rows + (s & 1) * (a.ring / 2);
+    if (lane == 0) mbar_arrive_expect_tx(full + (s & 1), static_cast<uint32_t>(nr + nt) * bytes);
+    __syncwarp();
+    if (lane < kSmallN) {
+      if (lane < nr)
+        bulk_load(dst + lane * pitch, lora_a + (static_cast<int64_t>(ad) * a.rank + n0 + lane) * a.K + e0 + o, bytes,
+                  full + (s & 1));
+    } else if (lane - kSmallN < nt) {
+      bulk_load(dst + (nr + lane - kSmallN) * pitch, x + static_cast<int64_t>(token[m0 + lane - kSmallN]) * a.K + e0 + o,
+                bytes, full + (s & 1));
+    }
+    __syncwarp();
+  };
+  if (warp == 0) {
+    if (steps > 0) load(0);
+    if (steps > 1) load(1);
+  }
+  const int g = lane >> 2, t4 = lane & 3;
+  const float sc = a.scales != nullptr && passes > 0 ? __ldg(a.scales + ad) : 1.0f;
+  lora_cluster_wait();
+
+  for (int pass = 0, s = 0; pass < passes; ++pass) {
+    const int m0 = first + pass * every;
+    const int nt = min(total - m0, kSmallM);
     float acc[2][4] = {};
-    for (int p0 = split * kSmallWarps + warp; p0 < pieces; p0 += stride * kUnroll) {
-      uint4 xv[kUnroll][2], av[kUnroll][2];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int v = (p0 + u * stride) * 4 + t4;
-        const bool in = v < kv;
+    for (int c = 0; c < chunks; ++c, ++s) {
+      if (!mbar_wait_bounded(full + (s & 1), (s >> 1) & 1)) latch_error(a.err, MOE_ETIMEOUT);
+      const uint8_t *rows = small_rows + (s & 1) * (a.ring / 2) + t4 * 16;
+      const int n = min(chunk, len - c * chunk);
+#pragma unroll 2
+      for (int p = warp; p * 32 < n; p += kSmallWarps) {
+        const bool in = p * 32 + t4 * 8 < n;
+        uint4 av[2], xv[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          av[u][i] = in && ar[i] != nullptr ? __ldg(ar[i] + v) : zero;
-          xv[u][i] = in && xr[i] != nullptr ? __ldg(xr[i] + v) : zero;
+          const uint8_t *q = rows + (i * 8 + g) * pitch + p * 64;
+          av[i] = xv[i] = make_uint4(0, 0, 0, 0);
+          if (in && i * 8 + g < nr) av[i] = *reinterpret_cast<const uint4 *>(q);
+          if (in && i * 8 + g < nt) xv[i] = *reinterpret_cast<const uint4 *>(q + nr * pitch);
         }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          mma_m16n8k16(acc[j], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, av[u][j].x, av[u][j].y);
-          mma_m16n8k16(acc[j], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][j].z, av[u][j].w);
+          mma_m16n8k16(acc[j], xv[0].x, xv[1].x, xv[0].y, xv[1].y, av[j].x, av[j].y);
+          mma_m16n8k16(acc[j], xv[0].z, xv[1].z, xv[0].w, xv[1].w, av[j].z, av[j].w);
         }
+      }
+      if (s + 2 < steps) {
+        __syncthreads();  // this half has been read
+        if (warp == 0) load(s + 2);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -583,23 +649,24 @@ __global__ void __launch_bounds__(kSmallThreads)
       for (int c = 0; c < 4; ++c) part[warp][(c >> 1) * 8 + g][j * 8 + t4 * 2 + (c & 1)] = acc[j][c];
     __syncthreads();
     {
-      const int m = tid / kSmallN, n = tid - m * kSmallN;  // one sum a thread
+      const int m = tid / kSmallN, n = tid - m * kSmallN;  // one sum a thread; 8 of them have one owner
       float f = 0.0f;
 #pragma unroll
       for (int w = 0; w < kSmallWarps; ++w) f += part[w][m][n];
-      red[m][n] = f;
+      peer_store(smem_addr(&recv[pass & 1][split][tid]), (tid >> 3) % splits, f);
     }
     lora_cluster_sync();
     // 8 columns a thread, the cluster's sums in the order of its CTAs
     const int i = tid * splits + split, m = i >> 1, c = (i & 1) * 8;
     if (m < nt && n0 + c < a.rank) {
-      float f[8];
-      cluster_sum8<kLMaxCluster>(smem_addr(&red[m][c]), splits, f);
+      float f[8] = {};
+      for (int p = 0; p < splits; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += recv[pass & 1][p][i * 8 + j];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= sc;
       *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(token[m0 + m]) * a.rank + n0 + c) = round8(f);
     }
-    lora_cluster_sync();  // no CTA goes on or leaves while another may still read its sums
   }
 }
 
@@ -1001,13 +1068,17 @@ constexpr int kShrinkRing = 84 * 1024;
 constexpr int kSplitRing = 84 * 1024;
 constexpr int kSplitRingFew = 128 * 1024;  // up to 8 tokens: their shrink CTAs leave SMs enough
 constexpr int kFewTokens = 8;
-// Few tokens' shrink CTAs, where there are no more of them than SMs: one an SM,
-// beside a CTA of the projection. They come while the last call's projection is
-// ending; two of them on an SM that it does not use would leave no registers for
-// the next projection's CTA there, whose cluster then starts when they end.
-constexpr int kSmallAlone = 104 * 1024;
+// Rows of few tokens' shrink CTAs: two CTAs an SM. Where there are no more of
+// them than SMs, one an SM: they come while the last call's projection is ending,
+// and several on an SM that it does not use would leave no room for the next
+// projection's CTA there, whose cluster then starts when they end (64 tokens: 5 to
+// 7 us late for half of the clusters).
+constexpr int kSmallRows = 80 * 1024;
+constexpr int kSmallAlone = 90 * 1024;
+constexpr int kSmallLeast = 12 * 1024;  // a half holds 64 elements of the most rows
+static_assert(small_chunk(kSmallLeast / 2, kSmallM + kSmallN) >= 64 && kSmallRows % 256 == 0 && kSmallLeast % 256 == 0, "");
 
-moe_status launch_shrink_small(const LoraArgs &a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
+moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   if (a.adapters > 0x7fffffff / kLMaxCluster) return MOE_EINVAL;
   const int nchunks = (a.rank + kSmallN - 1) / kSmallN;
   const int64_t busy = static_cast<int64_t>(a.adapters < a.T ? a.adapters : a.T) * nchunks;  // clusters with work, at most
@@ -1016,8 +1087,14 @@ moe_status launch_shrink_small(const LoraArgs &a, const void *x, const void *lor
   const dim3 grid(static_cast<unsigned>(a.adapters * splits), static_cast<unsigned>(nchunks),
                   static_cast<unsigned>((a.T + kSmallTokensPerCta - 1) / kSmallTokensPerCta));
   const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y * grid.z;
-  return launch_cluster(lora_shrink_small_kernel, grid, kSmallThreads, splits, ctas <= sms ? kSmallAlone : 0, stream, a,
-                        static_cast<const uint4 *>(x), static_cast<const uint4 *>(lora_a));
+  const int rows = (a.rank < kSmallN ? a.rank : kSmallN) + (a.T < kSmallM ? a.T : kSmallM);
+  const int64_t slice = static_cast<int64_t>((a.K + 31) / 32 + splits - 1) / splits * 32;  // a CTA's K elements, at most
+  const int64_t need = rows * ((slice + 63) / 64 * 128 + kSmallPad);
+  a.ring = need < kSmallRows ? static_cast<int>((need + 255) / 256 * 256) : kSmallRows;
+  if (a.ring < kSmallLeast) a.ring = kSmallLeast;
+  const int least = a.T > kFewTokens && ctas <= sms ? kSmallAlone : 0;
+  return launch_cluster(lora_shrink_small_kernel, grid, kSmallThreads, splits, a.ring > least ? a.ring : least, stream, a,
+                        static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(lora_a));
 }
 
 moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
