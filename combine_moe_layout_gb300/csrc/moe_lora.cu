@@ -41,6 +41,7 @@ namespace {
 constexpr int kLBM = 128;           // tokens of a tile
 constexpr int kLBK = 64;            // K elements of a stage: one 128-byte swizzle row
 constexpr int kLRow = kLBK * 2;     // bytes of a tile row
+constexpr int kLPieceRow = 32;      // bytes of a row of 16 columns of a B_a
 constexpr int kLMaxStages = 8;
 constexpr int kLMaxRank = 256;
 constexpr int kLSmemMax = 227 * 1024;
@@ -51,6 +52,11 @@ constexpr int kGemmLThreads = 320;
 constexpr int kShrinkCols = 128;    // adapter rows of a shrink tile (or one adapter's, if it has more)
 constexpr int kLMaxCluster = 8;    // of the shrink kernel
 constexpr int kLMaxSplit = 4;      // of the projection
+// Ranks up to 32 have several adapters' B_a in a stage, as pieces of 16 columns:
+// a block of 64 columns would be half empty or more, and each would take a
+// stage's way through the ring (64 tokens, 32 adapters of rank 16: 17.1 us with
+// blocks of 64 columns, 16.1 with eight adapters a stage).
+constexpr int kLPackedPieces = 2;
 
 struct LoraArgs {
   const int32_t *adapter;
@@ -70,6 +76,7 @@ struct LoraArgs {
   // projection
   int lora, ntiles_n, mtiles, group_n;
   int whole, total;      // tiles taken whole, and tiles and halves in all
+  int pieces, packed;    // ranks up to 32: pieces of 16 columns of one B_a, and the B_a of a stage (0: 64 columns a stage)
 };
 
 __device__ __forceinline__ uint32_t lora_cluster_rank() {
@@ -191,6 +198,14 @@ __device__ __forceinline__ void tmem_load8_wait(uint32_t taddr, float (&f)[8]) {
 // A block's products take 256 cycles (BN = 128); descriptors made anew for every
 // step took longer than that.
 constexpr uint32_t kDescHi = static_cast<uint32_t>(sw128_desc(0) >> 32);
+
+// As sw128_desc for tiles of 16 elements a row: 32-byte rows, 8-row groups 256
+// bytes apart, swizzle mode 6 = 32 bytes (tiles start on 256-byte boundaries).
+__host__ __device__ constexpr uint64_t sw32_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16 >> 4) << 16) |
+         (static_cast<uint64_t>(256 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(6) << 61);
+}
 
 __device__ __forceinline__ uint64_t full_desc(uint32_t lo) { return (static_cast<uint64_t>(kDescHi) << 32) | lo; }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return static_cast<uint32_t>(sw128_desc(saddr)); }
@@ -809,14 +824,31 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
       if (!ok) break;
       const int blocks = sh.count[b] * rblocks;
-      for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
-        ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
-        if (!ok) break;
-        if (leader) {
-          mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(t.cols) * kLRow);
-          load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
+      if (a.packed > 0) {  // a piece a lane
+        for (int j = split; j < blocks; j += splits * a.packed, ++it, r.next(a.stages)) {
+          ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+          if (!ok) break;
+          const int n = min(a.packed, (blocks - j + splits - 1) / splits) * a.pieces;
+          if (leader) mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(n * t.cols) * kLPieceRow);
+          __syncwarp();
+          if (lane < n) {
+            const int row = sh.list[b][j + lane / a.pieces * splits] * a.N + t.n0, k = lane % a.pieces * 16;
+            const uint32_t dst = ring + r.s * a.stage + lane * (BN * kLPieceRow), fb = fulls + r.s * 8;
+            tma_load_2d(dst, &map_b, k, row, fb);
+            if (t.cols > kBoxRows) tma_load_2d(dst + kBoxRows * kLPieceRow, &map_b, k, row + kBoxRows, fb);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
+          ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+          if (!ok) break;
+          if (leader) {
+            mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(t.cols) * kLRow);
+            load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
+          }
+          __syncwarp();
+        }
       }
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       __syncwarp();
@@ -861,20 +893,40 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
           if (!ok) break;
           ++uphase;
         }
-        for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
-          ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const uint32_t lo = xlo + r.s * step, ulo = desc_lo(ubuf) + (j % rblocks) * xstep;
-            const uint4 off = sh.off[b][j / rblocks];
-            // columns past the rank are zeros in both tiles, so a step's last ones add nothing
-            const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
-            for (int kk = 0; kk * 16 < cols; ++kk)
-              mma_bf16_rows(d, full_desc(ulo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
-            mma_commit(empty + r.s * 8);
+        if (a.packed > 0) {
+          for (int j = split; j < blocks; j += splits * a.packed, r.next(a.stages)) {
+            ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            const int n = min(a.packed, (blocks - j + splits - 1) / splits);
+            if (leader) {
+              uint64_t piece = sw32_desc(smem_addr(smem) + r.s * a.stage);
+              const uint32_t ulo = desc_lo(ubuf);
+              for (int i = 0; i < n; ++i) {
+                const uint4 off = sh.off[b][j + i * splits];
+                for (int q = 0; q < a.pieces; ++q, piece += (BN * kLPieceRow) >> 4)
+                  mma_bf16_rows(d, full_desc(ulo + q * 2), piece, idesc, off);
+              }
+              mma_commit(empty + r.s * 8);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        } else {
+          for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
+            ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              const uint32_t lo = xlo + r.s * step, ulo = desc_lo(ubuf) + (j % rblocks) * xstep;
+              const uint4 off = sh.off[b][j / rblocks];
+              // columns past the rank are zeros in both tiles, so a step's last ones add nothing
+              const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
+              for (int kk = 0; kk * 16 < cols; ++kk)
+                mma_bf16_rows(d, full_desc(ulo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
+              mma_commit(empty + r.s * 8);
+            }
+            __syncwarp();
+          }
         }
         if (leader) {
           mbar_arrive(smem_addr(sh.lempty + b));
@@ -1005,16 +1057,17 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-// 2-D map of a row-major [rows][K] bf16 matrix, boxes of box_rows x 64 elements, 128-byte swizzle.
-bool make_box_map(CUtensorMap *map, const void *base, int64_t K, int64_t rows, int box_rows) {
+// 2-D map of a row-major [rows][K] bf16 matrix, boxes of box_rows x 64 (or 16) elements, 128-byte (32-byte) swizzle.
+bool make_box_map(CUtensorMap *map, const void *base, int64_t K, int64_t rows, int box_rows, int box_k = kLBK) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(kLBK), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_k == kLBK ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1132,20 +1185,23 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
 }
 
 // The projection's tiles: their width and the CTAs that share one's K, by the
-// time they are expected to take: waves of CTAs x K blocks of one x the time of
-// a block (measured beside other CTAs: 0.20, 0.30 and 0.33 us for 64, 128 and
-// 256 outputs; a wide tile has more products for the bytes that it loads), then
-// the sum over a cluster (3 us), and what the last tile's stores take, with,
-// for 256-wide tiles, the shrink kernel that their CTAs have to let finish
-// first (1.2 and 5 us). Only 256-wide tiles come several to a CTA. Widths of 64
-// only pay where 128 tokens or fewer leave SMs idle. Measured against 128-wide tiles throughout: 1500 tokens 4096 ->
-// 2048 41 to 36.5 us, 700 tokens 4104 -> 2056 31 to 29 us; against 256-wide
-// ones: 389 tokens 2056 -> 4104 23.6 to 20.6 us.
+// time they are expected to take, in ns: waves of CTAs x K blocks of one x the
+// time of a block, the sum over a cluster, and an end (a tile's stores and, for
+// 256-wide tiles, the shrink kernel that their CTAs have to let finish first).
+// A block takes longer the more CTAs there are, and where rows of x and W do not
+// begin on 128-byte lines; sums of 128 tokens or fewer take half the time. Only
+// 256-wide tiles come several to a CTA, and widths of 64 are for 128 tokens.
+// The constants were fitted to the times of every choice at 360 shapes (1 to 2500
+// tokens, 512 to 7168 inputs and outputs): the calls take 1% longer than with the
+// best choice in the geometric mean, 12% at worst but for one shape. 256 tokens
+// 1024 -> 2048: 12.2 us with 128-wide tiles, 14.4 with two CTAs a tile, 16.9 with
+// four; 1000 tokens 4096 -> 1024: 24.2, 19.5 and 25.3 us.
 int tile_width(const LoraArgs &a, int sms, int *splits) {
   constexpr int kWidths[3] = {64, 128, 256};
-  constexpr int kBlockNs[3] = {200, 300, 330}, kEndNs[3] = {1200, 1200, 5000};
-  constexpr int kSumNs = 3000;
-  int64_t best = INT64_MAX;
+  constexpr int kBlockNs[3] = {220, 290, 340}, kEndNs[3] = {1200, 1100, 4700};
+  constexpr int kSum2Ns = 2800, kSum4Ns = 6700;
+  const double unaligned = a.K % kLBK != 0 ? 1.35 : 1.0;
+  double best = 1e300;
   int width = 256;
   *splits = 1;
   for (int i = 0; i < 3; ++i)
@@ -1153,7 +1209,10 @@ int tile_width(const LoraArgs &a, int sms, int *splits) {
       if (s > a.kblocks || (kWidths[i] == 64 && (a.mtiles > 1 || s == 1))) continue;
       const int64_t ctas = static_cast<int64_t>(a.mtiles) * ((a.N + kWidths[i] - 1) / kWidths[i]) * s;
       if ((s > 1 || kWidths[i] < 256) && ctas > sms) continue;
-      const int64_t ns = (ctas + sms - 1) / sms * ((a.kblocks + s - 1) / s) * kBlockNs[i] + kEndNs[i] + (s > 1 ? kSumNs : 0);
+      const double busy = ctas < sms ? static_cast<double>(ctas) / sms : 1.0;
+      const double block = kBlockNs[i] * unaligned * (0.57 + 0.43 * busy);
+      const double sum = (s == 1 ? 0 : s == 2 ? kSum2Ns : kSum4Ns) * (a.T <= kLBM ? 0.5 : 1.0);
+      const double ns = static_cast<double>((ctas + sms - 1) / sms) * ((a.kblocks + s - 1) / s) * block + kEndNs[i] + sum;
       if (ns < best) {
         best = ns;
         width = kWidths[i];
@@ -1189,12 +1248,14 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   const int smem = with_columns(1024 + a.stages * a.stage + tail, (SPLIT ? 1 : 2) * BN);
   if (smem > kLSmemMax - kLStatic) return MOE_EINVAL;
   constexpr int kBox = BN < kBoxRows ? BN : kBoxRows;
+  a.pieces = (a.rank + 15) / 16;
+  a.packed = a.lora && a.pieces <= kLPackedPieces ? a.stage / (BN * kLPieceRow) / a.pieces : 0;
   CUtensorMap mx, mw, mu, mb;
   if (!make_box_map(&mx, x, a.K, a.T, a.xrows) || !make_box_map(&mw, w, a.K, a.N, kBox)) return MOE_ECUDA;
   mu = mx;
   mb = mw;  // not used without adapters
   if (a.lora && (!make_box_map(&mu, a.u, a.rank, a.T, a.xrows) ||
-                 !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBox)))
+                 !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBox, a.packed > 0 ? 16 : kLBK)))
     return MOE_ECUDA;
   return launch_cluster(lora_gemm_kernel<BN, SPLIT>, dim3(static_cast<unsigned>(grid)), kGemmLThreads, SPLIT ? splits : 1, smem,
                         stream, mx, mw, mu, mb, a);
