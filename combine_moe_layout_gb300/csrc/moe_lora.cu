@@ -33,6 +33,8 @@
 // did could wait for ever). Every other wait is bounded, as in the expert stage.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "moe_tc.cuh"
 
 namespace moe {
@@ -1071,15 +1073,30 @@ bool make_box_map(CUtensorMap *map, const void *base, int64_t K, int64_t rows, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch with a cluster of `cluster` CTAs and programmatic dependent launch.
-template <class... P, class... Q>
-moe_status launch_cluster(void (*fn)(P...), dim3 grid, int threads, int cluster, int smem, cudaStream_t stream,
-                          Q &&...args) {
-  // the largest carve-out, so that an SM which runs one of the two kernels has room for the other
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+// A kernel's attributes, set once on a device (a call of two kernels spent 1 us
+// of 6 on the host setting them anew): up to `most` bytes of dynamic shared
+// memory, and the largest carve-out, so that an SM which runs one of the kernels
+// has room for the other.
+template <auto FN>
+bool kernel_ready(int most) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return true;
+  if (cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(FN, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
           cudaSuccess)
-    return MOE_ECUDA;
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+// Launch with a cluster of `cluster` CTAs and programmatic dependent launch.
+template <auto FN, class... Q>
+moe_status launch_cluster(int most, dim3 grid, int threads, int cluster, int smem, cudaStream_t stream, Q &&...args) {
+  if (smem > most) return MOE_EINVAL;
+  if (!kernel_ready<FN>(most)) return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -1094,7 +1111,7 @@ moe_status launch_cluster(void (*fn)(P...), dim3 grid, int threads, int cluster,
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, fn, args...) != cudaSuccess) return MOE_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, FN, args...) != cudaSuccess) return MOE_ECUDA;
   return launch_status();
 }
 
@@ -1146,7 +1163,7 @@ moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, in
   a.ring = need < kSmallRows ? static_cast<int>((need + 255) / 256 * 256) : kSmallRows;
   if (a.ring < kSmallLeast) a.ring = kSmallLeast;
   const int least = a.T > kFewTokens && ctas <= sms ? kSmallAlone : 0;
-  return launch_cluster(lora_shrink_small_kernel, grid, kSmallThreads, splits, a.ring > least ? a.ring : least, stream, a,
+  return launch_cluster<lora_shrink_small_kernel>(kSmallAlone, grid, kSmallThreads, splits, a.ring > least ? a.ring : least, stream, a,
                         static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(lora_a));
 }
 
@@ -1181,7 +1198,7 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
     return MOE_ECUDA;
   const int64_t grid = static_cast<int64_t>(a.mtiles) * a.groups * splits;
   if (grid > 0x7fffffffll) return MOE_EINVAL;
-  return launch_cluster(lora_shrink_kernel, dim3(static_cast<unsigned>(grid)), kShrinkThreads, splits, smem, stream, mx, ma, a);
+  return launch_cluster<lora_shrink_kernel>(kLSmemMax - kLStatic, dim3(static_cast<unsigned>(grid)), kShrinkThreads, splits, smem, stream, mx, ma, a);
 }
 
 // The projection's tiles: their width and the CTAs that share one's K, by the
@@ -1257,8 +1274,8 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   if (a.lora && (!make_box_map(&mu, a.u, a.rank, a.T, a.xrows) ||
                  !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBox, a.packed > 0 ? 16 : kLBK)))
     return MOE_ECUDA;
-  return launch_cluster(lora_gemm_kernel<BN, SPLIT>, dim3(static_cast<unsigned>(grid)), kGemmLThreads, SPLIT ? splits : 1, smem,
-                        stream, mx, mw, mu, mb, a);
+  return launch_cluster<lora_gemm_kernel<BN, SPLIT>>(kLSmemMax - kLStatic, dim3(static_cast<unsigned>(grid)), kGemmLThreads,
+                                                     SPLIT ? splits : 1, smem, stream, mx, mw, mu, mb, a);
 }
 
 }  // namespace
