@@ -172,7 +172,7 @@ class LocalMoe:
         self.h = rows(n, inter) if inter else None
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.grad_y, self.grad_x = None, None  # allocated by the first backward
-        self.u = self.shared_out = None        # by the first shared
+        self.u = self.shared_out = None        # by shared, for its shapes
 
     def route(self, logits, bias=None, stream=None):
         B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err, stream)
@@ -216,7 +216,7 @@ class LocalMoe:
     def shared(self, x, w, lora_a, lora_b, scales, adapter, stream=None):
         """x w^T [tokens][out] with each token's adapter beside it (moe_lora_linear)."""
         A, rank, _ = lora_a.shape
-        if self.u is None:
+        if self.u is None or self.u.shape != (x.shape[0], rank) or self.shared_out.shape[1] != w.shape[0]:
             self.u = torch.empty((x.shape[0], rank), dtype=torch.bfloat16, device=x.device)
             self.shared_out = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
         desc = B.MoeLoraDesc(x.shape[0], x.shape[1], w.shape[0], rank, A, 0)

@@ -110,3 +110,25 @@ def test_shared_projection_beside_the_experts():
     # one bf16 rounding of y and one of u, with fp32 sums far below: 2^-7 of the magnitudes that are added
     mag = x.double().abs() @ w.double().abs().t() * 2.0 ** -8
     assert bool(((y.double() - want).abs() <= 2.0 ** -7 * want.abs() + mag).all())
+
+
+def test_shared_takes_another_shape():
+    """A second projection of another width and rank: its own buffers, and the first one's result stays."""
+    require_gpu()
+    g = torch.Generator().manual_seed(4)
+    layer = P.LocalMoe(20, 128, 4, 1, opts(), "cuda:0")
+    x = torch.randn((20, 128), generator=g).to(torch.bfloat16).cuda()
+    ids = (torch.arange(20) % 3).to(torch.int32).cuda()
+    first = None
+    for N, r in ((64, 8), (264, 40), (264, 16)):
+        w = torch.randn((N, 128), generator=g).to(torch.bfloat16).cuda()
+        la = torch.randn((3, r, 128), generator=g).to(torch.bfloat16).cuda()
+        lb = torch.zeros((3, N, r), dtype=torch.bfloat16, device="cuda")
+        y = layer.shared(x, w, la, lb, None, ids)
+        assert layer.error() == B.MOE_OK and y.shape == (20, N) and layer.u.shape == (20, r)
+        want = x.double() @ w.double().t()
+        bar = 2.0 ** -8 * want.abs() + 128 * 2.0 ** -23 * (x.double().abs() @ w.double().abs().t())
+        assert bool(((y.double() - want).abs() <= bar).all())
+        if first is None:
+            first, kept = y, y.clone()
+    assert torch.equal(first, kept)
