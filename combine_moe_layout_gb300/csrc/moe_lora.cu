@@ -18,7 +18,8 @@
 //     stacked rows of up to 128 / rank adapters that occur among them (or one
 //     adapter's, if it has more): a token's own columns are picked in the
 //     epilogue. in is split over a cluster of CTAs whose partial sums meet in
-//     distributed shared memory in a fixed order.
+//     distributed shared memory in a fixed order. Up to 128 tokens take
+//     lora_shrink_small_kernel: 16 tokens of one adapter at a time.
 //   lora_gemm_kernel    the projection with its extra K blocks. Tiles of 128
 //     tokens x BN outputs; TMA brings x and W (then u and B_a) tiles, one lane
 //     issues tcgen05.mma, four warps find the tile's adapters and their rows.
