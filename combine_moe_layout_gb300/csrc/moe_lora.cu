@@ -13,7 +13,7 @@
 // the tensor cores take, costs 2^-9 of the adapter's term: at most what rounding
 // y costs where that term is all of it.
 //
-// Two kernels:
+// Two kernels a call:
 //   lora_shrink_kernel  u[t] = s_a x[t] A_a^T. A tile is 128 tokens against the
 //     stacked rows of up to 128 / rank adapters that occur among them (or one
 //     adapter's, if it has more): a token's own columns are picked in the
@@ -27,6 +27,7 @@
 //     its tiles with two accumulators, so that a tile's stores overlap the next
 //     one's products. It starts on x and W while the shrink kernel is running;
 //     only the loads of u wait for that.
+//   lora_one_kernel     the projection of a single token, without tensor cores.
 //
 // Shared memory and tensor memory: a CTA that takes c of the 512 tensor-memory
 // columns of an SM takes at least c / 512 of its shared memory, so that CTAs
@@ -79,6 +80,7 @@ struct LoraArgs {
   // projection
   int lora, ntiles_n, mtiles, group_n;
   int whole, total;      // tiles taken whole, and tiles and halves in all
+  int own;               // one token: rows of W of a CTA
   int pieces, packed;    // ranks up to 32: pieces of 16 columns of one B_a, and the B_a of a stage (0: 64 columns a stage)
 };
 
@@ -1058,6 +1060,109 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// The projection of one token: a dot product of each row of W with it.
+//
+// Bound by the stream of W, so what counts besides it is what a call does before
+// its first load and after its last: there is no ring to set up, no tensor memory
+// and no cluster, only shuffles and one barrier. A CTA takes a few rows of W and
+// all of K: thread tid the 16-byte vectors tid, tid + 256, ... of eight rows at a
+// time, two vectors in turn, so that sixteen loads are in flight in a thread.
+// Products and sums are in fp32, the sums over lanes and warps in a fixed order.
+// The adapter's term is added last, from u and the rows of B_a, by eight lanes
+// for each row.
+// Against the tiles above, with an adapter of rank 16: 4096 -> 4096 10.8 to 9.2
+// us, 7168 -> 2048 12.1 to 7.7; without one: 9.9 to 8.8, 10.4 to 7.8, 4096 ->
+// 14336 23.8 to 24.4, 512 -> 7168 4.8 to 5.2. Two tokens came out even with an
+// adapter (10.8 and 11.2 us), four behind (11.5 and 14.1 us: the sums take the
+// registers that loads in flight need).
+// ---------------------------------------------------------------------------
+constexpr int kOneThreads = 256;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kOneChunk = 8;  // rows at a time
+constexpr int kOneRows = 16;  // rows of a CTA, at most
+
+__device__ __forceinline__ void unpack8(const uint4 &r, float (&f)[8]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = __uint_as_float(u[q] << 16);
+    f[2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+  }
+}
+
+__global__ void __launch_bounds__(kOneThreads, 2)
+    lora_one_kernel(const LoraArgs a, const uint4 *__restrict__ x, const uint4 *__restrict__ w,
+                    const uint4 *__restrict__ lora_b) {
+  __shared__ float part[kOneWarps][kOneRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row0 = static_cast<int>(blockIdx.x) * a.own, rows = min(a.own, a.N - row0);
+  const int kv = a.K / 8, rv = a.rank / 8;  // 16-byte vectors of a row of W and of B_a
+  if (!a.lora) grid_dependency_wait();      // (as in the kernel above)
+  for (int c0 = 0; c0 < rows; c0 += kOneChunk) {
+    float acc[kOneChunk] = {};
+    const uint4 *wr = w + static_cast<int64_t>(row0 + c0) * kv;
+#pragma unroll 2
+    for (int v = tid; v < kv; v += kOneThreads) {
+      uint4 wv[kOneChunk];
+#pragma unroll
+      for (int j = 0; j < kOneChunk; ++j)
+        wv[j] = c0 + j < rows ? __ldcs(wr + static_cast<int64_t>(j) * kv + v) : make_uint4(0, 0, 0, 0);
+      float xf[8];
+      unpack8(__ldg(x + v), xf);
+#pragma unroll
+      for (int j = 0; j < kOneChunk; ++j) {
+        float wf[8];
+        unpack8(wv[j], wf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[j] = fmaf(wf[e], xf[e], acc[j]);
+      }
+    }
+    // each step halves the rows that a lane holds: in the end lane l has row l / 4 of the chunk
+#pragma unroll
+    for (int half = kOneChunk / 2, bit = 16; half > 0; half >>= 1, bit >>= 1) {
+      const bool up = (lane & bit) != 0;
+#pragma unroll
+      for (int j = 0; j < half; ++j) {
+        const float send = up ? acc[j] : acc[j + half], keep = up ? acc[j + half] : acc[j];
+        acc[j] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+      }
+    }
+    float f = acc[0];
+    f += __shfl_xor_sync(0xffffffffu, f, 2);
+    f += __shfl_xor_sync(0xffffffffu, f, 1);
+    if ((lane & 3) == 0) part[warp][c0 + (lane >> 2)] = f;
+  }
+  grid_dependents_launch();  // what comes next may be on its way during the sums
+  grid_dependency_wait();    // u is written
+  __syncthreads();
+  const int r = tid >> 3, sub = tid & 7;
+  float f = 0.0f;
+  if (r < rows) {
+    if (sub == 0) {
+#pragma unroll
+      for (int i = 0; i < kOneWarps; ++i) f += part[i][r];
+    }
+    const int id = a.lora ? __ldg(a.adapter) : -1;
+    if (id >= 0 && id < a.adapters) {
+      const uint4 *u = reinterpret_cast<const uint4 *>(a.u);
+      const uint4 *b = lora_b + (static_cast<int64_t>(id) * a.N + row0 + r) * rv;
+      for (int v = sub; v < rv; v += 8) {
+        float uf[8], bf[8];
+        unpack8(__ldcg(u + v), uf);
+        unpack8(__ldg(b + v), bf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f = fmaf(uf[e], bf[e], f);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+  if (r < rows && sub == 0) a.y[row0 + r] = __float2bfloat16_rn(f);
+}
+
+static_assert(kOneRows * 8 <= kOneThreads, "eight lanes a row");
+
+// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 // 2-D map of a row-major [rows][K] bf16 matrix, boxes of box_rows x 64 (or 16) elements, 128-byte (32-byte) swizzle.
@@ -1137,8 +1242,8 @@ int ring_stages(int stage, int blocks, int bytes) {
 // projection, or two of the projection.
 constexpr int kShrinkRing = 84 * 1024;
 constexpr int kSplitRing = 84 * 1024;
-constexpr int kSplitRingFew = 128 * 1024;  // up to 8 tokens: their shrink CTAs leave SMs enough
-constexpr int kFewTokens = 8;
+constexpr int kSplitRingFew = 128 * 1024;  // up to kFewShrink tokens: their shrink CTAs leave SMs enough
+constexpr int kFewShrink = 8;
 // Rows of few tokens' shrink CTAs: two CTAs an SM. Where there are no more of
 // them than SMs, one an SM: they come while the last call's projection is ending,
 // and several on an SM that it does not use would leave no room for the next
@@ -1163,7 +1268,7 @@ moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, in
   const int64_t need = rows * ((slice + 63) / 64 * 128 + kSmallPad);
   a.ring = need < kSmallRows ? static_cast<int>((need + 255) / 256 * 256) : kSmallRows;
   if (a.ring < kSmallLeast) a.ring = kSmallLeast;
-  const int least = a.T > kFewTokens && ctas <= sms ? kSmallAlone : 0;
+  const int least = a.T > kFewShrink && ctas <= sms ? kSmallAlone : 0;
   return launch_cluster<lora_shrink_small_kernel>(kSmallAlone, grid, kSmallThreads, splits, a.ring > least ? a.ring : least, stream, a,
                         static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(lora_a));
 }
@@ -1251,7 +1356,7 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   // BN 256: four stages, or three beside a u of rank above 64. BN 128 over whole tiles: three (with six, which keep
   // the shrink kernel's CTAs off the SM, no block came sooner)
   a.stages = BN > 128 ? (rblocks <= 1 ? 4 : 3)
-             : SPLIT  ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, a.T > kFewTokens ? kSplitRing : kSplitRingFew)
+             : SPLIT  ? ring_stages(a.stage, (a.kblocks + splits - 1) / splits, a.T > kFewShrink ? kSplitRing : kSplitRingFew)
                       : 3;
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
   if (tiles > 0x3fffffffll / kLMaxSplit) return MOE_EINVAL;
@@ -1277,6 +1382,15 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
     return MOE_ECUDA;
   return launch_cluster<lora_gemm_kernel<BN, SPLIT>>(kLSmemMax - kLStatic, dim3(static_cast<unsigned>(grid)), kGemmLThreads,
                                                      SPLIT ? splits : 1, smem, stream, mx, mw, mu, mb, a);
+}
+
+// The projection of one token: two CTAs an SM, as far as their rows go.
+moe_status launch_one(LoraArgs a, const void *x, const void *w, const void *lora_b, int sms, cudaStream_t stream) {
+  a.own = (a.N + 2 * sms - 1) / (2 * sms);
+  if (a.own > kOneRows) a.own = kOneRows;
+  return launch_cluster<lora_one_kernel>(0, dim3(static_cast<unsigned>((a.N + a.own - 1) / a.own)), kOneThreads, 1, 0, stream, a,
+                                         static_cast<const uint4 *>(x), static_cast<const uint4 *>(w),
+                                         static_cast<const uint4 *>(lora_b));
 }
 
 }  // namespace
@@ -1324,6 +1438,7 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
     const moe_status st = launch_shrink(a, x, lora_a, sms, cs);
     if (st != MOE_OK) return st;
   }
+  if (T == 1) return launch_one(a, x, w, lora_b, sms, cs);
   int splits = 1;
   switch (tile_width(a, sms, &splits)) {
     case 256:

@@ -112,6 +112,13 @@ def test_long_rows_and_every_split(T, K, N, r, A, mix):
     check(T, K, N, r, A, mix)
 
 
+@pytest.mark.parametrize("mix", ["one", "none"])
+@pytest.mark.parametrize("K,N,r,A", [(8, 8, 8, 1), (520, 4872, 24, 3), (2056, 8, 256, 2), (4104, 4112, 64, 5),
+                                     (264, 40008, 8, 4), (16400, 72, 136, 2)])
+def test_one_token(K, N, r, A, mix):
+    check(1, K, N, r, A, mix)
+
+
 @pytest.mark.parametrize("mix", ["none", "one"])
 @pytest.mark.parametrize("T", [3, 200, 2000])
 def test_no_and_one_adapter_in_use(T, mix):
