@@ -521,10 +521,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
 }
 
 // ---------------------------------------------------------------------------
-// u for few tokens: one cluster of CTAs per (adapter, 16 of its rows), which
+// u for few tokens: one cluster of CTAs per (adapter in use, 16 of its rows), which
 // takes its tokens 16 at a time, K split over the cluster. The tensor-core tiles
 // above take 128 tokens whether they use the adapter or not; here a token's x row
 // meets only its own adapter.
+// With more adapters than tokens there is a cluster per token instead, and the
+// first token of an adapter takes all of its tokens: clusters without work cost
+// 29 us for one token and 1000 adapters.
 // Bound by the latency of the loads, beside the projection's stream of W: a CTA
 // asks for all of its rows' pieces at once, with one bulk copy a row into shared
 // memory (two halves in turn where they do not fit). Loading them to registers,
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   __shared__ uint64_t full[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = static_cast<int>(lora_cluster_size()), split = static_cast<int>(lora_cluster_rank());
-  const int ad = blockIdx.x / splits, n0 = blockIdx.y * kSmallN;
+  const int first_of = blockIdx.x / splits, n0 = blockIdx.y * kSmallN;
   if (tid == 0) {
     mbar_init(full, 1);
     mbar_init(full + 1, 1);
@@ -583,16 +586,20 @@ __global__ void __launch_bounds__(kSmallThreads)
   // this adapter's tokens, in token order
   const int id = tid < a.T ? __ldg(a.adapter + tid) : -1;
   if ((id < -1 || id >= a.adapters) && blockIdx.x == 0 && n0 == 0 && blockIdx.z == 0) latch_error(a.err, MOE_EINVAL);
-  const unsigned users = __ballot_sync(0xffffffffu, id == ad);
+  // a cluster per adapter, or, with more adapters than tokens, per token: the first one of its adapter takes all
+  const int ad = a.adapters > a.T ? __ldg(a.adapter + first_of) : first_of;
+  const bool uses = id == ad && ad >= 0 && ad < a.adapters;
+  const unsigned users = __ballot_sync(0xffffffffu, uses);
   if (lane == 0) counts[warp] = __popc(users);
-  __syncthreads();
+  const bool taken = __syncthreads_or(a.adapters > a.T && uses && tid < first_of) != 0;
   int total = 0, at = __popc(users & ((1u << lane) - 1u));
 #pragma unroll
   for (int w = 0; w < kSmallWarps; ++w) {
     if (w < warp) at += counts[w];
     total += counts[w];
   }
-  if (id == ad) token[at] = tid;
+  if (taken) total = 0;
+  if (uses) token[at] = tid;
   __syncthreads();
 
   // this CTA's K elements, its passes of 16 tokens (the same in every CTA of the cluster) and the steps of a pass
@@ -1255,12 +1262,12 @@ constexpr int kSmallLeast = 12 * 1024;  // a half holds 64 elements of the most 
 static_assert(small_chunk(kSmallLeast / 2, kSmallM + kSmallN) >= 64 && kSmallRows % 256 == 0 && kSmallLeast % 256 == 0, "");
 
 moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
-  if (a.adapters > 0x7fffffff / kLMaxCluster) return MOE_EINVAL;
   const int nchunks = (a.rank + kSmallN - 1) / kSmallN;
-  const int64_t busy = static_cast<int64_t>(a.adapters < a.T ? a.adapters : a.T) * nchunks;  // clusters with work, at most
+  const int clusters = a.adapters < a.T ? a.adapters : a.T;  // for each 16 rows
+  const int64_t busy = static_cast<int64_t>(clusters) * nchunks;
   int splits = kLMaxCluster;
   while (splits > 1 && busy * splits > sms) splits >>= 1;
-  const dim3 grid(static_cast<unsigned>(a.adapters * splits), static_cast<unsigned>(nchunks),
+  const dim3 grid(static_cast<unsigned>(clusters * splits), static_cast<unsigned>(nchunks),
                   static_cast<unsigned>((a.T + kSmallTokensPerCta - 1) / kSmallTokensPerCta));
   const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y * grid.z;
   const int rows = (a.rank < kSmallN ? a.rank : kSmallN) + (a.T < kSmallM ? a.T : kSmallM);

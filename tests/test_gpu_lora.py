@@ -105,6 +105,7 @@ def test_many_tiles(T, K, N, r, A, mix):
     (128, 4104, 520, 32, 128, "tokens"), (9, 40, 72, 24, 9, "tokens"), (33, 4096, 8, 256, 2, "one"),
     (256, 1024, 2048, 16, 8, "runs"), (1000, 4096, 1024, 24, 5, "runs"), (389, 7168, 2048, 48, 6, "tokens"),
     (700, 2056, 1032, 32, 20, "tokens"), (16, 2048, 4104, 16, 4, "tokens"), (60, 1024, 7168, 8, 60, "tokens"),
+    (20, 520, 136, 16, 300, "tokens"), (20, 520, 136, 40, 21, "one"), (100, 264, 72, 8, 101, "tokens"),
 ])
 def test_long_rows_and_every_split(T, K, N, r, A, mix):
     """Rows whose pieces take several rounds of loads and tokens that take several passes; shapes at which a tile's K
