@@ -35,8 +35,9 @@ namespace moe {
 namespace {
 
 constexpr int kRankThreads = 1024;
-constexpr int kRankMaxCluster = 8;
+constexpr int kRankMaxCluster = 16;  // (more than 8 have to be allowed for the kernel)
 constexpr int kRankMaxExperts = 8192;
+constexpr int kRankMaxBits = 13;
 constexpr int kRankSmem = 200 * 1024;
 constexpr int kRankBatch = 8;  // loads in flight per lane
 
@@ -45,15 +46,15 @@ struct RankArgs {
   int32_t *region_offsets;  // [E * R + 1]
   int32_t *tok_packed;      // [R * T * k]
   int32_t *err;
-  int64_t n;                // R * T * k
-  int64_t per_rank;         // T * k
-  int64_t per_warp;         // choices of a warp's piece: a multiple of 32
+  uint32_t n;               // R * T * k, below 2^31
+  uint32_t per_rank;        // T * k
+  uint32_t per_warp;        // choices of a warp's piece: a multiple of 32
   int E, R, warps;          // warps: warps per CTA that take a piece
   int bits;                 // bits of an expert's index
 };
 
 // The expert of choice i, or -1 for a masked or invalid one.
-__device__ __forceinline__ int expert_at(const RankArgs &a, int64_t i, int64_t end, bool *bad) {
+__device__ __forceinline__ int expert_at(const RankArgs &a, uint32_t i, uint32_t end, bool *bad) {
   if (i >= end) return -1;
   const int e = __ldg(a.topk_idx + i);
   if (e >= 0 && e < a.E) return e;
@@ -64,10 +65,11 @@ __device__ __forceinline__ int expert_at(const RankArgs &a, int64_t i, int64_t e
 // The lanes whose expert equals this lane's (e < 0: none, and not asked for).
 __device__ __forceinline__ unsigned same_expert(int e, int bits) {
   unsigned same = __ballot_sync(0xffffffffu, e >= 0);
-  for (int b = 0; b < bits; ++b) {
-    const bool bit = (e >> b) & 1;
-    const unsigned set = __ballot_sync(0xffffffffu, bit);
-    same &= bit ? set : ~set;
+#pragma unroll
+  for (int b = 0; b < kRankMaxBits; ++b) {
+    if (b >= bits) break;
+    const int bit = static_cast<int>(static_cast<unsigned>(e) << (31 - b)) >> 31;  // 0 or -1
+    same &= ~(__ballot_sync(0xffffffffu, bit != 0) ^ static_cast<unsigned>(bit));
   }
   return same;
 }
@@ -87,12 +89,12 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(RankArgs a) {
   for (int i = tid; i < a.warps * a.E; i += kRankThreads) hist[i] = 0;
   __syncthreads();
 
-  const int64_t c0 = min((static_cast<int64_t>(cta) * a.warps + warp) * a.per_warp, a.n);
-  const int64_t c1 = warp < a.warps ? min(c0 + a.per_warp, a.n) : c0;
+  const uint32_t c0 = min((static_cast<uint32_t>(cta) * a.warps + warp) * a.per_warp, a.n);
+  const uint32_t c1 = warp < a.warps ? min(c0 + a.per_warp, a.n) : c0;
   int32_t *mine = hist + warp * a.E;
   bool bad = false;
   int e[kRankBatch];
-  for (int64_t i0 = c0; i0 < c1; i0 += 32 * kRankBatch) {
+  for (uint32_t i0 = c0; i0 < c1; i0 += 32 * kRankBatch) {
 #pragma unroll
     for (int b = 0; b < kRankBatch; ++b) e[b] = expert_at(a, i0 + b * 32 + lane, c1, &bad);
 #pragma unroll
@@ -147,17 +149,17 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(RankArgs a) {
   __syncthreads();
 
   // the choices of the piece in order; a piece of one batch still has its experts in registers
-  int64_t src = c0 < c1 ? c0 / a.per_rank : 0;
-  int64_t bound = src * a.per_rank;  // the next first choice of a source rank
+  uint32_t src = c0 < c1 ? c0 / a.per_rank : 0;
+  uint32_t bound = src * a.per_rank;  // the next first choice of a source rank
   if (bound < c0) bound += a.per_rank, ++src;
-  for (int64_t i0 = c0; i0 < c1; i0 += 32 * kRankBatch) {
+  for (uint32_t i0 = c0; i0 < c1; i0 += 32 * kRankBatch) {
     if (c1 - c0 > 32 * kRankBatch) {
 #pragma unroll
       for (int b = 0; b < kRankBatch; ++b) e[b] = expert_at(a, i0 + b * 32 + lane, c1, &bad);
     }
 #pragma unroll
     for (int b = 0; b < kRankBatch; ++b) {
-      const int64_t c = i0 + b * 32;
+      const uint32_t c = i0 + b * 32;
       if (c >= c1) break;  // the whole warp
       // the group's choices, cut where a source rank begins
       for (int lo = 0; lo < 32 && c + lo < c1;) {
@@ -334,8 +336,12 @@ __global__ void __launch_bounds__(kUnsortGradMaxWarps * 32) unsort_grad_kernel(U
   }
 }
 
-// Cluster shape of the ranking: a CTA per 1024 choices, one a lane, as far as
-// clusters go (8192 choices of 256 experts: 15.8 us with one, 7.6 us with eight).
+// Cluster shape of the ranking: a CTA per 512 choices, one a lane of 16 warps, as
+// far as clusters go: handing out the positions is bound by instructions, about
+// 0.8 us for a group of 32 choices in each of a CTA's warps. 8192 choices of 256
+// experts: 15.8 us with one CTA, 7.6 with eight of 32 warps. A whole sort of 128
+// elements a row with eight and with sixteen CTAs: 65536 choices 15.4 and 12.5
+// us, a million 207 and 128 us.
 moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_offsets, int32_t *tok_packed,
                        int32_t *err, cudaStream_t stream) {
   if (s.E > kRankMaxExperts) return MOE_EINVAL;
@@ -357,8 +363,12 @@ moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_
   int warps = kRankSmem / 4 / s.E - 2;
   if (warps > kRankThreads / 32) warps = kRankThreads / 32;
   if (warps < 1) return MOE_EINVAL;
-  int64_t ctas = (n + 1023) / 1024;
+  int64_t ctas = (n + 511) / 512;
   if (ctas > kRankMaxCluster) ctas = kRankMaxCluster;
+  if (ctas > 8 && cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return MOE_ECUDA;
+  const int64_t needed = ((n + 31) / 32 + ctas - 1) / ctas;
+  if (warps > needed) warps = static_cast<int>(needed);
   const int64_t pieces = ctas * warps;
   const int64_t per_warp = ((n + pieces - 1) / pieces + 31) / 32 * 32;
   const size_t smem = static_cast<size_t>(warps + 2) * s.E * sizeof(int32_t);
@@ -367,8 +377,8 @@ moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_
     return MOE_ECUDA;
   int bits = 0;
   while ((1 << bits) < s.E) ++bits;
-  RankArgs a{topk_idx, region_offsets, tok_packed, err, n, static_cast<int64_t>(s.T) * s.k, per_warp,
-             s.E, s.R, warps, bits};
+  RankArgs a{topk_idx, region_offsets, tok_packed, err, static_cast<uint32_t>(n),
+             static_cast<uint32_t>(static_cast<int64_t>(s.T) * s.k), static_cast<uint32_t>(per_warp), s.E, s.R, warps, bits};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(kRankThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;

@@ -128,6 +128,18 @@ def test_sort_matches_the_dispatch_path(R, T, H, E, k, masked, dtype):
     assert bool((px[m:] == POISON_BYTE).all()) and bool((ps[m:] == -7.0).all())
 
 
+@pytest.mark.parametrize("R,T,E,k,masked", [(7, 1111, 301, 7, 0.1), (32, 61, 8192, 5, 0.0), (1, 40000, 2, 1, 0.3),
+                                            (33, 3, 33, 4, 0.0), (3, 171, 258, 1, 0.0)])
+def test_ranking_of_many_choices(R, T, E, k, masked):
+    """As many CTAs as a cluster takes, source ranks that begin inside a group of 32 choices, experts of 1 to 13 bits."""
+    require_gpu()
+    idx = choices(R, T, E, k, E + T, masked)
+    off, _, _, tok, status = run_sort(make(R, T, 8, E, k), idx, bf16((R * T, 8), 3))
+    t_ref, o_ref, _ = plain_order(idx, R, E)
+    assert status == B.MOE_OK
+    assert np.array_equal(tok.cpu().numpy(), t_ref) and np.array_equal(off.cpu().numpy(), o_ref)
+
+
 def test_sort_repeated_experts_keep_choice_order():
     require_gpu()
     d = make(2, 50, 32, 6, 6)
