@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(256) sort_rows_kernel(RowArgs a) {
 // The sum over the row is a shuffle tree per warp and the warps in order, the
 // same on every run. dout is read again for each choice, from L1 after the
 // first: with it in registers a CTA of 8 warps would hold one width of row only.
-// 8192 tokens of 4096 elements, two choices (335 MB): 53 us, 6.3 TB/s, HBM.
+// 8192 tokens of 4096 elements, two choices (335 MB): 49 us, 6.8 TB/s, HBM. At 32
+// registers a thread eight CTAs fit an SM (at 40 it took 53 us); several choices
+// at a time took more registers and longer.
 struct UnsortGradArgs {
   const uint16_t *y;
   const int32_t *tok_packed;
@@ -308,21 +310,24 @@ __global__ void __launch_bounds__(kUnsortGradMaxWarps * 32) unsort_grad_kernel(U
   grid_dependency_wait();
   const uint4 *g = reinterpret_cast<const uint4 *>(a.gout) + t * a.V;
   for (int j = 0; j < a.k; ++j) {
-    const int32_t p = __ldg(a.tok_packed + t * a.k + j);
-    if (p >= a.nrows && tid == 0) latch_error(a.err, MOE_EINVAL);
+    int32_t p = __ldg(a.tok_packed + t * a.k + j);
+    const float w = __ldg(a.weights + t * a.k + j);
+    if (p >= a.nrows) {
+      if (tid == 0) latch_error(a.err, MOE_EINVAL);
+      p = -1;
+    }
     float dot = 0.0f;
-    if (p >= 0 && p < a.nrows) {
-      const float w = __ldg(a.weights + t * a.k + j);
-      const uint4 *y = reinterpret_cast<const uint4 *>(a.y) + static_cast<int64_t>(p) * a.V;
-      uint4 *gy = reinterpret_cast<uint4 *>(a.gy) + static_cast<int64_t>(p) * a.V;
-      for (int v = tid; v < a.V; v += nt) {
-        float gf[8], yf[8];
-        unpack_bf16x8(__ldg(g + v), gf);
-        unpack_bf16x8(__ldcs(y + v), yf);
+    const uint4 *y = reinterpret_cast<const uint4 *>(a.y) + static_cast<int64_t>(p) * a.V;
+    uint4 *gy = reinterpret_cast<uint4 *>(a.gy) + static_cast<int64_t>(p) * a.V;
+    for (int v = tid; v < a.V; v += nt) {
+      if (p < 0) break;
+      const uint4 yv = __ldcs(y + v);
+      float gf[8], yf[8];
+      unpack_bf16x8(__ldg(g + v), gf);
+      unpack_bf16x8(yv, yf);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) dot = fmaf(yf[q], gf[q], dot);
-        __stcs(gy + v, scale_bf16x8(gf, w));
-      }
+      for (int q = 0; q < 8; ++q) dot = fmaf(yf[q], gf[q], dot);
+      __stcs(gy + v, scale_bf16x8(gf, w));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
