@@ -18,7 +18,7 @@
 //     stacked rows of up to 128 / rank adapters that occur among them (or one
 //     adapter's, if it has more): a token's own columns are picked in the
 //     epilogue. in is split over a cluster of CTAs whose partial sums meet in
-//     distributed shared memory in a fixed order. Up to 128 tokens take
+//     distributed shared memory in a fixed order. Few tokens take
 //     lora_shrink_small_kernel: 16 tokens of one adapter at a time.
 //   lora_gemm_kernel    the projection with its extra K blocks. Tiles of 128
 //     tokens x BN outputs; TMA brings x and W (then u and B_a) tiles, one lane
@@ -550,7 +550,7 @@ constexpr int kSmallThreads = 256;
 constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kSmallM = 16, kSmallN = 16;
 constexpr int kSmallPad = 64;  // bytes between rows in shared memory
-constexpr int kSmallTokensPerCta = 64;  // calls of more tokens have more CTAs per adapter, which exit where there is nothing to do
+constexpr int kSmallTokens = 64;  // of a call, at most
 
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   extern __shared__ __align__(128) uint8_t small_rows[];  // a.ring bytes: rows of A_a, then of x
   __shared__ float part[kSmallWarps][kSmallM][kSmallN + 1];
   __shared__ __align__(16) float recv[2][kLMaxCluster][kSmallM * kSmallN];  // the parts of the sums that this CTA owns
-  __shared__ int32_t token[kLBM];
+  __shared__ int32_t token[kSmallTokens];
   __shared__ int32_t counts[kSmallWarps];
   __shared__ uint64_t full[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   grid_dependents_launch();  // the projection finds what this kernel's predecessors wrote
   // this adapter's tokens, in token order
   const int id = tid < a.T ? __ldg(a.adapter + tid) : -1;
-  if ((id < -1 || id >= a.adapters) && blockIdx.x == 0 && n0 == 0 && blockIdx.z == 0) latch_error(a.err, MOE_EINVAL);
+  if ((id < -1 || id >= a.adapters) && blockIdx.x == 0 && n0 == 0) latch_error(a.err, MOE_EINVAL);
   // a cluster per adapter, or, with more adapters than tokens, per token: the first one of its adapter takes all
   const int ad = a.adapters > a.T ? __ldg(a.adapter + first_of) : first_of;
   const bool uses = id == ad && ad >= 0 && ad < a.adapters;
@@ -606,17 +606,16 @@ __global__ void __launch_bounds__(kSmallThreads)
   const int pieces = (a.K + 31) / 32;
   const int e0 = static_cast<int>(static_cast<int64_t>(pieces) * split / splits) * 32;
   const int len = max(min(static_cast<int>(static_cast<int64_t>(pieces) * (split + 1) / splits) * 32, a.K) - e0, 0);
-  const int first = blockIdx.z * kSmallM, every = gridDim.z * kSmallM;
-  const int passes = total > first ? (total - first + every - 1) / every : 0;
+  const int passes = (total + kSmallM - 1) / kSmallM;
   const int nr = min(kSmallN, a.rank - n0);                  // rows of A_a
-  const int most = nr + min(kSmallM, max(total - first, 0));  // and of x
+  const int most = nr + min(kSmallM, total);  // and of x
   const bool whole = passes == 1 && len <= small_chunk(a.ring, most);
   const int chunk = whole ? (len + 63) / 64 * 64 : small_chunk(a.ring / 2, most);
   const int chunks = len > 0 ? (len + chunk - 1) / chunk : 0, steps = passes * chunks;
   const int pitch = chunk * 2 + kSmallPad;
   // asks for step s into half s & 1 (warp 0)
   const auto load = [&](int s) {
-    const int m0 = first + s / chunks * every, o = s % chunks * chunk;
+    const int m0 = s / chunks * kSmallM, o = s % chunks * chunk;
     const int nt = min(total - m0, kSmallM);
     const uint32_t bytes = static_cast<uint32_t>(min(chunk, len - o)) * 2;
     uint8_t *dst = small_rows + (s & 1) * (a.ring / 2);
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   lora_cluster_wait();
 
   for (int pass = 0, s = 0; pass < passes; ++pass) {
-    const int m0 = first + pass * every;
+    const int m0 = pass * kSmallM;
     const int nt = min(total - m0, kSmallM);
     float acc[2][4] = {};
     for (int c = 0; c < chunks; ++c, ++s) {
@@ -717,7 +716,7 @@ struct GemmShared {
   int abort;
 };
 
-static_assert(kSmallThreads >= kLBM, "a thread per token");
+static_assert(kSmallThreads >= kSmallTokens, "a thread per token");
 static_assert(kSmallThreads == kSmallM * kSmallN, "a thread per sum");
 static_assert(sizeof(GemmShared) <= kLStatic && sizeof(ShrinkShared) <= kLStatic, "");
 
@@ -1261,15 +1260,28 @@ constexpr int kSmallAlone = 90 * 1024;
 constexpr int kSmallLeast = 12 * 1024;  // a half holds 64 elements of the most rows
 static_assert(small_chunk(kSmallLeast / 2, kSmallM + kSmallN) >= 64 && kSmallRows % 256 == 0 && kSmallLeast % 256 == 0, "");
 
+// Whether u is computed 16 tokens of an adapter at a time: up to 16 tokens, one
+// pass each; up to 64 where they are likely to use enough adapters. Every further
+// pass of an adapter's tokens costs 3 us or more, while the tensor-memory tiles
+// take all of them at once. Which adapters are used is not known here, so this
+// goes by how many there are. Measured, small tiles and tensor memory, 4096 ->
+// 4096: 16 tokens of one adapter 12.3 and 14.4 us, 20 of one 17.4 and 14.3, 24 of
+// two 12.7 and 14.7, 64 of 16 19.7 and 20.4 (four used: 21.7 and 19.6), 64 of 8
+// 20.2 and 19.2 (24.5 and 18.4), 128 of 32 20.5 and 24.0 (27.4 and 21.8); 64
+// tokens 7168 -> 2048 of 32: 15.9 and 20.7.
+bool few_tokens(const LoraArgs &a) {
+  if (a.T <= kSmallM) return true;
+  return a.T <= 2 * kSmallM ? a.adapters >= 2 : a.T <= kSmallTokens && a.T <= 4 * static_cast<int64_t>(a.adapters);
+}
+
 moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
   const int nchunks = (a.rank + kSmallN - 1) / kSmallN;
   const int clusters = a.adapters < a.T ? a.adapters : a.T;  // for each 16 rows
   const int64_t busy = static_cast<int64_t>(clusters) * nchunks;
   int splits = kLMaxCluster;
   while (splits > 1 && busy * splits > sms) splits >>= 1;
-  const dim3 grid(static_cast<unsigned>(clusters * splits), static_cast<unsigned>(nchunks),
-                  static_cast<unsigned>((a.T + kSmallTokensPerCta - 1) / kSmallTokensPerCta));
-  const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y * grid.z;
+  const dim3 grid(static_cast<unsigned>(clusters * splits), static_cast<unsigned>(nchunks));
+  const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y;
   const int rows = (a.rank < kSmallN ? a.rank : kSmallN) + (a.T < kSmallM ? a.T : kSmallM);
   const int64_t slice = static_cast<int64_t>((a.K + 31) / 32 + splits - 1) / splits * 32;  // a CTA's K elements, at most
   const int64_t need = rows * ((slice + 63) / 64 * 128 + kSmallPad);
@@ -1281,7 +1293,7 @@ moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, in
 }
 
 moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
-  if (a.T <= kLBM) return launch_shrink_small(a, x, lora_a, sms, stream);
+  if (few_tokens(a)) return launch_shrink_small(a, x, lora_a, sms, stream);
   const int most = a.adapters < a.T ? (a.adapters < kLBM ? a.adapters : kLBM) : (a.T < kLBM ? a.T : kLBM);
   // up to two CTAs an SM (8192 tokens: the whole call takes 184 us so, 189 us with one)
   int splits = kLMaxCluster;

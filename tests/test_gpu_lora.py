@@ -106,6 +106,7 @@ def test_many_tiles(T, K, N, r, A, mix):
     (256, 1024, 2048, 16, 8, "runs"), (1000, 4096, 1024, 24, 5, "runs"), (389, 7168, 2048, 48, 6, "tokens"),
     (700, 2056, 1032, 32, 20, "tokens"), (16, 2048, 4104, 16, 4, "tokens"), (60, 1024, 7168, 8, 60, "tokens"),
     (20, 520, 136, 16, 300, "tokens"), (20, 520, 136, 40, 21, "one"), (100, 264, 72, 8, 101, "tokens"),
+    (31, 16392, 264, 16, 2, "one"), (64, 4104, 72, 40, 16, "one"), (63, 12296, 136, 8, 70, "one"), (64, 2056, 72, 256, 20, "tokens"),
 ])
 def test_long_rows_and_every_split(T, K, N, r, A, mix):
     """Rows whose pieces take several rounds of loads and tokens that take several passes; shapes at which a tile's K
