@@ -1288,8 +1288,10 @@ moe_status launch_shrink_small(LoraArgs a, const void *x, const void *lora_a, in
   a.ring = need < kSmallRows ? static_cast<int>((need + 255) / 256 * 256) : kSmallRows;
   if (a.ring < kSmallLeast) a.ring = kSmallLeast;
   const int least = a.T > kFewShrink && ctas <= sms ? kSmallAlone : 0;
-  return launch_cluster<lora_shrink_small_kernel>(kSmallAlone, grid, kSmallThreads, splits, a.ring > least ? a.ring : least, stream, a,
-                        static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(lora_a));
+  return launch_cluster<lora_shrink_small_kernel>(kSmallAlone, grid, kSmallThreads, splits,
+                                                  a.ring > least ? a.ring : least, stream, a,
+                                                  static_cast<const __nv_bfloat16 *>(x),
+                                                  static_cast<const __nv_bfloat16 *>(lora_a));
 }
 
 moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms, cudaStream_t stream) {
@@ -1323,7 +1325,8 @@ moe_status launch_shrink(LoraArgs a, const void *x, const void *lora_a, int sms,
     return MOE_ECUDA;
   const int64_t grid = static_cast<int64_t>(a.mtiles) * a.groups * splits;
   if (grid > 0x7fffffffll) return MOE_EINVAL;
-  return launch_cluster<lora_shrink_kernel>(kLSmemMax - kLStatic, dim3(static_cast<unsigned>(grid)), kShrinkThreads, splits, smem, stream, mx, ma, a);
+  return launch_cluster<lora_shrink_kernel>(kLSmemMax - kLStatic, dim3(static_cast<unsigned>(grid)), kShrinkThreads, splits,
+                                            smem, stream, mx, ma, a);
 }
 
 // The projection's tiles: their width and the CTAs that share one's K, by the
