@@ -11,6 +11,7 @@ and a projection shared by all requests with each request's low-rank adapter.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import numpy as np
@@ -151,6 +152,10 @@ class LocalMoe:
     output back through moe_unsort_grad, the caller's expert gradient, moe_sort_grad and moe_gate_grad. shared runs
     the projection beside the experts with the adapters of the batch's requests. Every buffer is allocated once.
 
+    Each method runs on ``stream`` (None: the current one) whole, what it does with torch and expert_grad included.
+    The layer may have been made on another stream: the first call on a stream waits for that one's work up to then.
+    Methods called on different streams share the layer's buffers, and ordering them is the caller's part.
+
     tokens x hidden bf16 rows, num_experts experts of width inter (a multiple of 128 when the expert stage runs)."""
 
     def __init__(self, tokens: int, hidden: int, num_experts: int, topk: int, opts: B.MoeGateOpts, device="cuda",
@@ -171,46 +176,85 @@ class LocalMoe:
         self.packed_x, self.packed_y, self.out = rows(n, hidden), rows(n, hidden), rows(tokens, hidden)
         self.h = rows(n, inter) if inter else None
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.grad_y, self.grad_x = None, None  # allocated by the first backward
+        self.grad_y = self.grad_x = self.grad_weights = self.grad_logits = None  # allocated by the first backward
         self.u = self.shared_out = None        # by shared, for its shapes
+        self.device = self.err.device
+        self._streams = {}  # the streams that have used the buffers, by their handles
+        if dev.type == "cuda":
+            made_on = torch.cuda.current_stream(self.device)
+            self._made = made_on.record_event()
+            self._streams[made_on.cuda_stream] = made_on
+
+    def _on(self, stream):
+        """The context that a method runs in: ``stream`` is the current one there, and the layer's buffers may be used
+        on it. Handles are compared, since building a Stream object takes longer than a small kernel's launch."""
+        if self.device.type != "cuda":
+            return nullcontext()  # the binding refuses it
+        handle = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else stream.cuda_stream
+        if handle not in self._streams:
+            s = torch.cuda.current_stream(self.device) if stream is None else stream
+            with torch.cuda.stream(s):
+                # (a capture begins with nothing pending, and a captured stream may not wait for an event before it)
+                if not torch.cuda.is_current_stream_capturing():
+                    s.wait_event(self._made)
+            self._streams[handle] = s
+            self._keep_for([s])
+        return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    def _keep_for(self, streams):
+        """The layer's buffers are given out again, after the layer, only when these streams have passed them."""
+        for t in vars(self).values():
+            if isinstance(t, torch.Tensor):
+                for s in streams:
+                    t.record_stream(s)
 
     def route(self, logits, bias=None, stream=None):
-        B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err, stream)
+        with self._on(stream):
+            B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err)
 
     def sort(self, x, stream=None):
-        B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed,
-                   self.err, stream)
+        with self._on(stream):
+            B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed,
+                       self.err)
 
     def experts(self, weights, stream=None):
         """The expert stage on the sorted rows (weights: workloads.ExpertWeights)."""
-        B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up,
-                             self.h, self.err, stream)
-        B.moe_expert_down(self.desc, self.inter, self.region_offsets, self.h, weights.w_down, self.packed_y, self.err,
-                          stream)
+        with self._on(stream):
+            B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate,
+                                 weights.w_up, self.h, self.err)
+            B.moe_expert_down(self.desc, self.inter, self.region_offsets, self.h, weights.w_down, self.packed_y,
+                              self.err)
 
     def unsort(self, stream=None):
-        B.moe_unsort(self.desc, self.packed_y, self.tok_packed, self.topk_weights, self.out, self.err, stream)
+        with self._on(stream):
+            B.moe_unsort(self.desc, self.packed_y, self.tok_packed, self.topk_weights, self.out, self.err)
         return self.out
 
     def forward(self, x, logits, weights, bias=None, stream=None):
-        """x [tokens][hidden], logits [tokens][num_experts] -> the routed experts' output [tokens][hidden]."""
+        """x [tokens][hidden], logits [tokens][num_experts] -> the routed experts' output [tokens][hidden], a buffer of
+        the layer that the next forward writes again."""
         self.route(logits, bias, stream)
         self.sort(x, stream)
         self.experts(weights, stream)
         return self.unsort(stream)
 
     def backward(self, grad_out, logits, expert_grad, stream=None):
-        """The gradients of x and of the logits. expert_grad(packed_x, region_offsets, grad_y) is the caller's
-        gradient of the experts: from the gradient of packed_y to that of packed_x, row by row."""
-        if self.grad_y is None:
-            self.grad_y, self.grad_x = torch.zeros_like(self.packed_y), torch.empty_like(self.out)
-            self.grad_weights, self.grad_logits = torch.empty_like(self.topk_weights), torch.empty_like(logits)
-        B.moe_unsort_grad(self.desc, self.packed_y, self.tok_packed, self.topk_weights, grad_out, self.grad_y,
-                          self.grad_weights, self.err, stream)
-        grad_packed = expert_grad(self.packed_x, self.region_offsets, self.grad_y)
-        B.moe_sort_grad(self.desc, grad_packed, self.tok_packed, self.grad_x, self.err, stream)
-        B.moe_gate_grad(self.desc, self.opts, logits, self.topk_idx, self.grad_weights, self.grad_logits, self.err,
-                        stream)
+        """The gradients of x and of the logits, in buffers of the layer that the next backward writes again.
+        expert_grad(packed_x, region_offsets, grad_y) is the caller's gradient of the experts: from the gradient of
+        packed_y to that of packed_x, row by row, both bf16 [tokens * topk][hidden]. It is called with ``stream`` as
+        the current one. Rows at or above region_offsets' last entry belong to no choice: packed_x and grad_y hold
+        nothing of this batch there."""
+        with self._on(stream):
+            if self.grad_y is None:
+                self.grad_y, self.grad_x = torch.zeros_like(self.packed_y), torch.empty_like(self.out)
+                self.grad_weights = torch.empty_like(self.topk_weights)
+                self.grad_logits = torch.empty_like(logits)
+                self._keep_for(self._streams.values())
+            B.moe_unsort_grad(self.desc, self.packed_y, self.tok_packed, self.topk_weights, grad_out, self.grad_y,
+                              self.grad_weights, self.err)
+            grad_packed = expert_grad(self.packed_x, self.region_offsets, self.grad_y)
+            B.moe_sort_grad(self.desc, grad_packed, self.tok_packed, self.grad_x, self.err)
+            B.moe_gate_grad(self.desc, self.opts, logits, self.topk_idx, self.grad_weights, self.grad_logits, self.err)
         return self.grad_x, self.grad_logits
 
     def shared(self, x, w, lora_a, lora_b, scales, adapter, stream=None):
@@ -224,4 +268,5 @@ class LocalMoe:
         return self.shared_out
 
     def error(self, stream=None) -> int:
-        return B.moe_get_error(self.err, stream)
+        with self._on(stream):
+            return B.moe_get_error(self.err)
