@@ -150,7 +150,8 @@ class LocalMoe:
 
     forward: logits -> moe_gate -> moe_sort -> expert stage -> moe_unsort. backward takes the gradient of the
     output back through moe_unsort_grad, the caller's expert gradient, moe_sort_grad and moe_gate_grad. shared runs
-    the projection beside the experts with the adapters of the batch's requests. Every buffer is allocated once.
+    the projection beside the experts with the adapters of the batch's requests. The buffers of forward and backward
+    are allocated once.
 
     Each method runs on ``stream`` (None: the current one) whole, what it does with torch and expert_grad included.
     The layer may have been made on another stream: the first call on a stream waits for that one's work up to then.
@@ -177,7 +178,7 @@ class LocalMoe:
         self.h = rows(n, inter) if inter else None
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.grad_y = self.grad_x = self.grad_weights = self.grad_logits = None  # allocated by the first backward
-        self.u = self.shared_out = None        # by shared, for its shapes
+        self.u = None  # the last shared's scratch
         self.device = self.err.device
         self._streams = {}  # the streams that have used the buffers, by their handles
         if dev.type == "cuda":
@@ -258,14 +259,15 @@ class LocalMoe:
         return self.grad_x, self.grad_logits
 
     def shared(self, x, w, lora_a, lora_b, scales, adapter, stream=None):
-        """x w^T [tokens][out] with each token's adapter beside it (moe_lora_linear)."""
+        """x w^T [tokens][out] with each token's adapter beside it (moe_lora_linear). The result is the caller's own:
+        it and the scratch u are new in each call, so that two projections, on one stream or on two, share nothing."""
         A, rank, _ = lora_a.shape
-        if self.u is None or self.u.shape != (x.shape[0], rank) or self.shared_out.shape[1] != w.shape[0]:
+        with self._on(stream):
             self.u = torch.empty((x.shape[0], rank), dtype=torch.bfloat16, device=x.device)
-            self.shared_out = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
-        desc = B.MoeLoraDesc(x.shape[0], x.shape[1], w.shape[0], rank, A, 0)
-        B.moe_lora_linear(desc, x, w, lora_a, lora_b, scales, adapter, self.u, self.shared_out, self.err, stream)
-        return self.shared_out
+            out = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
+            desc = B.MoeLoraDesc(x.shape[0], x.shape[1], w.shape[0], rank, A, 0)
+            B.moe_lora_linear(desc, x, w, lora_a, lora_b, scales, adapter, self.u, out, self.err)
+        return out
 
     def error(self, stream=None) -> int:
         with self._on(stream):

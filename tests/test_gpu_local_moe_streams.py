@@ -106,6 +106,55 @@ def test_memory_of_a_dropped_layer_is_not_given_out_while_its_stream_works():
     assert all(bool((o == 7.0).all()) for o in other)
 
 
+def projection(N, r, seed):
+    g = torch.Generator().manual_seed(seed)
+
+    def draw(*shape):
+        return torch.randn(shape, generator=g).to(torch.bfloat16).cuda()
+
+    return draw(N, H), draw(3, r, H), draw(3, N, r)
+
+
+def test_shared_of_two_shapes_on_a_side_stream():
+    """What the first projection still writes on the side stream is not given out to the current one."""
+    require_gpu()
+    x, _, _ = data()
+    ids = (torch.arange(T) % 4 - 1).to(torch.int32).cuda()
+    layer = P.LocalMoe(T, H, E, K, opts(), "cuda:0")
+    first, second = projection(512, 16, 5), projection(264, 8, 6)
+    want = [layer.shared(x, *p, None, ids).clone() for p in (first, second)]
+    layer = P.LocalMoe(T, H, E, K, opts(), "cuda:0")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    y = layer.shared(x, *first, None, ids, stream=side)
+    shape = y.shape
+    del y
+    got = layer.shared(x, *second, None, ids, stream=side)
+    other = [torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda:0") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert layer.error() == B.MOE_OK and torch.equal(got, want[1])
+    assert all(bool((o == 7.0).all()) for o in other)
+
+
+def test_shared_on_two_streams_at_a_time():
+    require_gpu()
+    x, _, _ = data()
+    ids = (torch.arange(T) % 4 - 1).to(torch.int32).cuda()
+    layer = P.LocalMoe(T, H, E, K, opts(), "cuda:0")
+    ps = [projection(512, 16, 5), projection(512, 16, 6)]
+    want = [layer.shared(x, *p, None, ids).clone() for p in ps]
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(sides[0]):
+        torch.cuda._sleep(BUSY)
+    got = [layer.shared(x, *p, None, ids, stream=s) for p, s in zip(ps, sides)]
+    torch.cuda.synchronize()
+    assert layer.error() == B.MOE_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_a_captured_layer_replays():
     """Forward and backward captured together, on a stream that did not make the layer, and replayed on new inputs."""
     require_gpu()
