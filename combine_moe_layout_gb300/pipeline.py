@@ -11,6 +11,7 @@ and a projection shared by all requests with each request's low-rank adapter.
 """
 from __future__ import annotations
 
+import math
 from contextlib import nullcontext
 from dataclasses import dataclass
 
@@ -145,6 +146,21 @@ class MoeStep:
         return B.moe_get_error(self.buf.err, stream)
 
 
+def _expect(name: str, t, dtype, *shape):
+    """A tensor argument of LocalMoe: its type and sizes, before a kernel reads by them. Leading sizes may be joined or
+    split (rows of [batch][sequence][hidden] are as good as [tokens][hidden]); with a size of None, any, they are as
+    listed."""
+    good = isinstance(t, torch.Tensor) and t.dtype == dtype
+    if good and None in shape:
+        good = t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape))
+    elif good:
+        good = t.dim() > 0 and t.numel() == math.prod(shape) and (len(shape) == 1 or t.shape[-1] == shape[-1])
+    if not good:
+        what = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else repr(t)
+        sizes = ", ".join("any" if n is None else str(n) for n in shape)
+        raise ValueError(f"LocalMoe: {name} is {what}, not {dtype} ({sizes})")
+
+
 class LocalMoe:
     """An MoE layer of one device.
 
@@ -209,17 +225,31 @@ class LocalMoe:
                 for s in streams:
                     t.record_stream(s)
 
+    def _expect_logits(self, logits):
+        _expect("logits", logits, torch.bfloat16 if self.opts.logits_bf16 else torch.float32, self.desc.tokens_per_rank,
+                self.desc.num_experts)
+
     def route(self, logits, bias=None, stream=None):
+        self._expect_logits(logits)
+        if bias is not None:
+            _expect("bias", bias, torch.float32, self.desc.num_experts)
         with self._on(stream):
             B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err)
 
     def sort(self, x, stream=None):
+        _expect("x", x, torch.bfloat16, *self.out.shape)
         with self._on(stream):
             B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed,
                        self.err)
 
     def experts(self, weights, stream=None):
         """The expert stage on the sorted rows (weights: workloads.ExpertWeights)."""
+        E, H, I = self.desc.num_experts, self.desc.hidden, self.inter
+        if not I:
+            raise ValueError("LocalMoe: a layer made with inter = 0 has no expert stage")
+        _expect("w_gate", weights.w_gate, torch.bfloat16, E, I, H)
+        _expect("w_up", weights.w_up, torch.bfloat16, E, I, H)
+        _expect("w_down", weights.w_down, torch.bfloat16, E, H, I)
         with self._on(stream):
             B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate,
                                  weights.w_up, self.h, self.err)
@@ -245,6 +275,8 @@ class LocalMoe:
         packed_y to that of packed_x, row by row, both bf16 [tokens * topk][hidden]. It is called with ``stream`` as
         the current one. Rows at or above region_offsets' last entry belong to no choice: packed_x and grad_y hold
         nothing of this batch there."""
+        _expect("grad_out", grad_out, torch.bfloat16, *self.out.shape)
+        self._expect_logits(logits)
         with self._on(stream):
             if self.grad_y is None:
                 self.grad_y, self.grad_x = torch.zeros_like(self.packed_y), torch.empty_like(self.out)
@@ -254,19 +286,37 @@ class LocalMoe:
             B.moe_unsort_grad(self.desc, self.packed_y, self.tok_packed, self.topk_weights, grad_out, self.grad_y,
                               self.grad_weights, self.err)
             grad_packed = expert_grad(self.packed_x, self.region_offsets, self.grad_y)
+            _expect("expert_grad's result", grad_packed, torch.bfloat16, *self.packed_x.shape)
             B.moe_sort_grad(self.desc, grad_packed, self.tok_packed, self.grad_x, self.err)
             B.moe_gate_grad(self.desc, self.opts, logits, self.topk_idx, self.grad_weights, self.grad_logits, self.err)
         return self.grad_x, self.grad_logits
 
-    def shared(self, x, w, lora_a, lora_b, scales, adapter, stream=None):
-        """x w^T [tokens][out] with each token's adapter beside it (moe_lora_linear). The result is the caller's own:
-        it and the scratch u are new in each call, so that two projections, on one stream or on two, share nothing."""
-        A, rank, _ = lora_a.shape
+    def shared(self, x, w, lora_a=None, lora_b=None, scales=None, adapter=None, stream=None):
+        """x w^T [tokens][out] with each token's adapter beside it (moe_lora_linear), or, without lora_a, alone: x
+        [tokens][in] and w [out][in] bf16, lora_a [A][rank][in] and lora_b [A][out][rank] bf16, scales [A] float32 or
+        None, adapter [tokens] int32. The result is the caller's own: it and the scratch u are new in each call, so
+        that two projections, on one stream or on two, share nothing."""
+        bf16 = torch.bfloat16
+        _expect("x", x, bf16, None, None)
+        (T, K), A, rank = x.shape, 0, 0
+        _expect("w", w, bf16, None, K)
+        N = w.shape[0]
+        if lora_a is not None:
+            _expect("lora_a", lora_a, bf16, None, None, K)
+            A, rank, _ = lora_a.shape
+            _expect("lora_b", lora_b, bf16, A, N, rank)
+            _expect("adapter", adapter, torch.int32, T)
+            if scales is not None:
+                _expect("scales", scales, torch.float32, A)
+        else:
+            for name, t in (("lora_b", lora_b), ("scales", scales), ("adapter", adapter)):
+                if t is not None:
+                    raise ValueError(f"LocalMoe: {name} is given without lora_a")
         with self._on(stream):
-            self.u = torch.empty((x.shape[0], rank), dtype=torch.bfloat16, device=x.device)
-            out = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
-            desc = B.MoeLoraDesc(x.shape[0], x.shape[1], w.shape[0], rank, A, 0)
-            B.moe_lora_linear(desc, x, w, lora_a, lora_b, scales, adapter, self.u, out, self.err)
+            self.u = torch.empty((T, rank), dtype=bf16, device=x.device) if A else None
+            out = torch.empty((T, N), dtype=bf16, device=x.device)
+            B.moe_lora_linear(B.MoeLoraDesc(T, K, N, rank, A, 0), x, w, lora_a, lora_b, scales, adapter, self.u, out,
+                              self.err)
         return out
 
     def error(self, stream=None) -> int:

@@ -1,4 +1,4 @@
-"""LocalMoe.shared: results are the caller's own."""
+"""LocalMoe.shared: results are the caller's own, and the projection runs alone where there are no adapters."""
 from __future__ import annotations
 
 import pytest
@@ -32,3 +32,32 @@ def test_a_result_stays_when_another_projection_of_its_shape_follows():
     up = layer.shared(x, draw(256, 128), la, lb, None, ids)
     assert layer.error() == B.MOE_OK
     assert torch.equal(gate, kept) and not torch.equal(gate, up)
+
+
+@pytest.mark.parametrize("T", [1, 33, 200])
+def test_the_projection_alone(T):
+    """Bar: one bf16 rounding, and (K + 2) 2^-22 of the magnitudes that are added (as the projection's own tests)."""
+    require_gpu()
+    layer, draw = layer_and_rows(T, 128)
+    x, w = draw(T, 128), draw(264, 128)
+    y = layer.shared(x, w)
+    assert layer.error() == B.MOE_OK
+    want = x.double() @ w.double().t()
+    bar = 2.0 ** -8 * want.abs() + 130 * 2.0 ** -22 * (x.double().abs() @ w.double().abs().t())
+    assert bool(((y.double() - want).abs() <= bar).all())
+
+
+def test_a_result_of_expert_grad_of_another_type_or_size_is_refused():
+    """It goes on by address, and was read as bf16 [tokens * topk][hidden] whatever it was."""
+    require_gpu()
+    layer, draw = layer_and_rows(9, 128)
+    x, logits = draw(9, 128), draw(9, 4).float()
+    layer.route(logits)
+    layer.sort(x)
+    layer.packed_y.copy_(layer.packed_x)
+    layer.unsort()
+    for bad in (lambda px, off, gy: gy.float(), lambda px, off, gy: gy[:4], lambda px, off, gy: None):
+        with pytest.raises(ValueError, match="expert_grad's result"):
+            layer.backward(x, logits, bad)
+    layer.backward(x, logits, lambda px, off, gy: gy)
+    assert layer.error() == B.MOE_OK
