@@ -316,6 +316,17 @@ inline moe_status launch_status() { return cudaGetLastError() == cudaSuccess ? M
 // SM count of the current device (queried once per device).
 int sm_count();
 
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device. The
+// limit belongs to the kernel on its device, not to a launch, so it is raised and
+// never lowered: set to each call's own size, a host thread with a small call
+// took the limit away from another thread's larger one between that one's setting
+// and its launch. False when the device refuses.
+bool raise_smem_limit(const void *kernel, size_t bytes);
+template <class... Args>
+bool raise_smem_limit(void (*kernel)(Args...), size_t bytes) {
+  return raise_smem_limit(reinterpret_cast<const void *>(kernel), bytes);
+}
+
 // Launch with programmatic dependent launch (MOE_PDL=1): the kernel may be
 // scheduled while the previous kernel in the stream finishes and waits for its
 // results with griddepcontrol.wait.

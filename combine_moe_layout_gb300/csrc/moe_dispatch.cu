@@ -244,10 +244,7 @@ moe_status launch_dispatch(const Sizes &s, const void *x, const float *x_scales,
 
   size_t smem = static_cast<size_t>(a.stages) * a.piece_bytes;
   if (a.quant) smem += static_cast<size_t>(a.stages) * (a.piece_bytes / 2 + a.piece_bytes / 256 * sizeof(float));
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(dispatch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-          cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(dispatch_kernel, smem)) return MOE_ECUDA;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, dispatch_kernel, 32, smem) != cudaSuccess)
     return MOE_ECUDA;

@@ -654,9 +654,7 @@ moe_status launch_pair(const GemmArgs &a, const CUtensorMap &ma, const CUtensorM
   const int smem = pair_smem_bytes(a.E);
   if (smem > kSmemMax) return MOE_EINVAL;
   const int64_t max_tiles = (static_cast<int64_t>(a.rows) / (2 * kBM) + a.E) * a.ntiles_n;
-  if (cudaFuncSetAttribute(grouped_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(grouped_gemm_pair_kernel, smem)) return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kGemmThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
@@ -709,8 +707,7 @@ moe_status launch_grouped(GemmArgs a, const void *A, const void *B0, const void 
       !make_map(&mb1, B1, a.K, b_total_rows))
     return MOE_ECUDA;
   if (pair) return launch_pair(a, ma, mb0, mb1, num_sms, stream);
-  if (cudaFuncSetAttribute(grouped_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(grouped_gemm_kernel, smem)) return MOE_ECUDA;
   const int sms = num_sms > 0 ? num_sms : sm_count();
   const int64_t grid = max_tiles < sms ? max_tiles : sms;
   if (grid <= 0) return MOE_OK;

@@ -536,8 +536,7 @@ moe_status launch_form(const F8Args &a, const CUtensorMap &ma, const CUtensorMap
   auto kernel = grouped_gemm_fp8_kernel<STAGES, STAGED>;
   const int smem = f8_smem_fixed(STAGES, STAGED) + 12 * (a.E + 1);  // offsets + two class prefixes
   if (smem > kF8SmemMax) return MOE_EINVAL;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(kernel, smem)) return MOE_ECUDA;
   // the register split needs the launch allocation it was sized for
   cudaFuncAttributes fa{};
   if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs < kF8LaunchRegs) return MOE_ECUDA;

@@ -32,6 +32,8 @@
 // cluster writes the totals.
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 #include "moe_common.cuh"
 
 namespace cg = cooperative_groups;
@@ -232,6 +234,30 @@ int sm_count() {
   return n;
 }
 
+bool raise_smem_limit(const void *kernel, size_t bytes) {
+  struct Limit {
+    const void *kernel;
+    int dev;
+    size_t bytes;
+  };
+  static std::mutex lock;
+  static Limit limits[512];  // kernels x devices: far more than there are
+  static int used = 0;
+  if (bytes <= 48 * 1024) return true;  // what every kernel has
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const std::lock_guard<std::mutex> hold(lock);
+  int at = 0;
+  while (at < used && (limits[at].kernel != kernel || limits[at].dev != dev)) ++at;
+  if (at < used && limits[at].bytes >= bytes) return true;
+  if (at == 512 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+                       cudaSuccess)
+    return false;
+  limits[at] = Limit{kernel, dev, bytes};
+  if (at == used) ++used;
+  return true;
+}
+
 moe_status launch_layout(const Sizes &s, const int32_t *topk_idx, int32_t *counts, const SlotParts &parts,
                          int32_t *tok_slot, int32_t *err, cudaStream_t stream) {
   if (s.E > kLayoutMaxExperts) return MOE_EINVAL;
@@ -239,9 +265,7 @@ moe_status launch_layout(const Sizes &s, const int32_t *topk_idx, int32_t *count
   int csize = 0, tpc = 0, words = 0;
   size_t csmem = 0;
   if (cluster_shape(s, &csize, &tpc, &words, &csmem)) {
-    if (csmem > 48 * 1024 && cudaFuncSetAttribute(layout_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(csmem)) != cudaSuccess)
-      return MOE_ECUDA;
+    if (!raise_smem_limit(layout_cluster_kernel, csmem)) return MOE_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(csize, s.R, 1);
     cfg.blockDim = dim3(kClusterThreads, 1, 1);
@@ -260,10 +284,7 @@ moe_status launch_layout(const Sizes &s, const int32_t *topk_idx, int32_t *count
     return launch_status();
   }
   const size_t smem = static_cast<size_t>(s.E) * (1 + kLayoutWords) * sizeof(uint32_t);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-          cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(layout_kernel, smem)) return MOE_ECUDA;
   const int chunks = s.T > 0 ? (s.T + kLayoutChunk - 1) / kLayoutChunk : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(chunks, s.R, 1);

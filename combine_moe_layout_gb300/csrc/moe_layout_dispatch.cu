@@ -379,9 +379,7 @@ template <int W, int VPT, int KC, bool QUANT>
 static moe_status launch_fused(const FusedArgs &a, int sms, cudaStream_t stream) {
   auto kern = layout_dispatch_kernel<W, VPT, KC, QUANT>;
   const size_t smem = static_cast<size_t>(a.G) * sizeof(int32_t);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(kern, smem)) return MOE_ECUDA;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kFusedThreads, smem) != cudaSuccess)
     return MOE_ECUDA;

@@ -255,10 +255,7 @@ moe_status launch_recv(const Sizes &s, const int32_t *counts, const uint64_t *fl
   if (nreg <= kRecvMaxRegions) {
     RecvArgs ra{counts, flags, region_offsets, err, ca, early_trigger(s.ntok)};
     const size_t smem = static_cast<size_t>(nreg + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(recv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-            cudaSuccess)
-      return MOE_ECUDA;
+    if (!raise_smem_limit(recv_kernel, smem)) return MOE_ECUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, recv_kernel, kRecvThreads, smem) != cudaSuccess)
       return MOE_ECUDA;

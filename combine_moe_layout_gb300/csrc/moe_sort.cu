@@ -377,9 +377,7 @@ moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_
   const int64_t pieces = ctas * warps;
   const int64_t per_warp = ((n + pieces - 1) / pieces + 31) / 32 * 32;
   const size_t smem = static_cast<size_t>(warps + 2) * s.E * sizeof(int32_t);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess)
-    return MOE_ECUDA;
+  if (!raise_smem_limit(rank_kernel, smem)) return MOE_ECUDA;
   int bits = 0;
   while ((1 << bits) < s.E) ++bits;
   RankArgs a{topk_idx, region_offsets, tok_packed, err, static_cast<uint32_t>(n),
