@@ -27,6 +27,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "moe_common.cuh"
 
 namespace cg = cooperative_groups;
@@ -35,7 +37,12 @@ namespace moe {
 namespace {
 
 constexpr int kRankThreads = 1024;
-constexpr int kRankMaxCluster = 16;  // (more than 8 have to be allowed for the kernel)
+// CTAs of a cluster: up to 8 are granted everywhere, more have to be allowed for
+// the kernel and found room for on one part of the device.
+#ifndef MOE_RANK_CLUSTER
+#define MOE_RANK_CLUSTER 16
+#endif
+constexpr int kRankMaxCluster = MOE_RANK_CLUSTER, kRankPortableCluster = 8;
 constexpr int kRankMaxExperts = 8192;
 constexpr int kRankMaxBits = 13;
 constexpr int kRankSmem = 200 * 1024;
@@ -341,6 +348,38 @@ __global__ void __launch_bounds__(kUnsortGradMaxWarps * 32) unsort_grad_kernel(U
   }
 }
 
+// The most CTAs that a cluster of the ranking may have on the current device, asked
+// once with the most shared memory that one takes.
+int rank_cluster_limit() {
+  static std::atomic<int> known[64];
+  if (kRankMaxCluster <= kRankPortableCluster) return kRankMaxCluster;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kRankPortableCluster;
+  int most = known[dev].load(std::memory_order_relaxed);
+  if (most != 0) return most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kRankMaxCluster, 1, 1);
+  cfg.blockDim = dim3(kRankThreads, 1, 1);
+  cfg.dynamicSmemBytes = kRankSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kRankMaxCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  most = kRankMaxCluster;
+  if (!raise_smem_limit(rank_kernel, kRankSmem) ||
+      cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&clusters, rank_kernel, &cfg) != cudaSuccess || clusters < 1) {
+    cudaGetLastError();  // an answer, not a failed call
+    most = kRankPortableCluster;
+  }
+  known[dev].store(most, std::memory_order_relaxed);
+  return most;
+}
+
 // Cluster shape of the ranking: a CTA per 512 choices, one a lane of 16 warps, as
 // far as clusters go: handing out the positions is bound by instructions, about
 // 0.8 us for a group of 32 choices in each of a CTA's warps. 8192 choices of 256
@@ -369,9 +408,10 @@ moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_
   if (warps > kRankThreads / 32) warps = kRankThreads / 32;
   if (warps < 1) return MOE_EINVAL;
   int64_t ctas = (n + 511) / 512;
-  if (ctas > kRankMaxCluster) ctas = kRankMaxCluster;
-  if (ctas > 8 && cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return MOE_ECUDA;
+  if (ctas > kRankPortableCluster) {
+    const int most = rank_cluster_limit();
+    if (ctas > most) ctas = most;
+  }
   const int64_t needed = ((n + 31) / 32 + ctas - 1) / ctas;
   if (warps > needed) warps = static_cast<int>(needed);
   const int64_t pieces = ctas * warps;
