@@ -1439,7 +1439,7 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
                 !aligned16(lora_b) || !aligned4(scales) || !aligned4(adapter) || !aligned16(u)))
     return MOE_EINVAL;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int sms = desc->num_sms > 0 ? desc->num_sms : sm_count();
+  const int sms = desc->num_sms > 0 && desc->num_sms < sm_count() ? desc->num_sms : sm_count();
   LoraArgs a{};
   a.adapter = adapter;
   a.scales = scales;

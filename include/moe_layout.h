@@ -498,7 +498,7 @@ typedef struct {
   int32_t out_dim;      /* a multiple of 8 */
   int32_t rank;         /* a multiple of 8, at most 256 (ignored without adapters) */
   int32_t num_adapters; /* A >= 0; 0: the projection alone */
-  int32_t num_sms;      /* SMs the projection's CTAs are spread over; 0 = all */
+  int32_t num_sms;      /* SMs the projection's CTAs are spread over; 0, or more than there are: all */
 } moe_lora_desc;
 
 /* For every token t with a = adapter[t]:
