@@ -138,11 +138,13 @@ __device__ __forceinline__ int chunk_col(bool swiglu, int cbase, int c) {
 
 template <int N>
 __device__ __forceinline__ void regs_release() {
+  __syncwarp();
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int N>
 __device__ __forceinline__ void regs_claim() {
+  __syncwarp();
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
@@ -349,7 +351,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         for (int c = 0; c < 4; c += 2) {
           if (c < ncol) {
             uint32_t r[64];
-            tmem_load32x2_wait(tb + chunk_col(sw, cbase, c), tb + chunk_col(sw, cbase, c + 1), r);
+            // (the vote took every lane, and only arithmetic comes between it and the loads: a __syncwarp() here cost
+            // the DeepSeek prefill 0.7%)
+            tmem_load32x2_wait<true>(tb + chunk_col(sw, cbase, c), tb + chunk_col(sw, cbase, c + 1), r);
             if (c + 2 >= ncol) {
               // the partial has been read: the MMA warp may refill it
               tc_fence_before();

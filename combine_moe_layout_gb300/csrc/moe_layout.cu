@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kClusterThreads) layout_cluster_kernel(LayoutA
     for (int w = 0; w < words; ++w) c += __popc(bits[e * words + w]);
     hist[e] = c;
   }
+  __syncwarp();
   cluster.sync();  // every slice's counts are visible to the whole cluster
 
   for (int e = tid; e < a.E; e += blockDim.x) {
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(kClusterThreads) layout_cluster_kernel(LayoutA
     }
     out[i] = slot;
   }
+  __syncwarp();
   cluster.sync();  // no CTA leaves while another may still read its counts
 }
 

@@ -402,9 +402,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   grid_dependency_wait();
   // The projection's CTAs may come: they find what this kernel's predecessors wrote, and by the rule on shared
-  // memory they leave every CTA of this kernel its tensor memory. (A projection of several tiles a CTA in turn lets
-  // nothing start before it ends: with this kernel, which then claimed tensor memory before its wait, beside one of
-  // 128-wide tiles, calls of 2500 tokens and 520 inputs faulted, for a reason that reading did not show.)
+  // memory they leave every CTA of this kernel its tensor memory. (A projection of several tiles a CTA lets nothing
+  // start before it ends.)
   grid_dependents_launch();
   int slot = -1;
   __syncwarp();
@@ -554,6 +553,7 @@ constexpr int kSmallTokens = 64;  // of a call, at most
 
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
+  __syncwarp();  // the lanes' rows may end at different places
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
       "%2, %3};"
@@ -980,7 +980,6 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         __nv_bfloat16 *row = a.y + static_cast<int64_t>(valid ? t.t0 + m : 0) * a.N + t.n0;
         for (int c = 0; c < t.cols; c += 32) {
           uint32_t r[32];
-          __syncwarp();
           tmem_load32_wait(tb + c, r);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(RankArgs a) {
     }
     total[e] = run;
   }
+  __syncwarp();
   cluster.sync();  // every CTA's counts are visible to the cluster
 
   // exclusive scan over the experts of the cluster's counts: thread tid owns experts [e0, e1)
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(RankArgs a) {
       }
     }
   }
+  __syncwarp();
   cluster.sync();  // no CTA leaves while another may still read its counts
 }
 
