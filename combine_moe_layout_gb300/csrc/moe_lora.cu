@@ -744,12 +744,16 @@ __device__ __forceinline__ LTile ltile_of(int w, const LoraArgs &a) {
   return LTile{mt * kLBM, (g * a.group_n + r - mt * gw) * BN + half * (BN / 2), cols};
 }
 
+// Whether a CTA takes several tiles: whole 256-wide ones only. All other forms have a CTA (or a cluster) for each tile.
+template <int BN, bool SPLIT>
+constexpr bool kLWalks = BN > 128 && !SPLIT;
+
 template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kGemmLThreads, 1)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_b,
                      const LoraArgs a) {
-  constexpr int kAcc = SPLIT ? 1 : 2;               // accumulators
+  constexpr int kAcc = kLWalks<BN, SPLIT> ? 2 : 1;  // accumulators
   constexpr uint32_t kCols = kAcc * BN;
   constexpr int kRedPitch = BN + 4;                 // floats of a row of partial sums
   extern __shared__ uint8_t smem_raw[];
@@ -761,8 +765,8 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
   const int splits = SPLIT ? static_cast<int>(lora_cluster_size()) : 1;
   const int split = SPLIT ? static_cast<int>(lora_cluster_rank()) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.x) / splits : static_cast<int>(blockIdx.x);
-  const int stride = SPLIT ? static_cast<int>(gridDim.x) / splits : static_cast<int>(gridDim.x);
   const int total = a.total;
+  const int stride = kLWalks<BN, SPLIT> ? static_cast<int>(gridDim.x) : total;  // (the loops over tiles end after one)
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (split + 1) / splits);
   const int rblocks = (a.rank + kLBK - 1) / kLBK;   // K blocks of one adapter
@@ -1382,14 +1386,15 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   const int64_t tiles = static_cast<int64_t>(a.mtiles) * a.ntiles_n;
   if (tiles > 0x3fffffffll / kLMaxSplit) return MOE_EINVAL;
   a.whole = a.total = static_cast<int>(tiles);
-  const int64_t grid = SPLIT ? tiles * splits : (tiles < sms ? tiles : sms);
+  constexpr bool kWalks = kLWalks<BN, SPLIT>;
+  const int64_t grid = kWalks ? (tiles < sms ? tiles : sms) : tiles * splits;
   const int rest = static_cast<int>(tiles % grid);
-  if (BN > 128 && !SPLIT && rest > 0 && 2 * rest <= grid) {
+  if (kWalks && rest > 0 && 2 * rest <= grid) {
     a.whole -= rest;
     a.total += rest;
   }
   a.group_n = a.ntiles_n < 8 ? a.ntiles_n : 8;
-  const int smem = with_columns(1024 + a.stages * a.stage + tail, (SPLIT ? 1 : 2) * BN);
+  const int smem = with_columns(1024 + a.stages * a.stage + tail, (kWalks ? 2 : 1) * BN);
   if (smem > kLSmemMax - kLStatic) return MOE_EINVAL;
   constexpr int kBox = BN < kBoxRows ? BN : kBoxRows;
   a.pieces = (a.rank + 15) / 16;
