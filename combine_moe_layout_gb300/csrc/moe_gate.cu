@@ -138,6 +138,13 @@ __device__ __forceinline__ float load_logit(const void *logits, int64_t i) {
 
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }  // 1 for +inf
 
+// The sigmoid and, to its own size, what it leaves of one.
+__device__ __forceinline__ float sigmoid_and_rest(float l, float *rest) {
+  const float z = expf(-l), s = 1.0f / (1.0f + z);
+  *rest = fminf(z, FLT_MAX) * s;
+  return s;
+}
+
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
@@ -460,9 +467,29 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateArgs a) {
   }
 }
 
+// x of this lane, or the sum of x over all lanes that name the same expert, in their order.
+__device__ __forceinline__ float over_entries(float x, int my_e, int k) {
+  float sum = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const float v = __shfl_sync(0xffffffffu, x, j);
+    if (__shfl_sync(0xffffffffu, my_e, j) == my_e) sum += v;
+  }
+  return sum;
+}
+
 // The gradient's row is zero (renormalised softmax and sigmoid) or -s_e times
 // one number (plain softmax), but for the k chosen. A renormalised row needs the
 // chosen logits only, so the other E - k are not read.
+//
+// A score near one leaves 1 - s small, and it is lost when it is taken from the
+// rounded s (a logit of 17 gave a sigmoid's gradient of zero). The sigmoid's is
+// exp(-l) s. A softmax' differences g_j - sum_i g_i s_i are taken as
+//   s_t (g_j - g_t) + g_j r - sum_{i != t} g_i s_i
+// with t the largest score and r = sum_{i != t} s_i, the rest, added up without it:
+// nothing there is the small difference of two large numbers. 32768 tokens of 256
+// fp32 logits, k = 8, with the gate: 27.5 us (renormalised softmax, as with the
+// plain differences), 32.4 (softmax; 31.1 with them), 28.9 (renormalised sigmoid;
+// 27.8).
 template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -479,35 +506,54 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
       if (my_e != kMaskedExpert) latch_error(a.err, MOE_EINVAL);
       my_e = -1;
     } else {
-      g = a.gw[t * a.k + lane] * a.scale;
+      g = a.gw[t * a.k + lane];
       my_l = finite(load_logit<BF16>(a.logits, t * a.E + my_e));
     }
   }
+  // The choices' elements go through the warp's row in shared memory (comparing every value with every choice cost as
+  // much as the rest of the kernel). What no choice wrote stays kUnset, a NaN that no arithmetic gives. An expert
+  // named by two entries shows in the marks: its terms are added up, in order, in both.
+  constexpr uint32_t kUnset = 0xffffffffu;
+  __shared__ __align__(16) uint32_t rows[kGateWarps][VPL * 32];
+  uint32_t *row = rows[warp];
+#pragma unroll
+  for (int p = 0; p < VPL / 4; ++p)
+    *reinterpret_cast<uint4 *>(row + (p * 32 + lane) * 4) = make_uint4(kUnset, kUnset, kUnset, kUnset);
+  __syncwarp();
+  if (my_e >= 0) row[my_e] = lane;
+  __syncwarp();
+  const bool any_twice = __any_sync(0xffffffffu, my_e >= 0 && row[my_e] != static_cast<uint32_t>(lane));
+  __syncwarp();
+
   float out[VPL];
   float d = 0.0f;  // dL/dl of this lane's choice
-  if (a.sigmoid) {
-    const float s = my_e >= 0 ? sigmoid_of(my_l) : 0.0f;
-    if (a.renorm) {
-      const float total = warp_sum(s);
-      if (total > 0.0f) {
-        const float mean = warp_sum(g * (s / total));
-        d = (g - mean) / total * s * (1.0f - s);
-      }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
+  if (a.renorm) {
+    float p = 0.0f, most = 1.0f, rest_p = 1.0f;  // the score; of a softmax relative to the largest
+    if (a.sigmoid) {
+      if (my_e >= 0) p = sigmoid_and_rest(my_l, &rest_p);
+      most = redux_max(p);
     } else {
-      d = g * s * (1.0f - s);
+      const float m = redux_max(my_l);
+      if (my_l > -INFINITY) p = expf(my_l - m);
+      most = m > -INFINITY ? 1.0f : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
-  } else if (a.renorm) {
-    const float m = redux_max(my_l);
-    const float p = my_l > -INFINITY ? expf(my_l - m) : 0.0f;
-    const float total = warp_sum(p);
-    if (total > 0.0f) {
+    if (most > 0.0f) {  // (the whole warp)
+      const int top = __ffs(__ballot_sync(0xffffffffu, p == most)) - 1;
+      const float rest = warp_sum(lane == top ? 0.0f : p), total = most + rest;
       const float v = p / total;
-      d = v * (g - warp_sum(g * v));
+      const float others = warp_sum(lane == top ? 0.0f : g * v);
+      d = most / total * (g - __shfl_sync(0xffffffffu, g, top)) + (g * (rest / total) - others);
+      d *= a.sigmoid ? p * rest_p / total : v;
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = 0.0f;
+    d *= a.scale;
+    if (any_twice) d = over_entries(d, my_e, a.k);
+  } else if (a.sigmoid) {
+    float rest = 0.0f;
+    const float s = sigmoid_and_rest(my_l, &rest);
+    if (my_e >= 0) d = a.scale * g * (s * rest);
+    if (any_twice) d = over_entries(d, my_e, a.k);
   } else {
     float l[VPL];
     bool nan = false;
@@ -516,46 +562,40 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateArgs a) 
 #pragma unroll
     for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, l[i] = finite(l[i]));
     mx = redux_max(mx);
-    if (mx == -INFINITY) mx = 0.0f;
-    float sum = 0.0f;
+    const bool some = mx > -INFINITY;
+    if (!some) mx = 0.0f;
+    // exp(0) = 1 is the largest; the rest is what is below one and all but one of the ones
+    float rest = 0.0f, ones = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       l[i] = expf(l[i] - mx);
-      sum += l[i];
+      (l[i] < 1.0f ? rest : ones) += l[i];
     }
-    sum = warp_sum(sum);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    d = my_l > -INFINITY ? g * (expf(my_l - mx) * inv) : 0.0f;
-    const float total = warp_sum(d);
+    const unsigned with = __ballot_sync(0xffffffffu, ones > 0.0f);
+    if (lane == __ffs(with) - 1) ones -= 1.0f;
+    rest = warp_sum(rest + ones);
+    const float inv = some ? 1.0f / (1.0f + rest) : 0.0f;  // also the largest score
+    // the largest among the chosen, if it is one (of several equal ones any is as good as another)
+    const float p = my_l > -INFINITY ? expf(my_l - mx) : 0.0f, s = p * inv;
+    const int from = __ffs(__ballot_sync(0xffffffffu, p == 1.0f)) - 1;
+    const int top_e = __shfl_sync(0xffffffffu, my_e, from & 31);
+    const float others = warp_sum(from >= 0 && my_e == top_e ? 0.0f : g * s);
+    if (any_twice) g = over_entries(g, my_e, a.k);
+    const float g_top = __shfl_sync(0xffffffffu, g, from & 31), at_top = from >= 0 ? g_top : 0.0f;
+    const float sum = a.scale * (at_top * inv + others);
+    d = a.scale * (s * (inv * (g - at_top) + (g * (rest * inv) - others)));
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = -total * (l[i] * inv);
+    for (int i = 0; i < VPL; ++i) out[i] = -sum * (l[i] * inv);
   }
-  // the choices' terms, through the warp's row in shared memory (comparing every value with every choice cost as
-  // much as the rest of the kernel)
-  __shared__ __align__(16) float rows[kGateWarps][VPL * 32];
-  float *row = rows[warp];
-  int *mark = reinterpret_cast<int *>(row);
-#pragma unroll
-  for (int p = 0; p < VPL / 4; ++p) *reinterpret_cast<float4 *>(row + (p * 32 + lane) * 4) = make_float4(0, 0, 0, 0);
+  if (my_e >= 0) row[my_e] = __float_as_uint(d);
   __syncwarp();
-  if (my_e >= 0) mark[my_e] = lane;
-  __syncwarp();
-  const bool twice = my_e >= 0 && mark[my_e] != lane;  // an expert named by two entries: their terms add up, in order
-  const bool any_twice = __any_sync(0xffffffffu, twice);
-  if (my_e >= 0) row[my_e] = any_twice ? 0.0f : d;
-  __syncwarp();
-  if (any_twice)
-    for (int j = 0; j < a.k; ++j) {
-      if (lane == j && my_e >= 0) row[my_e] += d;
-      __syncwarp();
-    }
 #pragma unroll
   for (int p = 0; p < VPL / 4; ++p) {
-    const float4 v = *reinterpret_cast<const float4 *>(row + (p * 32 + lane) * 4);
-    out[4 * p] += v.x;
-    out[4 * p + 1] += v.y;
-    out[4 * p + 2] += v.z;
-    out[4 * p + 3] += v.w;
+    const uint4 v = *reinterpret_cast<const uint4 *>(row + (p * 32 + lane) * 4);
+    if (v.x != kUnset) out[4 * p] = __uint_as_float(v.x);
+    if (v.y != kUnset) out[4 * p + 1] = __uint_as_float(v.y);
+    if (v.z != kUnset) out[4 * p + 2] = __uint_as_float(v.z);
+    if (v.w != kUnset) out[4 * p + 3] = __uint_as_float(v.w);
   }
   const int64_t base = t * a.E;
 #pragma unroll
