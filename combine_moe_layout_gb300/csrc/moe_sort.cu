@@ -214,8 +214,7 @@ struct RowArgs {
   const int32_t *tok_packed;
   uint8_t *packed;
   float *packed_scales;
-  int32_t *err;
-  int64_t ntok, nrows;
+  int64_t ntok;
   int V, k, nsc;          // V: 16-byte vectors of a row
   int tpb, chunks, vpc;   // tokens per block; chunks of vpc vectors per row
 };
@@ -437,10 +436,10 @@ moe_status launch_rank(const Sizes &s, const int32_t *topk_idx, int32_t *region_
 }
 
 moe_status launch_sort_rows(const Sizes &s, const void *x, const float *x_scales, const int32_t *tok_packed,
-                            void *packed, float *packed_scales, int32_t *err, cudaStream_t stream) {
+                            void *packed, float *packed_scales, cudaStream_t stream) {
   const int V = static_cast<int>(s.in_row_bytes / 16);
   RowArgs a{static_cast<const uint8_t *>(x), x_scales, tok_packed, static_cast<uint8_t *>(packed), packed_scales,
-            err, s.ntok, s.ntok * s.k, V, s.k, s.nsc, 1, 1, V};
+            s.ntok, V, s.k, s.nsc, 1, 1, V};
   // blocks of at most 256 threads, cut so that the threads of a row's last block are not idle; whole 16-lane
   // groups (a quantised block) stay together
   a.chunks = (V + 255) / 256;
@@ -484,7 +483,7 @@ extern "C" moe_status moe_sort(const moe_desc *desc, const int32_t *topk_idx, co
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   st = launch_rank(s, topk_idx, region_offsets, tok_packed, err, cs);
   if (st != MOE_OK || s.ntok == 0) return st;
-  return launch_sort_rows(s, x, x_scales, tok_packed, packed_x, packed_scales, err, cs);
+  return launch_sort_rows(s, x, x_scales, tok_packed, packed_x, packed_scales, cs);
 }
 
 extern "C" moe_status moe_sort_grad(const moe_desc *desc, const uint16_t *grad_packed, const int32_t *tok_packed,
