@@ -9,9 +9,14 @@
 // product goes on with u and B_a for every adapter a among its tokens, each time
 // writing only the accumulator rows of the tokens that use it (the MMA's
 // disable-output-lane mask, so no adapter's value, not even a NaN, reaches
-// another request's row). y is rounded once. Rounding u to bf16, which is what
-// the tensor cores take, costs 2^-9 of the adapter's term: at most what rounding
-// y costs where that term is all of it.
+// another request's row). y is rounded once. u is rounded to bf16 too, which is what
+// the tensor cores take and what the caller's scratch holds: up to 2^-9 of each
+// u_i b_i, which is more than rounding y costs where these cancel. Over ten shapes
+// the error of y against 64 bits (relative, over the whole matrix) is 1.70e-3 to
+// 2.35e-3, where y's rounding alone leaves 1.63e-3 to 1.68e-3; against the formula
+// with u in bf16 what is left is the order of the sums (2.2e-4 and less). A second
+// part of u beside the first would leave 256-wide tiles three stages of their ring
+// for four (8192 tokens, 7168 -> 2048: 203 us for 181).
 //
 // Two kernels a call:
 //   lora_shrink_kernel  u[t] = s_a x[t] A_a^T. A tile is 128 tokens against the
@@ -58,8 +63,8 @@ constexpr int kLMaxCluster = 8;    // of the shrink kernel
 constexpr int kLMaxSplit = 4;      // of the projection
 // Ranks up to 32 have several adapters' B_a in a stage, as pieces of 16 columns:
 // a block of 64 columns would be half empty or more, and each would take a
-// stage's way through the ring (64 tokens, 32 adapters of rank 16: 17.1 us with
-// blocks of 64 columns, 16.1 with eight adapters a stage).
+// stage's way through the ring (64 tokens, 32 adapters of rank 16: eight adapters
+// a stage took it from 17.1 to 16.1 us).
 constexpr int kLPackedPieces = 2;
 
 struct LoraArgs {
@@ -541,9 +546,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
 // Sums: every CTA of the cluster sends its part of a sum to the CTA that owns it
 // and the owner adds them in the order of the CTAs. What it receives has two
 // places in turn, so one cluster barrier a pass is enough.
-// 64 tokens (7168 -> 2048, 32 adapters of rank 16): the call takes 21.6 us with
-// the tensor-memory kernel, 19.5 us with loads to registers and sums read from
-// the other CTAs, 17.3 us with this one.
+// 64 tokens (7168 -> 2048, 32 adapters of rank 16): the call takes 15.8 us, and 20.7
+// with the tensor-memory kernel. When this one was new it took 17.3 us, where loads
+// to registers and sums read from the other CTAs had taken 19.5.
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 256;
 constexpr int kSmallWarps = kSmallThreads / 32;
@@ -702,8 +707,8 @@ __global__ void __launch_bounds__(kSmallThreads)
 // Bound by the tensor cores for many tokens: 8192 tokens, 7168 -> 2048 with
 // adapters of rank 64, 151 us, 1.6 PFLOP/s. For few by what a call has to do one
 // after the other: u, W's way through one SM's ring, the last products and the
-// sum over the cluster (64 tokens, 7168 -> 2048, 32 adapters of rank 16: 19.5 us
-// with the shrink kernel, where the bytes alone are 5.7 us).
+// sum over the cluster (64 tokens, 7168 -> 2048, 32 adapters of rank 16: 15.8 us
+// with the shrink kernel, 12.1 without adapters, where the bytes alone are 5.7 us).
 // ---------------------------------------------------------------------------
 struct GemmShared {
   AdapterScratch scratch;
@@ -1079,10 +1084,13 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
 // Products and sums are in fp32, the sums over lanes and warps in a fixed order.
 // The adapter's term is added last, from u and the rows of B_a, by eight lanes
 // for each row.
-// Against the tiles above, with an adapter of rank 16: 4096 -> 4096 10.8 to 9.2
-// us, 7168 -> 2048 12.1 to 7.7; without one: 9.9 to 8.8, 10.4 to 7.8, 4096 ->
-// 14336 23.8 to 24.4, 512 -> 7168 4.8 to 5.2. Two tokens came out even with an
-// adapter (10.8 and 11.2 us), four behind (11.5 and 14.1 us: the sums take the
+// Against the tiles above, without an adapter and with one of rank 16: 4096 -> 4096
+// 8.5 and 9.6 us (tiles 9.8 and 12.0), 7168 -> 2048 7.5 and 8.5 (10.3 and 12.4),
+// 1024 -> 1024 4.3 and 7.2 (5.4 and 7.9), 2048 -> 7168 8.6 and 11.0 (9.3 and 11.5),
+// 512 -> 7168 5.6 and 8.50 (5.8 and 8.43), 4096 -> 14336 24.1 and 26.1 (23.8 and
+// 25.9): at worst 1% behind, so every single token comes here. When it was new, two
+// tokens came out even with an adapter (10.8 and 11.2 us) and four behind (11.5 and
+// 14.1: the sums take the
 // registers that loads in flight need).
 // ---------------------------------------------------------------------------
 constexpr int kOneThreads = 256;
