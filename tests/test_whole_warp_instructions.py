@@ -39,10 +39,20 @@ def function_around(text, at):
 def test_aligned_instructions_follow_a_syncwarp(name):
     text = strip_comments(open(os.path.join(CSRC, name)).read())
     # braces of the asm text itself are balanced within each statement
-    for m in re.finditer(r"\.aligned\b", text):
+    for m in re.finditer(r"(?<!setmaxnreg.inc.sync)(?<!setmaxnreg.dec.sync)\.aligned\b", text):
         body = function_around(text, m.start())
         first = body.index(".aligned")
         assert "__syncwarp();" in body[:first], body[:160]
+
+
+def test_registers_move_straight_after_a_block_barrier():
+    """setmaxnreg, the exception: between the last barrier of the block and the warps' own branches, nothing parts a warp."""
+    text = strip_comments(open(os.path.join(CSRC, "moe_expert_fp8.cu")).read())
+    kernel = text[text.index("grouped_gemm_fp8_kernel("):]
+    after = kernel[:kernel.index("regs_release<")].rpartition("__syncthreads();")[2]
+    assert re.fullmatch(r"\s*(const int \w+ = [^;{}]*;\s*)*if \(warp == 0\) \{\s*", after), after
+    for call in re.finditer(r"regs_(release|claim)<", kernel):
+        assert re.search(r"(if \(warp [^{}]*\)|else) \{\s*$", kernel[:call.start()]), kernel[:call.start()][-80:]
 
 
 @pytest.mark.parametrize("name", FILES)
