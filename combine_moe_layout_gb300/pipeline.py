@@ -199,7 +199,8 @@ class LocalMoe:
         self._streams = {}  # the streams that have used the buffers, by their handles
         if dev.type == "cuda":
             made_on = torch.cuda.current_stream(self.device)
-            self._made = made_on.record_event()
+            # (an event of a capture says nothing outside of it)
+            self._made = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
             self._streams[made_on.cuda_stream] = made_on
 
     def _on(self, stream):
@@ -212,7 +213,7 @@ class LocalMoe:
             s = torch.cuda.current_stream(self.device) if stream is None else stream
             with torch.cuda.stream(s):
                 # (a capture begins with nothing pending, and a captured stream may not wait for an event before it)
-                if not torch.cuda.is_current_stream_capturing():
+                if self._made is not None and not torch.cuda.is_current_stream_capturing():
                     s.wait_event(self._made)
             self._streams[handle] = s
             self._keep_for([s])

@@ -177,3 +177,20 @@ def test_a_captured_layer_replays():
     torch.cuda.synchronize()
     assert layer.error() == B.MOE_OK
     assert torch.equal(gx, gx_ref) and torch.equal(gl, gl_ref)
+
+
+def test_a_layer_made_in_a_capture():
+    """Its buffers are the graph's; calls after the capture use them too."""
+    require_gpu()
+    _, logits, _ = data()
+    ref = P.LocalMoe(T, H, E, K, opts(), "cuda:0")
+    ref.route(logits)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer = P.LocalMoe(T, H, E, K, opts(), "cuda:0")
+        layer.route(logits)
+    graph.replay()
+    assert layer.error() == B.MOE_OK and torch.equal(layer.topk_idx, ref.topk_idx)
+    layer.topk_idx.zero_()
+    layer.route(logits)
+    assert layer.error() == B.MOE_OK and torch.equal(layer.topk_idx, ref.topk_idx)
