@@ -66,6 +66,7 @@ class MoeLoraDesc(ctypes.Structure):
         ("rank", ctypes.c_int32),
         ("num_adapters", ctypes.c_int32),
         ("num_sms", ctypes.c_int32),
+        ("u_parts", ctypes.c_int32),
     ]
 
 

@@ -10,13 +10,17 @@
 // writing only the accumulator rows of the tokens that use it (the MMA's
 // disable-output-lane mask, so no adapter's value, not even a NaN, reaches
 // another request's row). y is rounded once. u is rounded to bf16 too, which is what
-// the tensor cores take and what the caller's scratch holds: up to 2^-9 of each
-// u_i b_i, which is more than rounding y costs where these cancel. Over ten shapes
-// the error of y against 64 bits (relative, over the whole matrix) is 1.70e-3 to
-// 2.35e-3, where y's rounding alone leaves 1.63e-3 to 1.68e-3; against the formula
-// with u in bf16 what is left is the order of the sums (2.2e-4 and less). A second
-// part of u beside the first would leave 256-wide tiles three stages of their ring
-// for four (8192 tokens, 7168 -> 2048: 203 us for 181).
+// the tensor cores take: up to 2^-9 of each u_i b_i, which is more than rounding y
+// costs where these cancel. Over ten shapes the error of y against 64 bits
+// (relative, over the whole matrix) is 1.70e-3 to 2.35e-3, where y's rounding alone
+// leaves 1.63e-3 to 1.68e-3. A call may ask for u in two parts, its rounding and the
+// rounding of what that left (2^-18 of u), which meet the same B_a one after the
+// other, with the error of y's rounding alone (1.63e-3 to 1.70e-3). That takes
+// 9.8 us for 9.7 (one token, 4096 -> 4096, rank 16), 17.3 for 15.5 (64 tokens, 7168
+// -> 2048, 32 adapters), 22.2 for 20.7 (389 tokens, 2056 -> 4104) and 191 for 179
+// (8192 tokens, 7168 -> 2048, rank 64): the parts share one place in shared memory,
+// since a second one would leave 256-wide tiles three stages of their ring for four
+// (203 us for 181).
 //
 // Two kernels a call:
 //   lora_shrink_kernel  u[t] = s_a x[t] A_a^T. A tile is 128 tokens against the
@@ -41,6 +45,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cfloat>
 
 #include "moe_tc.cuh"
 
@@ -84,6 +89,7 @@ struct LoraArgs {
   uint32_t cols;         // tensor-memory columns
   // projection
   int lora, ntiles_n, mtiles, group_n;
+  int parts;             // 1, or 2: u is followed by what its rounding left
   int whole, total;      // tiles taken whole, and tiles and halves in all
   int own;               // one token: rows of W of a CTA
   int pieces, packed;    // ranks up to 32: pieces of 16 columns of one B_a, and the B_a of a stage (0: 64 columns a stage)
@@ -256,6 +262,21 @@ __device__ __forceinline__ uint4 round8(const float (&f)[8]) {
     u[q] = *reinterpret_cast<const uint32_t *>(&p);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Eight columns of a token's u, as its one or two parts.
+__device__ __forceinline__ void store_u(const LoraArgs &a, int64_t t, int c, const float (&f)[8]) {
+  __nv_bfloat16 *at = a.u + t * a.rank + c;
+  *reinterpret_cast<uint4 *>(at) = round8(f);
+  if (a.parts > 1) {
+    float rest[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      rest[j] = f[j] - __bfloat162float(__float2bfloat16_rn(f[j]));
+      if (!(fabsf(rest[j]) <= FLT_MAX)) rest[j] = 0.0f;  // of an infinity or a NaN the first part says all
+    }
+    *reinterpret_cast<uint4 *>(at + static_cast<int64_t>(a.T) * a.rank) = round8(rest);
+  }
 }
 
 // A whole warp's bounded wait on an mbarrier phase: every lane gets the same
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       cluster_sum8<kLMaxCluster>(smem_addr(red + m * a.rank + c), splits, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= sc;
-      *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(t0 + m) * a.rank + c) = round8(f);
+      store_u(a, t0 + m, c, f);
     }
     fence_proxy_async_smem();  // the ring is loaded again where the sums were
     lora_cluster_sync();       // and no CTA leaves while another may still read its sums
@@ -696,7 +717,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         for (int j = 0; j < 8; ++j) f[j] += recv[pass & 1][p][i * 8 + j];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= sc;
-      *reinterpret_cast<uint4 *>(a.u + static_cast<int64_t>(token[m0 + m]) * a.rank + n0 + c) = round8(f);
+      store_u(a, token[m0 + m], n0 + c, f);
     }
   }
 }
@@ -844,30 +865,32 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
       if (!ok) break;
       const int blocks = sh.count[b] * rblocks;
-      if (a.packed > 0) {  // a piece a lane
-        for (int j = split; j < blocks; j += splits * a.packed, ++it, r.next(a.stages)) {
-          ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
-          if (!ok) break;
-          const int n = min(a.packed, (blocks - j + splits - 1) / splits) * a.pieces;
-          if (leader) mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(n * t.cols) * kLPieceRow);
-          __syncwarp();
-          if (lane < n) {
-            const int row = sh.list[b][j + lane / a.pieces * splits] * a.N + t.n0, k = lane % a.pieces * 16;
-            const uint32_t dst = ring + r.s * a.stage + lane * (BN * kLPieceRow), fb = fulls + r.s * 8;
-            tma_load_2d(dst, &map_b, k, row, fb);
-            if (t.cols > kBoxRows) tma_load_2d(dst + kBoxRows * kLPieceRow, &map_b, k, row + kBoxRows, fb);
+      for (int part = 0; ok && part < a.parts; ++part) {
+        if (a.packed > 0) {  // a piece a lane
+          for (int j = split; j < blocks; j += splits * a.packed, ++it, r.next(a.stages)) {
+            ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+            if (!ok) break;
+            const int n = min(a.packed, (blocks - j + splits - 1) / splits) * a.pieces;
+            if (leader) mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(n * t.cols) * kLPieceRow);
+            __syncwarp();
+            if (lane < n) {
+              const int row = sh.list[b][j + lane / a.pieces * splits] * a.N + t.n0, k = lane % a.pieces * 16;
+              const uint32_t dst = ring + r.s * a.stage + lane * (BN * kLPieceRow), fb = fulls + r.s * 8;
+              tma_load_2d(dst, &map_b, k, row, fb);
+              if (t.cols > kBoxRows) tma_load_2d(dst + kBoxRows * kLPieceRow, &map_b, k, row + kBoxRows, fb);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-      } else {
-        for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
-          ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
-          if (!ok) break;
-          if (leader) {
-            mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(t.cols) * kLRow);
-            load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
+        } else {
+          for (int j = split; j < blocks; j += splits, ++it, r.next(a.stages)) {
+            ok = warp_wait(sh.empty + r.s, r.ph ^ 1u, abort, a.err);
+            if (!ok) break;
+            if (leader) {
+              mbar_arrive_expect_tx(sh.full + r.s, static_cast<uint32_t>(t.cols) * kLRow);
+              load_w(&map_b, r.s, sh.list[b][j / rblocks] * a.N + t.n0, (j % rblocks) * kLBK, t.cols);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       if (leader) mbar_arrive(smem_addr(sh.lempty + b));
@@ -883,7 +906,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     int lt = 0;
     const uint32_t xlo = desc_lo(smem_addr(smem)), step = a.stage >> 4, xstep = a.xbytes >> 4;
     const uint32_t empty = smem_addr(sh.empty);
-    uint32_t uphase = 0;  // tiles whose u was used
+    uint32_t uphase = 0;  // parts of tiles' u that were used
     bool ok = true;
     for (int w = first; ok && w < total; w += stride, ++lt) {
       const int buf = lt % kAcc;
@@ -908,50 +931,50 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
         ok = warp_wait(sh.lfull + b, (lt >> 1) & 1u, abort, a.err);
         if (!ok) break;
         const int blocks = sh.count[b] * rblocks;
-        if (split < blocks) {
-          ok = warp_wait(&sh.ufull, uphase & 1u, abort, a.err);
-          if (!ok) break;
-          ++uphase;
-        }
-        if (a.packed > 0) {
-          for (int j = split; j < blocks; j += splits * a.packed, r.next(a.stages)) {
-            ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+        for (int part = 0; ok && part < a.parts; ++part) {
+          if (split < blocks) {
+            ok = warp_wait(&sh.ufull, uphase & 1u, abort, a.err);
             if (!ok) break;
-            tc_fence_after();
-            const int n = min(a.packed, (blocks - j + splits - 1) / splits);
-            if (leader) {
-              uint64_t piece = sw32_desc(smem_addr(smem) + r.s * a.stage);
-              const uint32_t ulo = desc_lo(ubuf);
-              for (int i = 0; i < n; ++i) {
-                const uint4 off = sh.off[b][j + i * splits];
-                for (int q = 0; q < a.pieces; ++q, piece += (BN * kLPieceRow) >> 4)
-                  mma_bf16_rows(d, full_desc(ulo + q * 2), piece, idesc, off);
+            ++uphase;
+          }
+          if (a.packed > 0) {
+            for (int j = split; j < blocks; j += splits * a.packed, r.next(a.stages)) {
+              ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+              if (!ok) break;
+              tc_fence_after();
+              const int n = min(a.packed, (blocks - j + splits - 1) / splits);
+              if (leader) {
+                uint64_t piece = sw32_desc(smem_addr(smem) + r.s * a.stage);
+                const uint32_t ulo = desc_lo(ubuf);
+                for (int i = 0; i < n; ++i) {
+                  const uint4 off = sh.off[b][j + i * splits];
+                  for (int q = 0; q < a.pieces; ++q, piece += (BN * kLPieceRow) >> 4)
+                    mma_bf16_rows(d, full_desc(ulo + q * 2), piece, idesc, off);
+                }
+                mma_commit(empty + r.s * 8);
               }
-              mma_commit(empty + r.s * 8);
+              __syncwarp();
             }
-            __syncwarp();
-          }
-        } else {
-          for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
-            ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-              const uint32_t lo = xlo + r.s * step, ulo = desc_lo(ubuf) + (j % rblocks) * xstep;
-              const uint4 off = sh.off[b][j / rblocks];
-              // columns past the rank are zeros in both tiles, so a step's last ones add nothing
-              const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
-              for (int kk = 0; kk * 16 < cols; ++kk)
-                mma_bf16_rows(d, full_desc(ulo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
-              mma_commit(empty + r.s * 8);
+          } else {
+            for (int j = split; j < blocks; j += splits, r.next(a.stages)) {
+              ok = warp_wait(sh.full + r.s, r.ph, abort, a.err);
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+                const uint32_t lo = xlo + r.s * step, ulo = desc_lo(ubuf) + (j % rblocks) * xstep;
+                const uint4 off = sh.off[b][j / rblocks];
+                // columns past the rank are zeros in both tiles, so a step's last ones add nothing
+                const int cols = min(kLBK, a.rank - (j % rblocks) * kLBK);
+                for (int kk = 0; kk * 16 < cols; ++kk)
+                  mma_bf16_rows(d, full_desc(ulo + kk * 2), full_desc(lo + xstep + kk * 2), idesc, off);
+                mma_commit(empty + r.s * 8);
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
+          if (leader && split < blocks) mma_commit(smem_addr(&sh.uempty));
         }
-        if (leader) {
-          mbar_arrive(smem_addr(sh.lempty + b));
-          if (split < blocks) mma_commit(smem_addr(&sh.uempty));
-        }
+        if (leader) mbar_arrive(smem_addr(sh.lempty + b));
       }
       if (ok && leader) mma_commit(smem_addr(sh.tfull + buf));
       __syncwarp();
@@ -1009,7 +1032,7 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
     // ---- the tile's adapters, the rows that do not use each of them, and u ----
     const int m = tid - 192;
     int lt = 0;
-    uint32_t uphase = 0;  // tiles whose u was loaded
+    uint32_t uphase = 0;  // parts of tiles' u that were loaded
     for (int w = first; w < total; w += stride, ++lt) {
       const int b = lt & 1;
       const LTile t = ltile_of<BN>(w, a);
@@ -1028,11 +1051,12 @@ __global__ void __launch_bounds__(kGemmLThreads, 1)
       // they took 0.7 us a block.
       if (warp == 6 && split < n * rblocks) {
         grid_dependency_wait();  // u is written
-        if (warp_wait(&sh.uempty, (uphase & 1u) ^ 1u, abort, a.err)) {
+        for (int part = 0; part < a.parts; ++part) {
+          if (!warp_wait(&sh.uempty, (uphase & 1u) ^ 1u, abort, a.err)) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&sh.ufull, static_cast<uint32_t>(rblocks * a.xrows) * kLRow);
             for (int q = 0; q < rblocks; ++q)
-              tma_load_2d(ubuf + q * a.xbytes, &map_u, q * kLBK, t.t0, smem_addr(&sh.ufull));
+              tma_load_2d(ubuf + q * a.xbytes, &map_u, q * kLBK, part * a.T + t.t0, smem_addr(&sh.ufull));
           }
           __syncwarp();
           ++uphase;
@@ -1164,11 +1188,14 @@ __global__ void __launch_bounds__(kOneThreads, 2)
       const uint4 *u = reinterpret_cast<const uint4 *>(a.u);
       const uint4 *b = lora_b + (static_cast<int64_t>(id) * a.N + row0 + r) * rv;
       for (int v = sub; v < rv; v += 8) {
-        float uf[8], bf[8];
-        unpack8(__ldcg(u + v), uf);
+        float bf[8];
         unpack8(__ldg(b + v), bf);
+        for (int part = 0; part < a.parts; ++part) {
+          float uf[8];
+          unpack8(__ldcg(u + part * rv + v), uf);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f = fmaf(uf[e], bf[e], f);
+          for (int e = 0; e < 8; ++e) f = fmaf(uf[e], bf[e], f);
+        }
       }
     }
   }
@@ -1411,7 +1438,7 @@ moe_status launch_gemm(LoraArgs a, const void *x, const void *w, const void *lor
   if (!make_box_map(&mx, x, a.K, a.T, a.xrows) || !make_box_map(&mw, w, a.K, a.N, kBox)) return MOE_ECUDA;
   mu = mx;
   mb = mw;  // not used without adapters
-  if (a.lora && (!make_box_map(&mu, a.u, a.rank, a.T, a.xrows) ||
+  if (a.lora && (!make_box_map(&mu, a.u, a.rank, static_cast<int64_t>(a.parts) * a.T, a.xrows) ||
                  !make_box_map(&mb, lora_b, a.rank, static_cast<int64_t>(a.adapters) * a.N, kBox, a.packed > 0 ? 16 : kLBK)))
     return MOE_ECUDA;
   return launch_cluster<lora_gemm_kernel<BN, SPLIT>>(kLSmemMax - kLStatic, dim3(static_cast<unsigned>(grid)), kGemmLThreads,
@@ -1439,9 +1466,11 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
   const int T = desc->num_tokens, K = desc->in_dim, N = desc->out_dim, r = desc->rank, A = desc->num_adapters;
   if (T < 0 || K < 8 || N < 8 || A < 0 || K % 8 != 0 || N % 8 != 0 || desc->num_sms < 0) return MOE_EINVAL;
   if (A > 0 && (r < 8 || r > kLMaxRank || r % 8 != 0)) return MOE_EINVAL;
+  const int parts = desc->u_parts > 1 ? desc->u_parts : 1;
+  if (desc->u_parts < 0 || parts > 2) return MOE_EINVAL;
   // weight rows are 32-bit TMA coordinates, a tile's last ones may lie up to 256 past the end
   if (static_cast<int64_t>(A) * N > INT32_MAX - 256 || static_cast<int64_t>(A) * r > INT32_MAX - 256 ||
-      T > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256)
+      static_cast<int64_t>(parts) * T > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256)
     return MOE_EINVAL;
   if (err == nullptr || !aligned4(err)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
@@ -1464,6 +1493,7 @@ extern "C" moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, 
   a.rank = A > 0 ? r : kLBK;
   a.adapters = A;
   a.lora = A > 0;
+  a.parts = parts;
   a.xrows = T >= kLBM ? kLBM : (T + 7) / 8 * 8;
   a.xbytes = a.xrows * kLRow;
   a.kblocks = (K + kLBK - 1) / kLBK;

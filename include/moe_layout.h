@@ -499,11 +499,14 @@ typedef struct {
   int32_t rank;         /* a multiple of 8, at most 256 (ignored without adapters) */
   int32_t num_adapters; /* A >= 0; 0: the projection alone */
   int32_t num_sms;      /* SMs the projection's CTAs are spread over; 0, or more than there are: all */
+  int32_t u_parts;      /* 0 or 1: u is one bf16 matrix; 2: two, so that it keeps 16 bits and more of a product */
 } moe_lora_desc;
 
 /* For every token t with a = adapter[t]:
  *   u[t] = bf16_rne( scales[a] * x[t] lora_a[a]^T ),
  *   y[t] = bf16_rne( x[t] w^T + u[t] lora_b[a]^T ),
+ * or, with u_parts = 2, u[t] and u'[t] = bf16_rne( scales[a] * x[t] lora_a[a]^T - u[t] ) and the sum of both with
+ * lora_b[a]^T (u' is 0 where u is not finite), so that rounding u leaves 2^-18 of it instead of 2^-9;
  * products in bf16 accumulated in fp32 on the tensor cores; adapter -1 has no
  * second term. Adapters of a smaller rank are padded with zero rows of lora_a or
  * zero columns of lora_b. The adapters may be in any order over the tokens; a
@@ -511,7 +514,7 @@ typedef struct {
  *   x [T][in_dim], w [out_dim][in_dim], lora_a [A][rank][in_dim],
  *   lora_b [A][out_dim][rank] bf16; scales [A] float or NULL (all 1);
  *   adapter [T] int32 (read);
- *   u [T][rank] bf16 (written: rows of tokens with an adapter; a scratch buffer
+ *   u [u_parts][T][rank] bf16 (written: rows of tokens with an adapter; a scratch buffer
  *   the caller may reuse after the call in stream order); y [T][out_dim] bf16
  *   (written). All matrices 16-byte aligned. With A = 0 lora_a, lora_b, scales,
  *   adapter and u may be NULL.

@@ -61,3 +61,18 @@ def test_a_result_of_expert_grad_of_another_type_or_size_is_refused():
             layer.backward(x, logits, bad)
     layer.backward(x, logits, lambda px, off, gy: gy)
     assert layer.error() == B.MOE_OK
+
+
+@pytest.mark.parametrize("parts", [1, 2])
+def test_parts_of_u(parts):
+    """The bits of the entry point with as many parts; two are what shared takes by itself."""
+    require_gpu()
+    layer, draw = layer_and_rows(90, 128)
+    x, w, la, lb = draw(90, 128), draw(264, 128), draw(3, 24, 128), draw(3, 264, 24)
+    ids = (torch.arange(90) % 4 - 1).to(torch.int32).cuda()
+    y = layer.shared(x, w, la, lb, None, ids, u_parts=parts)
+    u, want = torch.empty((parts, 90, 24), dtype=torch.bfloat16, device="cuda:0"), torch.empty_like(y)
+    B.moe_lora_linear(B.MoeLoraDesc(90, 128, 264, 24, 3, 0, parts), x, w, la, lb, None, ids, u, want, layer.err)
+    assert layer.error() == B.MOE_OK and torch.equal(y, want) and layer.u.shape == (90, 24)
+    if parts == 2:
+        assert torch.equal(layer.shared(x, w, la, lb, None, ids), y)

@@ -80,6 +80,11 @@ def test_shared_without_adapters_takes_none_of_their_arguments():
     refused("adapter", layer().shared, GOOD["x"], GOOD["w"], adapter=GOOD["adapter"])
 
 
+@pytest.mark.parametrize("parts", [0, 3, None])
+def test_shared_refuses_parts(parts):
+    refused("u_parts", layer().shared, **GOOD, u_parts=parts)
+
+
 def test_what_passes_reaches_the_binding():
     w = type("W", (), dict(w_gate=z(E, 128, H), w_up=z(E, 128, H), w_down=z(E, H, 128)))()
     for call in (lambda: layer().route(f(T, E), f(E)), lambda: layer().route(f(2, 3, E)),
