@@ -70,6 +70,39 @@ class MoeLoraDesc(ctypes.Structure):
     ]
 
 
+MOE_ACT_SILU, MOE_ACT_GELU_TANH = 0, 1
+MOE_SAVE_NONE, MOE_SAVE_BF16, MOE_SAVE_FP8 = 0, 1, 2
+
+
+class MoeFfnDesc(ctypes.Structure):
+    """A gated feed-forward block and what its forward keeps (moe_ffn_desc of include/moe_layout.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("hidden", ctypes.c_int32),
+        ("inter", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("num_ranks", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("save", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+    ]
+
+
+MOE_GATE_NONE, MOE_GATE_ROW, MOE_GATE_CHANNEL = 0, 1, 2
+
+
+class MoeNormDesc(ctypes.Structure):
+    """The norms around a block, its gate and the residual scale (moe_norm_desc of include/moe_layout.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("stream_fp32", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("alpha", ctypes.c_float),
+    ]
+
+
 MOE_MAX_PARTS = 8
 
 
@@ -140,6 +173,13 @@ def _open(path: str):
     lib.moe_unsort.argtypes = [pdesc] + [vp] * 6
     lib.moe_unsort_grad.argtypes = [pdesc] + [vp] * 8
     lib.moe_lora_linear.argtypes = [ctypes.POINTER(MoeLoraDesc)] + [vp] * 10
+    pffn, pnorm = ctypes.POINTER(MoeFfnDesc), ctypes.POINTER(MoeNormDesc)
+    lib.moe_ffn.argtypes = [pffn] + [vp] * 13
+    lib.moe_ffn_grad.argtypes = [pffn] + [vp] * 19
+    lib.moe_norm.argtypes = [pnorm] + [vp] * 9
+    lib.moe_norm_workspace.argtypes = [pnorm]
+    lib.moe_norm_workspace.restype = ctypes.c_int64
+    lib.moe_norm_grad.argtypes = [pnorm] + [vp] * 15
     lib.moe_get_error.argtypes = [vp, vp]
     lib.moe_layout_dispatch_kernels.argtypes = [pdesc]
     lib.moe_layout_dispatch_kernels.restype = ctypes.c_int32
@@ -150,7 +190,8 @@ def _open(path: str):
                  "moe_expert_gate_up", "moe_expert_down", "moe_expert_mlp_noalloc", "moe_expert_gate_up_fp8",
                  "moe_expert_down_fp8", "moe_expert_mlp_noalloc_fp8", "moe_layout_dispatch_parts",
                  "moe_combine_parts", "moe_expert_stub_parts", "moe_reset_parts", "moe_gate", "moe_gate_grad",
-                 "moe_sort", "moe_sort_grad", "moe_unsort", "moe_unsort_grad", "moe_lora_linear", "moe_get_error"):
+                 "moe_sort", "moe_sort_grad", "moe_unsort", "moe_unsort_grad", "moe_lora_linear", "moe_ffn", "moe_ffn_grad",
+                 "moe_norm", "moe_norm_grad", "moe_get_error"):
         getattr(lib, name).restype = st
     return lib
 
@@ -348,6 +389,40 @@ def moe_unsort_grad(desc, packed_y, tok_packed, topk_weights, grad_out, grad_pac
 def moe_lora_linear(desc: MoeLoraDesc, x, w, lora_a, lora_b, scales, adapter, u, y, err, stream=None):
     _check(load().moe_lora_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b), _ptr(scales),
                                   _ptr(adapter), _ptr(u), _ptr(y), _ptr(err), _stream(stream)), "moe_lora_linear")
+
+
+def moe_ffn(desc: MoeFfnDesc, region_offsets, x, w_gate, w_up, w_down, h, y, gate, gate_scales, up, up_scales, err,
+            stream=None):
+    _check(load().moe_ffn(ctypes.byref(desc), _ptr(region_offsets), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                          _ptr(h), _ptr(y), _ptr(gate), _ptr(gate_scales), _ptr(up), _ptr(up_scales), _ptr(err),
+                          _stream(stream)), "moe_ffn")
+
+
+def moe_ffn_grad(desc: MoeFfnDesc, region_offsets, x, gate, gate_scales, up, up_scales, w_gate, w_up, w_down, grad_y, h,
+                 grad_gate, grad_up, grad_x, grad_w_gate, grad_w_up, grad_w_down, err, stream=None):
+    _check(load().moe_ffn_grad(ctypes.byref(desc), _ptr(region_offsets), _ptr(x), _ptr(gate), _ptr(gate_scales),
+                               _ptr(up), _ptr(up_scales), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(grad_y),
+                               _ptr(h), _ptr(grad_gate), _ptr(grad_up), _ptr(grad_x), _ptr(grad_w_gate),
+                               _ptr(grad_w_up), _ptr(grad_w_down), _ptr(err), _stream(stream)), "moe_ffn_grad")
+
+
+def moe_norm(desc: MoeNormDesc, x, o, w_post, gate, w_pre, r, n, err, stream=None):
+    _check(load().moe_norm(ctypes.byref(desc), _ptr(x), _ptr(o), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(r),
+                           _ptr(n), _ptr(err), _stream(stream)), "moe_norm")
+
+
+def moe_norm_workspace(desc: MoeNormDesc) -> int:
+    n = int(load().moe_norm_workspace(ctypes.byref(desc)))
+    _check(min(n, 0), "moe_norm_workspace")
+    return n
+
+
+def moe_norm_grad(desc: MoeNormDesc, r, o, w_post, gate, w_pre, grad_r, grad_n, grad_x, grad_o, grad_w_post, grad_gate,
+                  grad_w_pre, workspace, err, stream=None):
+    _check(load().moe_norm_grad(ctypes.byref(desc), _ptr(r), _ptr(o), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                                _ptr(grad_r), _ptr(grad_n), _ptr(grad_x), _ptr(grad_o), _ptr(grad_w_post),
+                                _ptr(grad_gate), _ptr(grad_w_pre), _ptr(workspace), _ptr(err), _stream(stream)),
+           "moe_norm_grad")
 
 
 def moe_get_error(err, stream=None) -> int:

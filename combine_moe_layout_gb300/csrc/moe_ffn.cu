@@ -1,0 +1,781 @@
+// The gated feed-forward block in training: linear 1 that keeps its projections,
+// linear 2, and the gradients with respect to the rows and all three weights, for
+// the packed rows of every expert (or one dense block), on the 5th-generation
+// tensor cores.
+//
+//   g = x w_gate^T, u = x w_up^T, h = bf16(act(g) u), y = h w_down^T
+//   dh = dy w_down;  dg = dh u act'(g), du = dh act(g)
+//   dx = dg w_gate + du w_up
+//   dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h   (sums over an expert's rows)
+//
+// One persistent kernel, a CTA per SM, in five forms. Roles as in the expert
+// stage: a TMA producer warp, an MMA warp with two 128 x 256 fp32 accumulators in
+// tensor memory, four epilogue warps; in the weights' form a seventh warp that
+// clears what the last K block of an expert holds of the next one's rows.
+//
+//   form   D [128 x up to 256]        A                    B                     K
+//   kUp    g | u (128 + 128 columns)  x          K-major   w_gate | w_up K-major H
+//   kDown  y                          h          K-major   w_down  K-major       I
+//   kDh    dh, made dg, du and h      dy         K-major   w_down  N-major       H
+//   kDx    dx                         dg then du K-major   w_gate then w_up, N-major   2 I
+//   kDw    dw (three of them)         dg, du, dy M-major   x, x, h  N-major      rows of the expert
+//
+// The transposed operands are read as they lie in memory: a box of 64 columns and
+// 64 rows lands as 64 swizzled 128-byte lines, the M- or N-major form of the
+// 128-byte swizzle (64 elements contiguous, lines of successive k 128 bytes
+// apart), so that no kernel transposes anything. Weights have 3-D maps, [expert]
+// outermost: a box that passes an expert's last row or column is filled with
+// zeros, whatever the next expert's weights hold, and widths need only be
+// multiples of 8.
+//
+// What is rounded: h, dg and du to bf16 between two products (each is an operand
+// of bf16 tensor cores: 2^-9 of a term, as its output's own rounding), sums in
+// fp32 throughout.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "moe_tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBK = 64;
+constexpr int kUK = 16;
+constexpr int kBN = 256;
+constexpr int kStages = 4;
+constexpr int kTileA = kBM * kBK * 2;
+constexpr int kTileB = kBN * kBK * 2;
+constexpr int kStage = kTileA + kTileB;
+constexpr int kHalfBox = 64 * kBK * 2;    // a box of 64 columns x 64 rows
+constexpr int kFullBox = 128 * kBK * 2;   // a box of 64 columns x 128 rows
+constexpr int kThreads = 192, kThreadsDw = 224;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemFixed = 1024 + kStages * kStage + (2 * kStages + 7) * 8 + 8;
+constexpr int kSmemMax = 227 * 1024;
+
+enum Form { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
+
+__host__ __device__ constexpr bool a_is_mn(int form) { return form == kDw; }
+__host__ __device__ constexpr bool b_is_mn(int form) { return form >= kDh; }
+
+// Descriptor of an M- or N-major bf16 tile with the 128-byte swizzle, made of boxes
+// of 64 (M or N) x 64 (K): the leading-dimension offset is the next box (8192
+// bytes), the stride offset the next 8 lines of K (1024 bytes).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kHalfBox >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+struct FfnMaps {
+  CUtensorMap m[5];
+};
+
+struct FfnArgs {
+  const int32_t *offsets;  // [E * R + 1], or null: one expert with all rows
+  int32_t *err;
+  void *out0, *out1, *out2;             // by form: h | y | dg, du, h | dx | dw_gate, dw_up, dw_down
+  const void *gate, *up;                // kDh: what the forward kept
+  const float *gate_scales, *up_scales;
+  void *keep_gate, *keep_up;            // kUp: what it keeps
+  float *keep_gate_scales, *keep_up_scales;
+  int rows, E, R;
+  int H, I;
+  int kblocks;    // K blocks of a tile (kDw: by the expert's rows)
+  int n_total;    // output columns
+  int out_cols;   // output columns of a tile: 128 (kUp) or 256
+  int ntiles_n, group_n;
+  int act, save;
+  int dw_total;   // kDw: tiles of all experts
+};
+
+struct Job {
+  int e, row0, rows;  // packed rows (kDw: all of the expert's)
+  int m0, n0, ncols;  // kDw: first row of the weight; first output column and the tile's MMA width
+  int which;          // kDw: 0 dw_gate, 1 dw_up, 2 dw_down
+  int kblocks, tail;  // tail: rows of the last K block (kDw; 64 or 0: whole)
+};
+
+template <int FORM>
+__device__ __forceinline__ Job job_of(int w, const int32_t *pref, const int32_t *offs, const FfnArgs &a) {
+  Job j;
+  if constexpr (FORM == kDw) {
+    // expert by expert; in each the three weights, in groups of group_n column tiles swept by row tiles
+    const int mi = (a.I + kBM - 1) / kBM, mh = (a.H + kBM - 1) / kBM;
+    const int ni = (a.I + kBN - 1) / kBN, nh = (a.H + kBN - 1) / kBN;
+    const int p01 = mi * nh, per = 2 * p01 + mh * ni;
+    j.e = w / per;
+    int r = w - j.e * per;
+    j.which = r < p01 ? 0 : (r < 2 * p01 ? 1 : 2);
+    r -= j.which * p01;
+    const int mt = j.which == 2 ? mh : mi, nt = j.which == 2 ? ni : nh;
+    const int g = r / (mt * a.group_n);
+    r -= g * mt * a.group_n;
+    const int gw = min(a.group_n, nt - g * a.group_n);
+    const int m = r / gw;
+    j.m0 = m * kBM;
+    j.n0 = (g * a.group_n + r - m * gw) * kBN;
+    const int left = (j.which == 2 ? a.I : a.H) - j.n0;
+    j.ncols = min(kBN, (left + 63) & ~63);
+    const int lo = offs[j.e], hi = offs[j.e + 1];
+    const bool good = lo >= 0 && hi >= lo && hi <= a.rows;
+    j.row0 = good ? lo : 0;
+    j.rows = good ? hi - lo : 0;
+    j.kblocks = (j.rows + kBK - 1) / kBK;
+    j.tail = j.rows & (kBK - 1);
+  } else {
+    const Tile t = tile_of<kBM>(w, pref, offs, a);
+    j.e = t.e;
+    j.row0 = t.row0;
+    j.rows = t.rows;
+    j.m0 = 0;
+    j.n0 = t.n0;
+    j.which = 0;
+    j.kblocks = a.kblocks;
+    j.tail = 0;
+    if constexpr (FORM == kUp)
+      j.ncols = kBN;
+    else if constexpr (FORM == kDown)
+      j.ncols = a.n_total - t.n0 > 128 ? 256 : 128;
+    else
+      j.ncols = min(kBN, (a.n_total - t.n0 + 63) & ~63);
+  }
+  return j;
+}
+
+// act(g) and act'(g), in fp32.
+template <bool GRAD>
+__device__ __forceinline__ float act_of(float g, int act, float *da) {
+  if (act == MOE_ACT_SILU) {
+    const float p = 1.0f / (1.0f + expf(-g));
+    if constexpr (GRAD) *da = p * (1.0f + g * (1.0f - p));
+    return g * p;
+  }
+  constexpr float k = 0.7978845608028654f, c = 0.044715f;  // sqrt(2 / pi)
+  const float t = tanhf(k * (g + c * g * g * g));
+  if constexpr (GRAD) *da = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * k * (1.0f + 3.0f * c * g * g);
+  return 0.5f * g * (1.0f + t);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ float lo_of(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_of(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ void e4m3x2_to_float(uint16_t c, float *lo, float *hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  float a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "r"(h));
+  *lo = a;
+  *hi = b;
+}
+
+// ---- epilogues: one thread, its accumulator row ----
+
+// y, dx, dw: 32 columns, rounded.
+__device__ __forceinline__ void store_plain(__nv_bfloat16 *dst, const uint32_t *r, int left) {
+  uint4 *d = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (8 * v < left)
+      d[v] = make_uint4(pack2(__uint_as_float(r[8 * v]), __uint_as_float(r[8 * v + 1])),
+                        pack2(__uint_as_float(r[8 * v + 2]), __uint_as_float(r[8 * v + 3])),
+                        pack2(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
+                        pack2(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
+  }
+}
+
+// h = act(g) u for 32 columns; r: g then u.
+__device__ __forceinline__ void store_hidden(__nv_bfloat16 *dst, const uint32_t (&r)[64], int act, int left) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float h0 = act_of<false>(__uint_as_float(r[2 * i]), act, nullptr) * __uint_as_float(r[32 + 2 * i]);
+    const float h1 = act_of<false>(__uint_as_float(r[2 * i + 1]), act, nullptr) * __uint_as_float(r[33 + 2 * i]);
+    pk[i] = pack2(h0, h1);
+  }
+  uint4 *d = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (8 * v < left) d[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+}
+
+// 32 columns as e4m3 codes of the block's scale (library format: amax / 448 over 128 columns).
+__device__ __forceinline__ void store_codes(uint8_t *dst, const uint32_t *r, const BlockScale &bs) {
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    q[i] = static_cast<uint32_t>(
+               e4m3x2_of_quotients(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), bs)) |
+           (static_cast<uint32_t>(
+                e4m3x2_of_quotients(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]), bs))
+            << 16);
+  uint4 *d = reinterpret_cast<uint4 *>(dst);
+  d[0] = make_uint4(q[0], q[1], q[2], q[3]);
+  d[1] = make_uint4(q[4], q[5], q[6], q[7]);
+}
+
+__device__ __forceinline__ void epilogue_up(const FfnArgs &a, const Job &t, uint32_t tb, int m) {
+  const bool valid = m < t.rows;
+  const int64_t p = t.row0 + (valid ? m : 0);
+  const int left = a.I - t.n0;  // columns of the tile that exist
+  const int64_t at = p * a.I + t.n0;
+  BlockScale gs, us;
+  if (a.save == MOE_SAVE_FP8) {  // I is a multiple of 128: the tile's 128 columns are one block
+    float ga = 0.0f, ua = 0.0f;
+    for (int c = 0; c < 128; c += 32) {
+      uint32_t r[64];
+      tmem_load32x2_wait(tb + c, tb + 128 + c, r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        ga = fmaxf(ga, fabsf(__uint_as_float(r[i])));
+        ua = fmaxf(ua, fabsf(__uint_as_float(r[32 + i])));
+      }
+    }
+    gs = block_scale(ga);
+    us = block_scale(ua);
+    if (valid) {
+      const int64_t sc = p * (a.I / kScaleBlock) + t.n0 / kScaleBlock;
+      a.keep_gate_scales[sc] = gs.s;
+      a.keep_up_scales[sc] = us.s;
+    }
+  }
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t r[64];
+    tmem_load32x2_wait(tb + c, tb + 128 + c, r);
+    if (!valid) continue;
+    store_hidden(static_cast<__nv_bfloat16 *>(a.out0) + at + c, r, a.act, left - c);
+    if (a.save == MOE_SAVE_BF16) {
+      store_plain(static_cast<__nv_bfloat16 *>(a.keep_gate) + at + c, r, left - c);
+      store_plain(static_cast<__nv_bfloat16 *>(a.keep_up) + at + c, r + 32, left - c);
+    } else if (a.save == MOE_SAVE_FP8) {
+      store_codes(static_cast<uint8_t *>(a.keep_gate) + at + c, r, gs);
+      store_codes(static_cast<uint8_t *>(a.keep_up) + at + c, r + 32, us);
+    }
+  }
+}
+
+__device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint32_t tb, int m) {
+  const bool valid = m < t.rows;
+  const int64_t p = t.row0 + (valid ? m : 0);
+  for (int c = 0; c < t.ncols; c += 32) {
+    const int left = a.I - t.n0 - c;
+    const int64_t at = p * a.I + t.n0 + c;
+    uint32_t gq[16], uq[16];  // 32 values as bf16 pairs, or as codes in the first 8
+    float gsc = 1.0f, usc = 1.0f;
+    if (valid) {
+      const bool f8 = a.save == MOE_SAVE_FP8;
+      const uint4 *gp = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.gate) + (f8 ? at : 2 * at));
+      const uint4 *up = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.up) + (f8 ? at : 2 * at));
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if ((f8 ? 16 : 8) * v < left && !(f8 && v >= 2)) {
+          const uint4 x = __ldg(gp + v), y = __ldg(up + v);
+          gq[4 * v] = x.x, gq[4 * v + 1] = x.y, gq[4 * v + 2] = x.z, gq[4 * v + 3] = x.w;
+          uq[4 * v] = y.x, uq[4 * v + 1] = y.y, uq[4 * v + 2] = y.z, uq[4 * v + 3] = y.w;
+        } else {
+          gq[4 * v] = gq[4 * v + 1] = gq[4 * v + 2] = gq[4 * v + 3] = 0;
+          uq[4 * v] = uq[4 * v + 1] = uq[4 * v + 2] = uq[4 * v + 3] = 0;
+        }
+      }
+      if (f8 && left > 0) {
+        const int64_t sc = p * (a.I / kScaleBlock) + (t.n0 + c) / kScaleBlock;
+        gsc = __ldg(a.gate_scales + sc);
+        usc = __ldg(a.up_scales + sc);
+      }
+    }
+    uint32_t r[32];
+    tmem_load32_wait(tb + c, r);
+    if (!valid) continue;
+    uint4 *od = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out0) + at);
+    uint4 *ou = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out1) + at);
+    uint4 *oh = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out2) + at);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      uint32_t pd[4], pu[4], ph[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float g0, g1, u0, u1;
+        const int k = 4 * v + i;  // the pair of columns 2 k, 2 k + 1
+        if (a.save == MOE_SAVE_FP8) {
+          e4m3x2_to_float(static_cast<uint16_t>(gq[k >> 1] >> (16 * (k & 1))), &g0, &g1);
+          e4m3x2_to_float(static_cast<uint16_t>(uq[k >> 1] >> (16 * (k & 1))), &u0, &u1);
+          g0 *= gsc, g1 *= gsc, u0 *= usc, u1 *= usc;
+        } else {
+          g0 = lo_of(gq[k]), g1 = hi_of(gq[k]), u0 = lo_of(uq[k]), u1 = hi_of(uq[k]);
+        }
+        float d0, d1;
+        const float a0 = act_of<true>(g0, a.act, &d0), a1 = act_of<true>(g1, a.act, &d1);
+        const float h0 = __uint_as_float(r[2 * k]), h1 = __uint_as_float(r[2 * k + 1]);
+        pd[i] = pack2(h0 * u0 * d0, h1 * u1 * d1);
+        pu[i] = pack2(h0 * a0, h1 * a1);
+        ph[i] = pack2(a0 * u0, a1 * u1);
+      }
+      if (8 * v < left) {
+        od[v] = make_uint4(pd[0], pd[1], pd[2], pd[3]);
+        ou[v] = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+        oh[v] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+      }
+    }
+  }
+}
+
+template <int FORM>
+__device__ __forceinline__ void epilogue_plain(const FfnArgs &a, const Job &t, uint32_t tb, int m) {
+  bool valid;
+  __nv_bfloat16 *dst;
+  int width;
+  if constexpr (FORM == kDw) {
+    width = t.which == 2 ? a.I : a.H;
+    const int height = t.which == 2 ? a.H : a.I;
+    valid = t.m0 + m < height;
+    void *base = t.which == 0 ? a.out0 : (t.which == 1 ? a.out1 : a.out2);
+    dst = static_cast<__nv_bfloat16 *>(base) +
+          (static_cast<int64_t>(t.e) * height + t.m0 + (valid ? m : 0)) * width + t.n0;
+  } else {
+    width = a.n_total;
+    valid = m < t.rows;
+    dst = static_cast<__nv_bfloat16 *>(a.out0) + static_cast<int64_t>(t.row0 + (valid ? m : 0)) * width + t.n0;
+  }
+  if (FORM == kDw && t.kblocks == 0) {  // an expert without rows: its gradient is 0
+    for (int c = 0; valid && c < t.ncols && t.n0 + c < width; c += 8)
+      *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  for (int c = 0; c < t.ncols; c += 32) {
+    uint32_t r[32];
+    tmem_load32_wait(tb + c, r);
+    if (valid) store_plain(dst + c, r, width - t.n0 - c);
+  }
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs a) {
+  constexpr int kT = FORM == kDw ? kThreadsDw : kThreads;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage);
+  uint64_t *empty = full + kStages;
+  uint64_t *tail = empty + kStages;  // kDw: an expert's last K block has landed; its tail has been cleared
+  uint64_t *cleared = tail + 1;
+  uint64_t *tfull = cleared + 1;
+  uint64_t *tempty = tfull + 2;
+  uint64_t *done = tempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int32_t *offs = reinterpret_cast<int32_t *>(tmem_slot + 2);
+  int32_t *pref = offs + (a.E + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull + b, 1);
+      mbar_init(tempty + b, 4);
+    }
+    mbar_init(tail, 1);
+    mbar_init(cleared, 1);
+    mbar_init(done, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (tid == 32)
+    for (int i = 0; i < 5; ++i) prefetch_tensormap(&maps.m[i]);
+  grid_dependency_wait();
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  for (int e = tid; e <= a.E; e += kT)
+    offs[e] = a.offsets != nullptr ? a.offsets[static_cast<int64_t>(e) * a.R] : (e == 0 ? 0 : a.rows);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // (in the weights' form it only looks the offsets over)
+  if (warp == 0) tile_prefix<kBM>(offs, pref, a, lane);
+  __syncthreads();
+  const int total = FORM == kDw ? a.dw_total : tile_total(pref, a);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- TMA producer ----
+      uint32_t it = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+        const Job t = job_of<FORM>(w, pref, offs, a);
+        const uint32_t bytes = kTileA + t.ncols * kBK * 2;
+        for (int kb = 0; kb < t.kblocks; ++kb) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+          if (!role_wait(empty + s, ph ^ 1u, abort, a.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA, fb = smem_addr(full + s);
+          mbar_arrive_expect_tx(full + s, bytes);
+          if constexpr (FORM == kUp) {
+            tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
+            tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, fb);
+            tma_load_3d(sb + kFullBox, &maps.m[2], kb * kBK, t.n0, t.e, fb);
+          } else if constexpr (FORM == kDown) {
+            tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
+            tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, fb);
+            if (t.ncols > 128) tma_load_3d(sb + kFullBox, &maps.m[1], kb * kBK, t.n0 + 128, t.e, fb);
+          } else if constexpr (FORM == kDh) {
+            tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
+            for (int c = 0; c < t.ncols; c += 64)
+              tma_load_3d(sb + c / 64 * kHalfBox, &maps.m[1], t.n0 + c, kb * kBK, t.e, fb);
+          } else if constexpr (FORM == kDx) {
+            const int second = kb >= t.kblocks / 2 ? 1 : 0;
+            const int k = (kb - second * (t.kblocks / 2)) * kBK;
+            tma_load_2d(sa, &maps.m[second], k, t.row0, fb);
+            for (int c = 0; c < t.ncols; c += 64)
+              tma_load_3d(sb + c / 64 * kHalfBox, &maps.m[2 + second], t.n0 + c, k, t.e, fb);
+          } else {
+            // maps: dg, du, dy (A), x, h (B)
+            const int k = t.row0 + kb * kBK;
+            for (int c = 0; c < kBM; c += 64)
+              tma_load_2d(sa + c / 64 * kHalfBox, &maps.m[t.which], t.m0 + c, k, fb);
+            for (int c = 0; c < t.ncols; c += 64)
+              tma_load_2d(sb + c / 64 * kHalfBox, &maps.m[t.which == 2 ? 4 : 3], t.n0 + c, k, fb);
+          }
+          ++it;
+        }
+      }
+      // the last load issued into each stage lands before the CTA may exit
+      for (uint32_t s = 0; s < kStages && s < it; ++s) {
+        const uint32_t last = s + ((it - 1 - s) / kStages) * kStages;
+        mbar_wait_bounded(full + s, (last / kStages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- MMA issuer ----
+      uint32_t it = 0, tails = 0;
+      int lt = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++lt) {
+        const Job t = job_of<FORM>(w, pref, offs, a);
+        const uint32_t idesc = idesc_bf16(kBM, t.ncols) | (a_is_mn(FORM) ? 1u << 15 : 0u) |
+                               (b_is_mn(FORM) ? 1u << 16 : 0u);
+        const int buf = lt & 1;
+        const uint32_t ph = (lt >> 1) & 1;
+        if (!role_wait(tempty + buf, ph ^ 1u, abort, a.err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * kBN;
+        for (int kb = 0; kb < t.kblocks; ++kb) {
+          const uint32_t s = it % kStages, sph = (it / kStages) & 1u;
+          if (!role_wait(full + s, sph, abort, a.err)) {
+            ok = false;
+            break;
+          }
+          if (FORM == kDw && t.tail != 0 && kb == t.kblocks - 1) {
+            mbar_arrive(smem_addr(tail));
+            if (!role_wait(cleared, tails & 1u, abort, a.err)) {
+              ok = false;
+              break;
+            }
+            ++tails;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA;
+#pragma unroll
+          for (int kk = 0; kk < kBK / kUK; ++kk)
+            mma_bf16(d, a_is_mn(FORM) ? sw128_desc_mn(sa + kk * kUK * 128) : sw128_desc(sa + kk * kUK * 2),
+                     b_is_mn(FORM) ? sw128_desc_mn(sb + kk * kUK * 128) : sw128_desc(sb + kk * kUK * 2), idesc,
+                     (kb | kk) != 0);
+          mma_commit(smem_addr(empty + s));
+          ++it;
+        }
+        if (ok) mma_commit(smem_addr(tfull + buf));
+      }
+      // every MMA issued completes before the tensor memory is freed
+      mma_commit(smem_addr(done));
+      mbar_wait_bounded(done, 0);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // ---- epilogue: warps 2..5, warp w reads TMEM lanes 32 * (w % 4) .. + 31 ----
+    const int q = warp & 3;
+    const int m = q * 32 + lane;
+    int lt = 0;
+    for (int w = blockIdx.x; w < total; w += gridDim.x, ++lt) {
+      const int buf = lt & 1;
+      const uint32_t ph = (lt >> 1) & 1;
+      int ok = 0;
+      if (lane == 0) ok = role_wait(tfull + buf, ph, abort, a.err) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const Job t = job_of<FORM>(w, pref, offs, a);
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBN;
+      if constexpr (FORM == kUp)
+        epilogue_up(a, t, tb, m);
+      else if constexpr (FORM == kDh)
+        epilogue_dh(a, t, tb, m);
+      else
+        epilogue_plain<FORM>(a, t, tb, m);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(tempty + buf));
+    }
+  } else if constexpr (FORM == kDw) {
+    // ---- clears the rows of the last K block that are not the expert's (they may hold anything), in both
+    // operands: lines of 128 bytes, one for each k and 64 columns
+    uint32_t it = 0, tails = 0;
+    for (int w = blockIdx.x; w < total; w += gridDim.x) {
+      const Job t = job_of<FORM>(w, pref, offs, a);
+      it += t.kblocks;
+      if (t.tail == 0) continue;
+      const uint32_t s = (it - 1) % kStages;
+      // (asked for by the MMA warp, which waits: of a stage's own barrier this warp would miss phases)
+      int ok = 0;
+      if (lane == 0) ok = role_wait(tail, tails & 1u, abort, a.err) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      ++tails;
+      uint8_t *box = smem + s * kStage;
+      const int boxes = kBM / 64 + t.ncols / 64;  // those of A, and those of B right behind them
+      const int words = (kBK - t.tail) * 8;       // 16-byte words of a box's cleared lines
+      for (int b = 0; b < boxes; ++b)
+        for (int i = lane; i < words; i += 32)
+          *reinterpret_cast<uint4 *>(box + b * kHalfBox + t.tail * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(cleared));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+// Map of a row-major bf16 [z][rows][cols] array (2-D when z = 0), boxes of 64 columns x box_rows rows.
+bool ffn_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t z, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(z)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * rows * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, z > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct FfnSizes {
+  int rows, H, I, E, R, act, save, num_sms;
+};
+
+moe_status check_ffn(const moe_ffn_desc *d, FfnSizes *s) {
+  if (d == nullptr) return MOE_EINVAL;
+  if (d->rows < 0 || d->hidden < 8 || d->hidden % 8 != 0 || d->inter < 8 || d->inter % 8 != 0) return MOE_EINVAL;
+  if (d->num_experts < 1 || d->num_experts > MOE_FFN_MAX_EXPERTS || d->num_ranks < 1 || d->num_sms < 0)
+    return MOE_EINVAL;
+  if (static_cast<int64_t>(d->num_experts) * d->num_ranks > INT32_MAX) return MOE_EINVAL;
+  if (d->act != MOE_ACT_SILU && d->act != MOE_ACT_GELU_TANH) return MOE_EINVAL;
+  if (d->save != MOE_SAVE_NONE && d->save != MOE_SAVE_BF16 && d->save != MOE_SAVE_FP8) return MOE_EINVAL;
+  if (d->save == MOE_SAVE_FP8 && d->inter % kScaleBlock != 0) return MOE_EINVAL;
+  // tiles are counted in 32 bits
+  const int64_t wide = (d->hidden > d->inter ? d->hidden : d->inter) / 64 + 1;
+  if ((d->rows / kBM + static_cast<int64_t>(d->num_experts)) * wide > INT32_MAX ||
+      3 * d->num_experts * (static_cast<int64_t>(d->hidden) / 64 + 1) * (d->inter / 64 + 1) > INT32_MAX)
+    return MOE_EINVAL;
+  *s = FfnSizes{d->rows, d->hidden, d->inter, d->num_experts, d->num_ranks, d->act, d->save, d->num_sms};
+  return MOE_OK;
+}
+
+int group_width(int concurrent, int tile_rows, int tile_cols, int ntiles_n) {
+  const int64_t g = std::llround(std::sqrt(static_cast<double>(concurrent) * tile_rows / tile_cols));
+  return static_cast<int>(g < 1 ? 1 : (g > ntiles_n ? ntiles_n : g));
+}
+
+template <int FORM>
+moe_status launch_form(const FfnMaps &maps, FfnArgs a, const FfnSizes &s, cudaStream_t stream) {
+  const int all = sm_count();
+  const int sms = s.num_sms > 0 && s.num_sms < all ? s.num_sms : all;
+  const int smem = kSmemFixed + 12 * (a.E + 1);
+  if (smem > kSmemMax) return MOE_EINVAL;
+  int64_t tiles;
+  if (FORM == kDw) {
+    const int64_t mi = (a.I + kBM - 1) / kBM, mh = (a.H + kBM - 1) / kBM;
+    const int64_t ni = (a.I + kBN - 1) / kBN, nh = (a.H + kBN - 1) / kBN;
+    tiles = a.E * (2 * mi * nh + mh * ni);
+    a.dw_total = static_cast<int>(tiles);
+    a.ntiles_n = 1;
+    a.group_n = group_width(sms, kBM, kBN, static_cast<int>(nh > ni ? nh : ni));
+  } else {
+    a.ntiles_n = (a.n_total + a.out_cols - 1) / a.out_cols;
+    a.group_n = group_width(sms, kBM, kBN, a.ntiles_n);
+    tiles = (static_cast<int64_t>(a.rows) / kBM + a.E) * a.ntiles_n;
+  }
+  if (!raise_smem_limit(ffn_gemm_kernel<FORM>, smem)) return MOE_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < sms ? tiles : sms), 1, 1);
+  cfg.blockDim = dim3(FORM == kDw ? kThreadsDw : kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  use_pdl(cfg, attr);
+  if (cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<FORM>, maps, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_status();
+}
+
+FfnArgs base_args(const FfnSizes &s, const int32_t *offsets, int32_t *err) {
+  FfnArgs a{};
+  a.offsets = offsets;
+  a.err = err;
+  a.rows = s.rows;
+  a.E = s.E;
+  a.R = s.R;
+  a.H = s.H;
+  a.I = s.I;
+  a.act = s.act;
+  a.save = s.save;
+  return a;
+}
+
+int blocks_of(int k) { return (k + kBK - 1) / kBK; }
+
+bool good16(const void *p) { return p != nullptr && aligned16(p); }
+bool good4(const void *p) { return p != nullptr && aligned4(p); }
+
+bool offsets_ok(const FfnSizes &s, const int32_t *offsets) {
+  return offsets == nullptr ? s.E == 1 : aligned4(offsets);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_offsets, const void *x,
+                              const void *w_gate, const void *w_up, const void *w_down, void *h, void *y, void *gate,
+                              float *gate_scales, void *up, float *up_scales, int32_t *err, void *stream) {
+  FfnSizes s;
+  moe_status st = check_ffn(desc, &s);
+  if (st != MOE_OK) return st;
+  if (!offsets_ok(s, region_offsets) || !good4(err)) return MOE_EINVAL;
+  if (s.rows == 0) return MOE_OK;
+  if (!good16(x) || !good16(w_gate) || !good16(w_up) || !good16(w_down) || !good16(h) || !good16(y))
+    return MOE_EINVAL;
+  if (s.save != MOE_SAVE_NONE && (!good16(gate) || !good16(up))) return MOE_EINVAL;
+  if (s.save == MOE_SAVE_FP8 && (!good4(gate_scales) || !good4(up_scales))) return MOE_EINVAL;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  FfnMaps m{};
+  if (!ffn_map(&m.m[0], x, s.H, s.rows, 0, 128) || !ffn_map(&m.m[1], w_gate, s.H, s.I, s.E, 128) ||
+      !ffn_map(&m.m[2], w_up, s.H, s.I, s.E, 128))
+    return MOE_ECUDA;
+  m.m[3] = m.m[4] = m.m[2];
+  FfnArgs a = base_args(s, region_offsets, err);
+  a.out0 = h;
+  a.keep_gate = gate;
+  a.keep_up = up;
+  a.keep_gate_scales = gate_scales;
+  a.keep_up_scales = up_scales;
+  a.kblocks = blocks_of(s.H);
+  a.n_total = s.I;
+  a.out_cols = 128;
+  st = launch_form<kUp>(m, a, s, cs);
+  if (st != MOE_OK) return st;
+  if (!ffn_map(&m.m[0], h, s.I, s.rows, 0, 128) || !ffn_map(&m.m[1], w_down, s.I, s.H, s.E, 128)) return MOE_ECUDA;
+  a = base_args(s, region_offsets, err);
+  a.out0 = y;
+  a.kblocks = blocks_of(s.I);
+  a.n_total = s.H;
+  a.out_cols = kBN;
+  return launch_form<kDown>(m, a, s, cs);
+}
+
+extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *region_offsets, const void *x,
+                                   const void *gate, const float *gate_scales, const void *up, const float *up_scales,
+                                   const void *w_gate, const void *w_up, const void *w_down, const void *grad_y,
+                                   void *h, void *grad_gate, void *grad_up, void *grad_x, void *grad_w_gate,
+                                   void *grad_w_up, void *grad_w_down, int32_t *err, void *stream) {
+  FfnSizes s;
+  moe_status st = check_ffn(desc, &s);
+  if (st != MOE_OK) return st;
+  if (s.save == MOE_SAVE_NONE) return MOE_EINVAL;
+  if (!offsets_ok(s, region_offsets) || !good4(err)) return MOE_EINVAL;
+  const bool weights = grad_w_gate != nullptr;
+  if ((grad_w_up != nullptr) != weights || (grad_w_down != nullptr) != weights) return MOE_EINVAL;
+  if (weights && (!aligned16(grad_w_gate) || !aligned16(grad_w_up) || !aligned16(grad_w_down))) return MOE_EINVAL;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (s.rows == 0) {
+    if (!weights) return MOE_OK;
+    const size_t n = static_cast<size_t>(s.E) * s.H * s.I * 2;
+    if (cudaMemsetAsync(grad_w_gate, 0, n, cs) != cudaSuccess || cudaMemsetAsync(grad_w_up, 0, n, cs) != cudaSuccess ||
+        cudaMemsetAsync(grad_w_down, 0, n, cs) != cudaSuccess)
+      return MOE_ECUDA;
+    return MOE_OK;
+  }
+  if (!good16(x) || !good16(gate) || !good16(up) || !good16(w_gate) || !good16(w_up) || !good16(w_down) ||
+      !good16(grad_y) || !good16(h) || !good16(grad_gate) || !good16(grad_up) || !good16(grad_x))
+    return MOE_EINVAL;
+  if (s.save == MOE_SAVE_FP8 && (!good4(gate_scales) || !good4(up_scales))) return MOE_EINVAL;
+
+  FfnMaps m{};
+  if (!ffn_map(&m.m[0], grad_y, s.H, s.rows, 0, 128) || !ffn_map(&m.m[1], w_down, s.I, s.H, s.E, 64))
+    return MOE_ECUDA;
+  m.m[2] = m.m[3] = m.m[4] = m.m[1];
+  FfnArgs a = base_args(s, region_offsets, err);
+  a.out0 = grad_gate;
+  a.out1 = grad_up;
+  a.out2 = h;
+  a.gate = gate;
+  a.up = up;
+  a.gate_scales = gate_scales;
+  a.up_scales = up_scales;
+  a.kblocks = blocks_of(s.H);
+  a.n_total = s.I;
+  a.out_cols = kBN;
+  st = launch_form<kDh>(m, a, s, cs);
+  if (st != MOE_OK) return st;
+
+  if (!ffn_map(&m.m[0], grad_gate, s.I, s.rows, 0, 128) || !ffn_map(&m.m[1], grad_up, s.I, s.rows, 0, 128) ||
+      !ffn_map(&m.m[2], w_gate, s.H, s.I, s.E, 64) || !ffn_map(&m.m[3], w_up, s.H, s.I, s.E, 64))
+    return MOE_ECUDA;
+  a = base_args(s, region_offsets, err);
+  a.out0 = grad_x;
+  a.kblocks = 2 * blocks_of(s.I);
+  a.n_total = s.H;
+  a.out_cols = kBN;
+  st = launch_form<kDx>(m, a, s, cs);
+  if (st != MOE_OK || !weights) return st;
+
+  if (!ffn_map(&m.m[0], grad_gate, s.I, s.rows, 0, 64) || !ffn_map(&m.m[1], grad_up, s.I, s.rows, 0, 64) ||
+      !ffn_map(&m.m[2], grad_y, s.H, s.rows, 0, 64) || !ffn_map(&m.m[3], x, s.H, s.rows, 0, 64) ||
+      !ffn_map(&m.m[4], h, s.I, s.rows, 0, 64))
+    return MOE_ECUDA;
+  a = base_args(s, region_offsets, err);
+  a.out0 = grad_w_gate;
+  a.out1 = grad_w_up;
+  a.out2 = grad_w_down;
+  return launch_form<kDw>(m, a, s, cs);
+}

@@ -528,6 +528,101 @@ moe_status moe_lora_linear(const moe_lora_desc *desc, const void *x, const void 
                            const void *lora_b, const float *scales, const int32_t *adapter, void *u, void *y,
                            int32_t *err, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block, for the experts' packed rows (as moe_sort and the
+ * receive hook lay them out) or as one dense block, in training: a forward that
+ * can keep its two projections, in bf16 or in 8 bits, and the gradients.
+ * --------------------------------------------------------------------------- */
+#define MOE_FFN_MAX_EXPERTS 2048
+
+typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 } moe_act;
+/* What the forward keeps of x w_gate^T and x w_up^T: nothing, bf16 rows, or e4m3
+ * rows with one float scale (largest magnitude / 448; 1 for a block of zeros) for
+ * each 128 columns, the library's format of quantised rows. */
+typedef enum { MOE_SAVE_NONE = 0, MOE_SAVE_BF16 = 1, MOE_SAVE_FP8 = 2 } moe_save;
+
+typedef struct {
+  int32_t rows;        /* rows of x: at least region_offsets' last entry; >= 0 */
+  int32_t hidden;      /* H, a multiple of 8 */
+  int32_t inter;       /* I, a multiple of 8; of 128 with MOE_SAVE_FP8 */
+  int32_t num_experts; /* E, 1 .. MOE_FFN_MAX_EXPERTS */
+  int32_t num_ranks;   /* R: region_offsets has E*R + 1 entries, expert e's rows begin at entry e*R; >= 1 */
+  int32_t act;         /* moe_act */
+  int32_t save;        /* moe_save */
+  int32_t num_sms;     /* SMs the CTAs are spread over; 0, or more than there are: all */
+} moe_ffn_desc;
+
+/* For every packed row p of expert e:
+ *   g = x_p w_gate[e]^T, u = x_p w_up[e]^T, h_p = bf16_rne( act(g) * u ), y_p = bf16_rne( h_p w_down[e]^T ),
+ * act(g) = g / (1 + exp(-g)), or g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2; products of bf16 values summed in
+ * fp32, act in fp32. With save, g and u are kept as it says (from their fp32 values).
+ *   region_offsets [E*R + 1] int32, or NULL with E = 1: all rows; x [rows][H], w_gate and w_up [E][I][H], w_down
+ *   [E][H][I] bf16 (read); h [rows][I] bf16 (written: scratch), y [rows][H] bf16 (written); gate, up [rows][I] bf16
+ *   or e4m3, gate_scales, up_scales [rows][I/128] float (written with save; NULL where not used). Rows at or above
+ *   the last offset are left as they were. All matrices 16-byte aligned.
+ * Reads nothing before the dependency wait of its first kernel.
+ * Host errors: MOE_EINVAL; MOE_ECUDA when no TMA tensor map can be made. Device errors: offsets that are no ranges
+ * of the rows -> MOE_EINVAL (the expert has no rows); a stalled pipeline -> MOE_ETIMEOUT. */
+moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_offsets, const void *x, const void *w_gate,
+                   const void *w_up, const void *w_down, void *h, void *y, void *gate, float *gate_scales, void *up,
+                   float *up_scales, int32_t *err, void *stream);
+
+/* Gradients of moe_ffn from what it kept (save is not MOE_SAVE_NONE; g, u: the values the bf16 rows or the codes and
+ * scales stand for):
+ *   dh = grad_y w_down, dg = bf16_rne( dh u act'(g) ), du = bf16_rne( dh act(g) ), h = bf16_rne( act(g) u ),
+ *   grad_x = bf16_rne( dg w_gate + du w_up ),
+ *   grad_w_gate = bf16_rne( dg^T x ), grad_w_up = bf16_rne( du^T x ), grad_w_down = bf16_rne( grad_y^T h )
+ * over each expert's rows, in fp32; the gradients of an expert without rows are 0. dh is not rounded.
+ *   h, grad_gate, grad_up [rows][I] bf16 (written: scratch, h may be the forward's); grad_x [rows][H] bf16 (written;
+ *   rows at or above the last offset are left as they were); grad_w_gate, grad_w_up [E][I][H], grad_w_down [E][H][I]
+ *   bf16 (written whole; all three NULL: not wanted). All matrices 16-byte aligned. grad_x may be grad_y when no
+ *   weights' gradients are wanted, and nothing else may overlap.
+ * Errors as moe_ffn. */
+moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *region_offsets, const void *x, const void *gate,
+                        const float *gate_scales, const void *up, const float *up_scales, const void *w_gate,
+                        const void *w_up, const void *w_down, const void *grad_y, void *h, void *grad_gate,
+                        void *grad_up, void *grad_x, void *grad_w_gate, void *grad_w_up, void *grad_w_down,
+                        int32_t *err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a block, with its gate and the residual stream.
+ * --------------------------------------------------------------------------- */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_ROW = 1, MOE_GATE_CHANNEL = 2 } moe_gate_kind;
+
+typedef struct {
+  int32_t rows;        /* T >= 0 */
+  int32_t dim;         /* H, a multiple of 8, at most 32768 */
+  int32_t stream_fp32; /* the stream (x, r and their gradients) is 0: bf16, 1: float */
+  int32_t gate;        /* moe_gate_kind: none, one value for each row [T], one for each channel [H] */
+  float eps;           /* >= 0 */
+  float alpha;         /* the residual scale */
+} moe_norm_desc;
+
+/* For every row, with rms(v) = sqrt( mean(v^2) + eps ):
+ *   b = o / rms(o) * w_post, or o with w_post NULL;
+ *   r = x + alpha * gate * b;  n = r / rms(r) * w_pre  (from r before it is rounded),
+ * all in fp32, r and n rounded once. With o NULL (no block before it; w_post and gate then too) r = x, and r may be
+ * NULL. r may be x.
+ *   x [T][H] stream type, o [T][H] bf16, w_post, w_pre [H] float, gate [T] or [H] float (read); r [T][H] stream
+ *   type, n [T][H] bf16 (written). Matrices and vectors of H 16-byte aligned.
+ * Host errors: MOE_EINVAL. No device errors. */
+moe_status moe_norm(const moe_norm_desc *desc, const void *x, const void *o, const float *w_post, const float *gate,
+                    const float *w_pre, void *r, void *n, int32_t *err, void *stream);
+
+/* Bytes of moe_norm_grad's workspace; MOE_EINVAL for a desc that it refuses. */
+int64_t moe_norm_workspace(const moe_norm_desc *desc);
+
+/* Gradients of moe_norm, from r as it was kept and the gradients of r (NULL: none) and n:
+ *   grad_x [T][H] stream type (also the gradient of r with what came through n), grad_o [T][H] bf16 (with o),
+ *   grad_w_post (with w_post), grad_w_pre [H] float, grad_gate [T] or [H] float (with a gate) (written whole);
+ *   workspace: moe_norm_workspace bytes, 16-byte aligned, free again after the call in stream order. grad_x may be
+ *   grad_r, and grad_o may be grad_n or o.
+ * Sums over rows have a fixed order. Host errors: MOE_EINVAL. No device errors. */
+moe_status moe_norm_grad(const moe_norm_desc *desc, const void *r, const void *o, const float *w_post,
+                         const float *gate, const float *w_pre, const void *grad_r, const void *grad_n, void *grad_x,
+                         void *grad_o, float *grad_w_post, float *grad_gate, float *grad_w_pre, void *workspace,
+                         int32_t *err, void *stream);
+
 /* Synchronise `stream`, read the device error word, clear it, and return its
  * value (MOE_OK if no kernel latched an error). Host-synchronising. */
 moe_status moe_get_error(int32_t *err, void *stream);
