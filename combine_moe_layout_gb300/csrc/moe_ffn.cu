@@ -35,6 +35,7 @@
 
 #include <cmath>
 
+#include "moe_ffn.cuh"
 #include "moe_tc.cuh"
 
 namespace moe {
@@ -151,20 +152,6 @@ __device__ __forceinline__ Job job_of(int w, const int32_t *pref, const int32_t 
       j.ncols = min(kBN, (a.n_total - t.n0 + 63) & ~63);
   }
   return j;
-}
-
-// act(g) and act'(g), in fp32.
-template <bool GRAD>
-__device__ __forceinline__ float act_of(float g, int act, float *da) {
-  if (act == MOE_ACT_SILU) {
-    const float p = 1.0f / (1.0f + expf(-g));
-    if constexpr (GRAD) *da = p * (1.0f + g * (1.0f - p));
-    return g * p;
-  }
-  constexpr float k = 0.7978845608028654f, c = 0.044715f;  // sqrt(2 / pi)
-  const float t = tanhf(k * (g + c * g * g * g));
-  if constexpr (GRAD) *da = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * k * (1.0f + 3.0f * c * g * g);
-  return 0.5f * g * (1.0f + t);
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -589,10 +576,6 @@ bool ffn_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct FfnSizes {
-  int rows, H, I, E, R, act, save, num_sms;
-};
-
 moe_status check_ffn(const moe_ffn_desc *d, FfnSizes *s) {
   if (d == nullptr) return MOE_EINVAL;
   if (d->rows < 0 || d->hidden < 8 || d->hidden % 8 != 0 || d->inter < 8 || d->inter % 8 != 0) return MOE_EINVAL;
@@ -688,6 +671,8 @@ extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_of
   if (s.save != MOE_SAVE_NONE && (!good16(gate) || !good16(up))) return MOE_EINVAL;
   if (s.save == MOE_SAVE_FP8 && (!good4(gate_scales) || !good4(up_scales))) return MOE_EINVAL;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (s.rows <= kFewRows && s.save != MOE_SAVE_FP8 && s.num_sms == 0)
+    return launch_ffn_few(s, region_offsets, x, w_gate, w_up, w_down, h, y, gate, up, err, cs);
   FfnMaps m{};
   if (!ffn_map(&m.m[0], x, s.H, s.rows, 0, 128) || !ffn_map(&m.m[1], w_gate, s.H, s.I, s.E, 128) ||
       !ffn_map(&m.m[2], w_up, s.H, s.I, s.E, 128))

@@ -35,6 +35,7 @@ struct NormArgs {
   void *grad_x, *grad_o;
   float *grad_gate;
   float *parts;           // [2][parts][H]: sums of dn r q and of alpha dr o p
+  int32_t *err;
   int rows, H, row_gate, channel_gate, stages;
   float eps, alpha;
 };
@@ -99,22 +100,126 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float *part, int &turn
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-template <int NV, bool F32>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
-  __shared__ float part[2][32];
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+        "l"(reinterpret_cast<uint64_t &>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void *base, int64_t at, float2 (&v)[4]) {
+  float f[8];
+  load8<F32>(base, at, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void *base, int64_t at, const float2 (&v)[4]) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  store8<F32>(base, at, f);
+}
+
+// The rows that a CTA takes, t = blockIdx.x, + gridDim.x, ...: up to four row-long arrays each, brought to shared
+// memory a few rows ahead by bulk copies of thread 0.
+struct RowRing {
+  uint64_t *full;       // one barrier for each stage
+  uint8_t *data;
+  const void *from[4];  // null: not there
+  uint32_t bytes[4];    // of a row; 0 where not there
+  uint32_t stage_bytes;
+  int stages;
+
+  __device__ __forceinline__ void issue(int s, int64_t t) const {
+    mbar_arrive_expect_tx(full + s, stage_bytes);
+    uint32_t at = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (bytes[i] != 0) {
+        bulk_load(data + static_cast<size_t>(s) * stage_bytes + at, static_cast<const uint8_t *>(from[i]) + t * bytes[i],
+                  bytes[i], full + s);
+        at += bytes[i];
+      }
+  }
+};
+
+__device__ __forceinline__ RowRing make_ring(const NormArgs &a, uint8_t *smem, int stages, const void *p0, bool f0,
+                                             const void *p1, bool f1, const void *p2, bool f2, const void *p3,
+                                             bool f3) {
+  RowRing r;
+  r.full = reinterpret_cast<uint64_t *>(smem);
+  r.data = smem + 64;
+  const void *p[4] = {p0, p1, p2, p3};
+  const bool f[4] = {f0, f1, f2, f3};
+  r.stage_bytes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.from[i] = p[i];
+    r.bytes[i] = p[i] == nullptr ? 0u : static_cast<uint32_t>(a.H) * (f[i] ? 4u : 2u);
+    r.stage_bytes += r.bytes[i];
+  }
+  r.stages = stages;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(r.full + s, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   grid_dependency_wait();
-  int turn = 0;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < stages; ++s) {
+      const int64_t t = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (t < a.rows) r.issue(s, t);
+    }
+  return r;
+}
+
+// RING: the rows come through shared memory; else (rows too long for it) straight from memory.
+template <int NV, bool F32, bool RING, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+  __shared__ float part[2][32];
+  extern __shared__ __align__(128) uint8_t smem[];
+  RowRing ring;
+  if constexpr (RING)
+    ring = make_ring(a, smem, a.stages, a.x, F32, a.o, false, nullptr, false, nullptr, false);
+  else
+    grid_dependency_wait();
+  int turn = 0, stage = 0;
+  uint32_t phase = 0;
   const int vecs = a.H / 8;
   const float inv = 1.0f / static_cast<float>(a.H);
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    const void *px, *po;
+    if constexpr (RING) {
+      if (!mbar_wait_bounded(ring.full + stage, phase)) {
+        latch_error(a.err, MOE_ETIMEOUT);
+        return;
+      }
+      const uint8_t *d = ring.data + static_cast<size_t>(stage) * ring.stage_bytes;
+      px = d;
+      po = d + ring.bytes[0];
+    } else {
+      px = static_cast<const uint8_t *>(a.x) + t * a.H * (F32 ? 4 : 2);
+      po = static_cast<const uint8_t *>(a.o) + t * a.H * 2;
+    }
     float x[NV][8], b[NV][8], sum[1];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < vecs) {
-        load8<F32>(a.x, t * a.H + v * 8, x[i]);
-        if (a.o != nullptr) load8<false>(a.o, t * a.H + v * 8, b[i]);
+        load8<F32>(px, v * 8, x[i]);
+        if (a.o != nullptr) load8<false>(po, v * 8, b[i]);
       }
     }
     if (a.o != nullptr) {
@@ -162,6 +267,12 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
     }
     sum[0] = ss;
     block_sums<1>(sum, &part[0][0], turn);
+    if constexpr (RING) {
+      // every thread has read its part of the stage
+      const int64_t next = t + static_cast<int64_t>(ring.stages) * gridDim.x;
+      if (threadIdx.x == 0 && next < a.rows) ring.issue(stage, next);
+      if (++stage == ring.stages) stage = 0, phase ^= 1u;
+    }
     const float q = 1.0f / sqrtf(sum[0] * inv + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -177,104 +288,145 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
   }
 }
 
-template <int NV, bool F32>
-__global__ void __launch_bounds__(1024) norm_grad_kernel(NormArgs a) {
+template <int NV, bool F32, bool RING, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormArgs a) {
   __shared__ float part[2][6][32];
-  grid_dependency_wait();
-  int turn = 0;
+  extern __shared__ __align__(128) uint8_t smem[];
+  RowRing ring;
+  if constexpr (RING)
+    ring = make_ring(a, smem, a.stages, a.x, F32, a.grad_n, false, a.grad_r, F32, a.o, false);
+  else
+    grid_dependency_wait();
+  int turn = 0, stage = 0;
+  uint32_t phase = 0;
   const int vecs = a.H / 8;
   const float inv = 1.0f / static_cast<float>(a.H);
-  float acc_n[NV][8], acc_o[NV][8];
+  // the thread's columns: w_pre, c = w_post gate (of channels), and the sums over rows
+  float2 w[NV][4], c[NV][4], acc_n[NV][4], acc_o[NV][4];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc_n[i][k] = acc_o[i][k] = 0.0f;
+    for (int k = 0; k < 4; ++k) {
+      acc_n[i][k] = acc_o[i][k] = w[i][k] = both(0.0f);
+      c[i][k] = both(1.0f);
+    }
+    if (v < vecs) {
+      load8<true>(a.w_pre, v * 8, w[i]);
+      if (a.w_post != nullptr) load8<true>(a.w_post, v * 8, c[i]);
+      if (a.channel_gate) {
+        float2 g[4];
+        load8<true>(a.gate, v * 8, g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[i][k] = mul2(c[i][k], g[k]);
+      }
+    }
+  }
+  int64_t waiting = -1;  // the row to be asked for into the stage that the last row has left
+  int left = 0;
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    float r[NV][8], o[NV][8], dn[NV][8], dr[NV][8];  // dn: then dn w_pre
-    float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // r^2, dn w r, o^2, and c o with grad_r, dn w, r
+    const void *pr, *pn, *pd, *po;
+    if constexpr (RING) {
+      if (!mbar_wait_bounded(ring.full + stage, phase)) {
+        latch_error(a.err, MOE_ETIMEOUT);
+        return;
+      }
+      const uint8_t *d = ring.data + static_cast<size_t>(stage) * ring.stage_bytes;
+      pr = d;
+      pn = d + ring.bytes[0];
+      pd = d + ring.bytes[0] + ring.bytes[1];
+      po = d + ring.bytes[0] + ring.bytes[1] + ring.bytes[2];
+    } else {
+      pr = static_cast<const uint8_t *>(a.x) + t * a.H * (F32 ? 4 : 2);
+      pn = static_cast<const uint8_t *>(a.grad_n) + t * a.H * 2;
+      pd = static_cast<const uint8_t *>(a.grad_r) + t * a.H * (F32 ? 4 : 2);
+      po = static_cast<const uint8_t *>(a.o) + t * a.H * 2;
+    }
+    float2 s2[6];  // r^2, dn w r, o^2, and c o with grad_r, dn w, r
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s2[i] = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < vecs) {
-        const int64_t at = t * a.H + v * 8;
-        load8<F32>(a.x, at, r[i]);
-        load8<false>(a.grad_n, at, dn[i]);
-        if (a.grad_r != nullptr)
-          load8<F32>(a.grad_r, at, dr[i]);
-        else
+        float2 r[4], dn[4];
+        load8<F32>(pr, v * 8, r);
+        load8<false>(pn, v * 8, dn);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dr[i][k] = 0.0f;
-        if (a.o != nullptr)
-          load8<false>(a.o, at, o[i]);
-        else
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o[i][k] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < vecs) {
-        float w[8], c[8];
-        vector8(a.w_pre, v * 8, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = 1.0f;
-        if (a.w_post != nullptr) vector8(a.w_post, v * 8, c);
-        if (a.channel_gate) {
-          float g[8];
-          vector8(a.gate, v * 8, g);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) c[k] *= g[k];
+        for (int k = 0; k < 4; ++k) {
+          dn[k] = mul2(dn[k], w[i][k]);
+          s2[0] = fma2(r[k], r[k], s2[0]);
+          s2[1] = fma2(dn[k], r[k], s2[1]);
         }
+        if (a.o != nullptr) {
+          float2 o[4], dr[4];
+          load8<false>(po, v * 8, o);
+          if (a.grad_r != nullptr) load8<F32>(pd, v * 8, dr);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float d = dn[i][k] * w[k], co = c[k] * o[i][k];
-          s[0] += r[i][k] * r[i][k];
-          s[1] += d * r[i][k];
-          s[2] += o[i][k] * o[i][k];
-          s[3] += co * dr[i][k];
-          s[4] += co * d;
-          s[5] += co * r[i][k];
+          for (int k = 0; k < 4; ++k) {
+            const float2 co = mul2(c[i][k], o[k]);
+            s2[2] = fma2(o[k], o[k], s2[2]);
+            if (a.grad_r != nullptr) s2[3] = fma2(co, dr[k], s2[3]);
+            s2[4] = fma2(co, dn[k], s2[4]);
+            s2[5] = fma2(co, r[k], s2[5]);
+          }
         }
       }
     }
+    float s[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = s2[i].x + s2[i].y;
     block_sums<6>(s, &part[0][0][0], turn);
+    if constexpr (RING) {
+      // every thread has left the last row's stage
+      if (threadIdx.x == 0 && waiting >= 0) ring.issue(left, waiting);
+      const int64_t next = t + static_cast<int64_t>(ring.stages) * gridDim.x;
+      waiting = next < a.rows ? next : -1;
+      left = stage;
+      if (++stage == ring.stages) stage = 0, phase ^= 1u;
+    }
     const float q = 1.0f / sqrtf(s[0] * inv + a.eps);
     const float m = q * q * s[1] * inv;  // dr = grad_r + q (dn w - m r)
     const float p = a.w_post != nullptr ? 1.0f / sqrtf(s[2] * inv + a.eps) : 1.0f;
-    const float db = a.alpha * p * (s[3] + q * (s[4] - m * s[5]));  // alpha sum dr c o p
+    const float dro = s[3] + q * (s[4] - m * s[5]);  // sum dr c o
     float scale = a.alpha * p;
     if (a.row_gate) {
+      if (threadIdx.x == 0) a.grad_gate[t] = scale * dro;
       scale *= a.gate[t];
-      if (threadIdx.x == 0) a.grad_gate[t] = db;
     }
-    // grad_o = scale (c dr - o f), f = p sum(alpha dr c o p) / (alpha H) = p^2 sum(dr c o) / H
-    const float f = a.w_post != nullptr ? p * p * (s[3] + q * (s[4] - m * s[5])) * inv : 0.0f;
+    // grad_o = scale (c dr - f o), f = p^2 mean(dr c o)
+    const float f = a.w_post != nullptr ? p * p * dro * inv : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < vecs) {
         const int64_t at = t * a.H + v * 8;
-        float w[8], c[8];
-        vector8(a.w_pre, v * 8, w);
+        float2 r[4], dn[4], dr[4];
+        load8<F32>(pr, v * 8, r);
+        load8<false>(pn, v * 8, dn);
+        if (a.grad_r != nullptr)
+          load8<F32>(pd, v * 8, dr);
+        else
 #pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = 1.0f;
-        if (a.w_post != nullptr) vector8(a.w_post, v * 8, c);
-        if (a.channel_gate) {
-          float g[8];
-          vector8(a.gate, v * 8, g);
+          for (int k = 0; k < 4; ++k) dr[k] = both(0.0f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) c[k] *= g[k];
+        for (int k = 0; k < 4; ++k) {
+          acc_n[i][k] = fma2(dn[k], mul2(r[k], both(q)), acc_n[i][k]);
+          const float2 d = mul2(dn[k], w[i][k]);
+          dr[k] = fma2(both(q), fma2(both(-m), r[k], d), dr[k]);
         }
+        if (a.o != nullptr) {
+          float2 o[4];
+          load8<false>(po, v * 8, o);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          acc_n[i][k] += dn[i][k] * (r[i][k] * q);
-          dr[i][k] += q * (dn[i][k] * w[k] - m * r[i][k]);
-          acc_o[i][k] += scale * dr[i][k] * o[i][k];
-          o[i][k] = scale * (c[k] * dr[i][k] - f * o[i][k]);
+          for (int k = 0; k < 4; ++k) {
+            const float2 sd = mul2(both(scale), dr[k]);
+            acc_o[i][k] = fma2(sd, o[k], acc_o[i][k]);
+            o[k] = fma2(c[i][k], sd, mul2(both(-scale * f), o[k]));
+          }
+          store8<false>(a.grad_o, at, o);
         }
-        store8<F32>(a.grad_x, at, dr[i]);
-        if (a.o != nullptr) store8<false>(a.grad_o, at, o[i]);
+        store8<F32>(a.grad_x, at, dr);
       }
     }
   }
@@ -327,32 +479,69 @@ moe_status check_norm(const moe_norm_desc *d) {
 
 bool good16(const void *p) { return p != nullptr && aligned16(p); }
 
-// Rows of a gradient's CTA parts: at most 304 (two CTAs on each of 152 SMs), the same on every device, so that the
-// sums are too.
-int norm_parts(const moe_norm_desc *d) { return d->rows < 304 ? d->rows : 304; }
+// CTAs of a gradient, each with its part of the sums over rows: by the sizes alone, so that the sums are the same on
+// every device. One on each of 152 SMs where two rows fill much of the shared memory, else two.
+int norm_parts(const moe_norm_desc *d) {
+  const int most = d->dim > 4096 ? 152 : 304;
+  return d->rows < most ? d->rows : most;
+}
+
+constexpr int kRingBytes = 200 * 1024;  // for the rows of all CTAs on an SM
+constexpr int kRingStages = 4;
 
 struct NormShape {
-  int nv, threads;
+  int nv, threads, stages, ctas;  // stages: 0: no ring; ctas: on an SM
+  int smem;
 };
 
-NormShape norm_shape(int H) {
+// row_bytes: what a row brings to shared memory.
+NormShape norm_shape(int H, int64_t row_bytes, int ctas) {
+  NormShape s{};
   const int vecs = H / 8;
-  int nv = 1;
-  while (nv < 4 && (vecs + nv - 1) / nv > kNormThreads) nv *= 2;
-  const int t = (vecs + nv - 1) / nv;
-  return NormShape{nv, (t + 31) & ~31};
+  s.nv = 1;
+  while (s.nv < 4 && (vecs + s.nv - 1) / s.nv > kNormThreads) s.nv *= 2;
+  s.threads = ((vecs + s.nv - 1) / s.nv + 31) & ~31;
+  while (ctas > 1 && 2 * row_bytes > kRingBytes / ctas) --ctas;
+  s.ctas = ctas;
+  const int64_t n = kRingBytes / ctas / row_bytes;
+  s.stages = static_cast<int>(n > kRingStages ? kRingStages : n);
+  if (s.stages < 2 || s.threads > kNormThreads) s.stages = 0;
+  s.smem = s.stages > 0 ? 64 + static_cast<int>(s.stages * row_bytes) : 0;
+  return s;
 }
 
 template <class K>
-moe_status launch_norm(K kernel, int grid, int threads, const NormArgs &a, cudaStream_t stream) {
+moe_status launch_norm(K kernel, int grid, const NormShape &s, NormArgs a, cudaStream_t stream) {
+  a.stages = s.stages;
+  // (the limit that every kernel has counts its static shared memory too, so the ring asks for more than that)
+  constexpr int least = 64 * 1024;
+  if (s.smem > 0 && !raise_smem_limit(kernel, s.smem > least ? s.smem : least)) return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(s.threads), 1, 1);
+  cfg.dynamicSmemBytes = s.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   use_pdl(cfg, attr);
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return MOE_ECUDA;
   return launch_status();
+}
+
+template <bool GRAD, bool F32>
+moe_status launch_norm_typed(int grid, const NormShape &s, const NormArgs &a, cudaStream_t stream) {
+#define MOE_NORM(NV, RING, THREADS)                                                        \
+  (GRAD ? launch_norm(norm_grad_kernel<NV, F32, RING, THREADS>, grid, s, a, stream)         \
+        : launch_norm(norm_kernel<NV, F32, RING, THREADS>, grid, s, a, stream))
+  if (s.stages == 0) return s.threads > kNormThreads ? MOE_NORM(4, false, 1024) : MOE_NORM(4, false, kNormThreads);
+  if (s.nv == 1) return MOE_NORM(1, true, kNormThreads);
+  if (s.nv == 2) return MOE_NORM(2, true, kNormThreads);
+  return MOE_NORM(4, true, kNormThreads);
+#undef MOE_NORM
+}
+
+template <bool GRAD>
+moe_status launch_norm_any(bool fp32, int grid, const NormShape &s, const NormArgs &a, cudaStream_t stream) {
+  return fp32 ? launch_norm_typed<GRAD, true>(grid, s, a, stream) : launch_norm_typed<GRAD, false>(grid, s, a, stream);
 }
 
 }  // namespace
@@ -385,18 +574,11 @@ extern "C" moe_status moe_norm(const moe_norm_desc *desc, const void *x, const v
   a.channel_gate = desc->gate == MOE_GATE_CHANNEL;
   a.eps = desc->eps;
   a.alpha = desc->alpha;
-  const NormShape s = norm_shape(a.H);
-  const int room = sm_count() * (2048 / s.threads < 32 ? 2048 / s.threads : 32);
-  const int grid = a.rows < room ? a.rows : room;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (desc->stream_fp32) {
-    if (s.nv == 1) return launch_norm(norm_kernel<1, true>, grid, s.threads, a, cs);
-    if (s.nv == 2) return launch_norm(norm_kernel<2, true>, grid, s.threads, a, cs);
-    return launch_norm(norm_kernel<4, true>, grid, s.threads, a, cs);
-  }
-  if (s.nv == 1) return launch_norm(norm_kernel<1, false>, grid, s.threads, a, cs);
-  if (s.nv == 2) return launch_norm(norm_kernel<2, false>, grid, s.threads, a, cs);
-  return launch_norm(norm_kernel<4, false>, grid, s.threads, a, cs);
+  a.err = err;
+  const NormShape s = norm_shape(a.H, static_cast<int64_t>(a.H) * ((desc->stream_fp32 ? 4 : 2) + (o != nullptr ? 2 : 0)), 2);
+  const int room = sm_count() * s.ctas;
+  return launch_norm_any<false>(desc->stream_fp32 != 0, a.rows < room ? a.rows : room, s, a,
+                                static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int64_t moe_norm_workspace(const moe_norm_desc *desc) {
@@ -447,17 +629,12 @@ extern "C" moe_status moe_norm_grad(const moe_norm_desc *desc, const void *r, co
   a.channel_gate = desc->gate == MOE_GATE_CHANNEL;
   a.eps = desc->eps;
   a.alpha = desc->alpha;
-  const NormShape s = norm_shape(a.H);
+  a.err = err;
+  const int64_t of_stream = desc->stream_fp32 ? 4 : 2;
+  const int64_t row_bytes = a.H * (of_stream * (grad_r != nullptr ? 2 : 1) + (o != nullptr ? 4 : 2));
   const int grid = norm_parts(desc);
-  moe_status st;
-  if (desc->stream_fp32)
-    st = s.nv == 1   ? launch_norm(norm_grad_kernel<1, true>, grid, s.threads, a, cs)
-         : s.nv == 2 ? launch_norm(norm_grad_kernel<2, true>, grid, s.threads, a, cs)
-                     : launch_norm(norm_grad_kernel<4, true>, grid, s.threads, a, cs);
-  else
-    st = s.nv == 1   ? launch_norm(norm_grad_kernel<1, false>, grid, s.threads, a, cs)
-         : s.nv == 2 ? launch_norm(norm_grad_kernel<2, false>, grid, s.threads, a, cs)
-                     : launch_norm(norm_grad_kernel<4, false>, grid, s.threads, a, cs);
+  const NormShape s = norm_shape(a.H, row_bytes, grid > 152 ? 2 : 1);
+  const moe_status st = launch_norm_any<true>(desc->stream_fp32 != 0, grid, s, a, cs);
   if (st != MOE_OK) return st;
   NormSumArgs b{a.parts, w_post, gate, grad_w_pre, w_post != nullptr ? grad_w_post : nullptr,
                 a.channel_gate ? grad_gate : nullptr, grid, a.H};

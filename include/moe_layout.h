@@ -605,7 +605,7 @@ typedef struct {
  * NULL. r may be x.
  *   x [T][H] stream type, o [T][H] bf16, w_post, w_pre [H] float, gate [T] or [H] float (read); r [T][H] stream
  *   type, n [T][H] bf16 (written). Matrices and vectors of H 16-byte aligned.
- * Host errors: MOE_EINVAL. No device errors. */
+ * Host errors: MOE_EINVAL. Device errors: a stalled copy -> MOE_ETIMEOUT. */
 moe_status moe_norm(const moe_norm_desc *desc, const void *x, const void *o, const float *w_post, const float *gate,
                     const float *w_pre, void *r, void *n, int32_t *err, void *stream);
 
@@ -617,7 +617,7 @@ int64_t moe_norm_workspace(const moe_norm_desc *desc);
  *   grad_w_post (with w_post), grad_w_pre [H] float, grad_gate [T] or [H] float (with a gate) (written whole);
  *   workspace: moe_norm_workspace bytes, 16-byte aligned, free again after the call in stream order. grad_x may be
  *   grad_r, and grad_o may be grad_n or o.
- * Sums over rows have a fixed order. Host errors: MOE_EINVAL. No device errors. */
+ * Sums over rows have a fixed order. Errors as moe_norm. */
 moe_status moe_norm_grad(const moe_norm_desc *desc, const void *r, const void *o, const float *w_post,
                          const float *gate, const float *w_pre, const void *grad_r, const void *grad_n, void *grad_x,
                          void *grad_o, float *grad_w_post, float *grad_gate, float *grad_w_pre, void *workspace,

@@ -178,7 +178,7 @@ def check_codes(codes, scales, want, err):
 
 SHAPES = [  # counts, H, I
     ([1], 256, 128), ([1], 8, 8), ([5], 72, 136), ([64], 128, 128), ([65], 264, 72), ([129], 64, 264),
-    ([200], 1000, 712), ([0, 3, 0, 130, 1, 64, 0], 328, 200), ([63, 64, 65, 127, 128, 129], 256, 384),
+    ([16], 264, 200), ([17], 264, 200), ([0, 9, 0, 3, 1], 1000, 712), ([200], 1000, 712), ([0, 3, 0, 130, 1, 64, 0], 328, 200), ([63, 64, 65, 127, 128, 129], 256, 384),
     ([700, 5], 512, 640), ([0, 0], 128, 128),
 ]
 
