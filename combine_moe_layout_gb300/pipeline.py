@@ -6,8 +6,10 @@ synthetic ones of the workloads: identity for bf16 steps (combine reads the
 receive buffer itself) and ``moe_expert_stub`` for fp8 steps.
 
 ``LocalMoe`` is an MoE layer of one device that is no part of an EP group: router,
-token sort, expert stage and the way back, the gradients of all but the experts,
-and a projection shared by all requests with each request's low-rank adapter.
+token sort, expert stage and the way back with their gradients, from what the
+forward keeps in bf16 or in 8 bits; and what stands beside them: a projection shared
+by all requests with each request's low-rank adapter, a dense feed-forward block (a
+shared expert), and the norms before and after a block with its gate and residual.
 """
 from __future__ import annotations
 
@@ -161,13 +163,50 @@ def _expect(name: str, t, dtype, *shape):
         raise ValueError(f"LocalMoe: {name} is {what}, not {dtype} ({sizes})")
 
 
+SAVE = {None: B.MOE_SAVE_NONE, "bf16": B.MOE_SAVE_BF16, "fp8": B.MOE_SAVE_FP8}
+
+
+@dataclass
+class KeptFfn:
+    """What a feed-forward block's forward keeps of its two projections for its gradients: bf16 rows, or e4m3 rows
+    (uint8 codes) with a float scale for each 128 columns."""
+    desc: B.MoeFfnDesc
+    gate: torch.Tensor
+    up: torch.Tensor
+    gate_scales: torch.Tensor | None
+    up_scales: torch.Tensor | None
+
+
+@dataclass
+class NormGrads:
+    """Gradients of LocalMoe.norm; None for what it did not have."""
+    x: torch.Tensor
+    o: torch.Tensor | None
+    w_pre: torch.Tensor
+    w_post: torch.Tensor | None
+    gate: torch.Tensor | None
+
+
+def _keep(desc: B.MoeFfnDesc, device) -> KeptFfn:
+    n, I, fp8 = desc.rows, desc.inter, desc.save == B.MOE_SAVE_FP8
+
+    def rows():
+        return torch.empty((n, I), dtype=torch.uint8 if fp8 else torch.bfloat16, device=device)
+
+    def scales():
+        return torch.empty((n, I // 128), dtype=torch.float32, device=device) if fp8 else None
+
+    return KeptFfn(desc, rows(), rows(), scales(), scales())
+
+
 class LocalMoe:
     """An MoE layer of one device.
 
     forward: logits -> moe_gate -> moe_sort -> expert stage -> moe_unsort. backward takes the gradient of the
-    output back through moe_unsort_grad, the caller's expert gradient, moe_sort_grad and moe_gate_grad. shared runs
-    the projection beside the experts with the adapters of the batch's requests. The buffers of forward and backward
-    are allocated once.
+    output back through moe_unsort_grad, the experts' gradient (moe_ffn_grad, from what a forward with ``save`` kept, or
+    the caller's own), moe_sort_grad and moe_gate_grad. shared runs the projection beside the experts with the adapters
+    of the batch's requests, dense a feed-forward block of all tokens, norm the norms around a block; their results are
+    new tensors. The buffers of forward and backward are allocated once.
 
     Each method runs on ``stream`` (None: the current one) whole, what it does with torch and expert_grad included.
     The layer may have been made on another stream: the first call on a stream waits for that one's work up to then.
@@ -194,6 +233,10 @@ class LocalMoe:
         self.h = rows(n, inter) if inter else None
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.grad_y = self.grad_x = self.grad_weights = self.grad_logits = None  # allocated by the first backward
+        self.kept = None  # what the last forward with ``save`` kept, for backward
+        self._kept_now = False  # the last forward was one
+        self.grad_gate = self.grad_up = self.grad_packed_x = None
+        self.grad_w_gate = self.grad_w_up = self.grad_w_down = None  # by the first backward with the experts' weights
         self.u = None  # the last shared's scratch, its first part
         self.device = self.err.device
         self._streams = {}  # the streams that have used the buffers, by their handles
@@ -221,7 +264,8 @@ class LocalMoe:
 
     def _keep_for(self, streams):
         """The layer's buffers are given out again, after the layer, only when these streams have passed them."""
-        for t in vars(self).values():
+        kept = vars(self.kept).values() if self.kept is not None else ()
+        for t in (*vars(self).values(), *kept):
             if isinstance(t, torch.Tensor):
                 for s in streams:
                     t.record_stream(s)
@@ -243,15 +287,32 @@ class LocalMoe:
             B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed,
                        self.err)
 
-    def experts(self, weights, stream=None):
-        """The expert stage on the sorted rows (weights: workloads.ExpertWeights)."""
+    def _expect_weights(self, weights):
         E, H, I = self.desc.num_experts, self.desc.hidden, self.inter
         if not I:
             raise ValueError("LocalMoe: a layer made with inter = 0 has no expert stage")
         _expect("w_gate", weights.w_gate, torch.bfloat16, E, I, H)
         _expect("w_up", weights.w_up, torch.bfloat16, E, I, H)
         _expect("w_down", weights.w_down, torch.bfloat16, E, H, I)
+
+    def experts(self, weights, stream=None, save=None):
+        """The expert stage on the sorted rows (weights: workloads.ExpertWeights). save: "bf16" or "fp8" keeps what
+        backward needs of it (kept)."""
+        self._expect_weights(weights)
+        if save not in SAVE:
+            raise ValueError(f"LocalMoe: save is {save!r}, not None, 'bf16' or 'fp8'")
         with self._on(stream):
+            self._kept_now = save is not None
+            if save is not None:
+                if self.kept is None or self.kept.desc.save != SAVE[save]:
+                    n, H = self.packed_x.shape
+                    desc = B.MoeFfnDesc(n, H, self.inter, self.desc.num_experts, 1, B.MOE_ACT_SILU, SAVE[save], 0)
+                    self.kept = _keep(desc, self.device)
+                    self._keep_for(self._streams.values())
+                k = self.kept
+                B.moe_ffn(k.desc, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up, weights.w_down,
+                          self.h, self.packed_y, k.gate, k.gate_scales, k.up, k.up_scales, self.err)
+                return
             B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate,
                                  weights.w_up, self.h, self.err)
             B.moe_expert_down(self.desc, self.inter, self.region_offsets, self.h, weights.w_down, self.packed_y,
@@ -262,32 +323,52 @@ class LocalMoe:
             B.moe_unsort(self.desc, self.packed_y, self.tok_packed, self.topk_weights, self.out, self.err)
         return self.out
 
-    def forward(self, x, logits, weights, bias=None, stream=None):
+    def forward(self, x, logits, weights, bias=None, stream=None, save=None):
         """x [tokens][hidden], logits [tokens][num_experts] -> the routed experts' output [tokens][hidden], a buffer of
-        the layer that the next forward writes again."""
+        the layer that the next forward writes again. save as in experts."""
         self.route(logits, bias, stream)
         self.sort(x, stream)
-        self.experts(weights, stream)
+        self.experts(weights, stream, save)
         return self.unsort(stream)
 
     def backward(self, grad_out, logits, expert_grad, stream=None):
         """The gradients of x and of the logits, in buffers of the layer that the next backward writes again.
-        expert_grad(packed_x, region_offsets, grad_y) is the caller's gradient of the experts: from the gradient of
-        packed_y to that of packed_x, row by row, both bf16 [tokens * topk][hidden]. It is called with ``stream`` as
-        the current one. Rows at or above region_offsets' last entry belong to no choice: packed_x and grad_y hold
-        nothing of this batch there."""
+        expert_grad: the experts' weights, after a forward with ``save``, which leaves the weights' gradients in
+        grad_w_gate, grad_w_up and grad_w_down, buffers of the layer too. Or a function of the caller's,
+        expert_grad(packed_x, region_offsets, grad_y): from the gradient of packed_y to that of packed_x, row by row,
+        both bf16 [tokens * topk][hidden]. It is called with ``stream`` as the current one. Rows at or above
+        region_offsets' last entry belong to no choice: packed_x and grad_y hold nothing of this batch there."""
         _expect("grad_out", grad_out, torch.bfloat16, *self.out.shape)
         self._expect_logits(logits)
+        own = hasattr(expert_grad, "w_gate")
+        if own:
+            self._expect_weights(expert_grad)
+            if not self._kept_now:
+                raise ValueError("LocalMoe: backward with the experts' weights follows a forward with save")
         with self._on(stream):
             if self.grad_y is None:
                 self.grad_y, self.grad_x = torch.zeros_like(self.packed_y), torch.empty_like(self.out)
                 self.grad_weights = torch.empty_like(self.topk_weights)
                 self.grad_logits = torch.empty_like(logits)
                 self._keep_for(self._streams.values())
+            if own and self.grad_packed_x is None:
+                self.grad_packed_x = torch.empty_like(self.packed_x)
+                self.grad_gate, self.grad_up = torch.empty_like(self.h), torch.empty_like(self.h)
+                self.grad_w_gate, self.grad_w_up, self.grad_w_down = (
+                    torch.empty(t.shape, dtype=t.dtype, device=self.device)
+                    for t in (expert_grad.w_gate, expert_grad.w_up, expert_grad.w_down))
+                self._keep_for(self._streams.values())
             B.moe_unsort_grad(self.desc, self.packed_y, self.tok_packed, self.topk_weights, grad_out, self.grad_y,
                               self.grad_weights, self.err)
-            grad_packed = expert_grad(self.packed_x, self.region_offsets, self.grad_y)
-            _expect("expert_grad's result", grad_packed, torch.bfloat16, *self.packed_x.shape)
+            if own:
+                k, w = self.kept, expert_grad
+                B.moe_ffn_grad(k.desc, self.region_offsets, self.packed_x, k.gate, k.gate_scales, k.up, k.up_scales,
+                               w.w_gate, w.w_up, w.w_down, self.grad_y, self.h, self.grad_gate, self.grad_up,
+                               self.grad_packed_x, self.grad_w_gate, self.grad_w_up, self.grad_w_down, self.err)
+                grad_packed = self.grad_packed_x
+            else:
+                grad_packed = expert_grad(self.packed_x, self.region_offsets, self.grad_y)
+                _expect("expert_grad's result", grad_packed, torch.bfloat16, *self.packed_x.shape)
             B.moe_sort_grad(self.desc, grad_packed, self.tok_packed, self.grad_x, self.err)
             B.moe_gate_grad(self.desc, self.opts, logits, self.topk_idx, self.grad_weights, self.grad_logits, self.err)
         return self.grad_x, self.grad_logits
@@ -323,6 +404,87 @@ class LocalMoe:
             B.moe_lora_linear(B.MoeLoraDesc(T, K, N, rank, A, 0, u_parts), x, w, lora_a, lora_b, scales, adapter, u, out,
                               self.err)
         return out
+
+    def dense(self, x, w_gate, w_up, w_down, act=B.MOE_ACT_SILU, save=None, stream=None):
+        """A feed-forward block of all tokens, act(x w_gate^T) * (x w_up^T) w_down^T (a shared expert): x [rows][in],
+        w_gate and w_up [inter][in], w_down [in][inter] bf16. The result y [rows][in], a new tensor, and what dense_grad
+        needs of it: None without save ("bf16" or "fp8")."""
+        bf16 = torch.bfloat16
+        if save not in SAVE:
+            raise ValueError(f"LocalMoe: save is {save!r}, not None, 'bf16' or 'fp8'")
+        _expect("x", x, bf16, None, None)
+        _expect("w_gate", w_gate, bf16, None, x.shape[1])
+        I = w_gate.shape[0]
+        _expect("w_up", w_up, bf16, I, x.shape[1])
+        _expect("w_down", w_down, bf16, x.shape[1], I)
+        desc = B.MoeFfnDesc(*x.shape, I, 1, 1, act, SAVE[save], 0)
+        with self._on(stream):
+            h, y = torch.empty((x.shape[0], I), dtype=bf16, device=x.device), torch.empty_like(x)
+            k = _keep(desc, x.device) if save is not None else None
+            B.moe_ffn(desc, None, x, w_gate, w_up, w_down, h, y, *((k.gate, k.gate_scales, k.up, k.up_scales) if k else
+                                                                   (None,) * 4), self.err)
+        return y, k
+
+    def dense_grad(self, kept: KeptFfn, x, w_gate, w_up, w_down, grad_y, stream=None):
+        """Gradients of dense with respect to x, w_gate, w_up and w_down (new tensors), from what it kept."""
+        n, H, I = kept.desc.rows, kept.desc.hidden, kept.desc.inter
+        bf16 = torch.bfloat16
+        for name, t, shape in (("x", x, (n, H)), ("w_gate", w_gate, (I, H)), ("w_up", w_up, (I, H)),
+                               ("w_down", w_down, (H, I)), ("grad_y", grad_y, (n, H))):
+            _expect(name, t, bf16, *shape)
+        with self._on(stream):
+            scratch = [torch.empty((n, I), dtype=bf16, device=x.device) for _ in range(3)]
+            grads = [torch.empty_like(t) for t in (x, w_gate, w_up, w_down)]
+            B.moe_ffn_grad(kept.desc, None, x, kept.gate, kept.gate_scales, kept.up, kept.up_scales, w_gate, w_up, w_down,
+                           grad_y, *scratch, *grads, self.err)
+        return tuple(grads)
+
+    @staticmethod
+    def _norm_desc(x, w_pre, o, w_post, gate, by, eps, alpha):
+        _expect("x", x, x.dtype if isinstance(x, torch.Tensor) and x.dtype == torch.float32 else torch.bfloat16, None, None)
+        T, H = x.shape
+        _expect("w_pre", w_pre, torch.float32, H)
+        if by not in ("row", "channel"):
+            raise ValueError(f"LocalMoe: by is {by!r}, not 'row' or 'channel'")
+        if o is not None:
+            _expect("o", o, torch.bfloat16, T, H)
+        elif w_post is not None or gate is not None:
+            raise ValueError("LocalMoe: w_post or gate is given without o")
+        if w_post is not None:
+            _expect("w_post", w_post, torch.float32, H)
+        kind = B.MOE_GATE_NONE
+        if gate is not None:
+            _expect("gate", gate, torch.float32, T if by == "row" else H)
+            kind = B.MOE_GATE_ROW if by == "row" else B.MOE_GATE_CHANNEL
+        return B.MoeNormDesc(T, H, int(x.dtype == torch.float32), kind, eps, alpha)
+
+    def norm(self, x, w_pre, o=None, w_post=None, gate=None, by="channel", eps=1e-6, alpha=1.0, stream=None):
+        """The stream with a block's output o added, r = x + alpha gate (o / rms(o) w_post), and n = r / rms(r) w_pre,
+        the next block's input (new tensors). x [rows][width] bf16 or float32, o bf16 or None (r is x then); w_post or
+        None: o as it is; gate: float32, a value for each row or channel (by), or None."""
+        desc = self._norm_desc(x, w_pre, o, w_post, gate, by, eps, alpha)
+        with self._on(stream):
+            r = torch.empty_like(x) if o is not None else None
+            n = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+            B.moe_norm(desc, x, o, w_post, gate, w_pre, r, n, self.err)
+        return (r if o is not None else x), n
+
+    def norm_grad(self, r, grad_n, w_pre, grad_r=None, o=None, w_post=None, gate=None, by="channel", eps=1e-6, alpha=1.0,
+                  stream=None) -> NormGrads:
+        """Gradients of norm (new tensors) from the stream r that it returned and the gradients of both its results;
+        grad_r None: r was not used beside n."""
+        desc = self._norm_desc(r, w_pre, o, w_post, gate, by, eps, alpha)
+        _expect("grad_n", grad_n, torch.bfloat16, *r.shape)
+        if grad_r is not None:
+            _expect("grad_r", grad_r, r.dtype, *r.shape)
+        with self._on(stream):
+            g = NormGrads(torch.empty_like(r), torch.empty_like(o) if o is not None else None, torch.empty_like(w_pre),
+                          torch.empty_like(w_post) if w_post is not None else None,
+                          torch.empty_like(gate) if gate is not None else None)
+            work = torch.empty(max(1, B.moe_norm_workspace(desc)), dtype=torch.uint8, device=r.device)
+            B.moe_norm_grad(desc, r, o, w_post, gate, w_pre, grad_r, grad_n, g.x, g.o, g.w_post, g.gate, g.w_pre, work,
+                            self.err)
+        return g
 
     def error(self, stream=None) -> int:
         with self._on(stream):

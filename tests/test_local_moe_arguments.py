@@ -93,3 +93,65 @@ def test_what_passes_reaches_the_binding():
                  lambda: layer().shared(GOOD["x"], GOOD["w"]), lambda: layer().backward(z(T, H), f(T, E), None)):
         with pytest.raises(ValueError, match="libmoe_layout takes device tensors"):
             call()
+
+
+@pytest.mark.parametrize("save", ["fp16", 1, "none"])
+def test_what_is_kept_is_refused(save):
+    w = type("W", (), dict(w_gate=z(E, 128, H), w_up=z(E, 128, H), w_down=z(E, H, 128)))()
+    refused("save", layer(inter=128).experts, w, save=save)
+    refused("save", layer().dense, z(5, H), z(24, H), z(24, H), z(H, 24), save=save)
+
+
+def test_backward_with_weights_follows_a_forward_that_kept():
+    w = type("W", (), dict(w_gate=z(E, 128, H), w_up=z(E, 128, H), w_down=z(E, H, 128)))()
+    with pytest.raises(ValueError, match="follows a forward with save"):
+        layer(inter=128).backward(z(T, H), f(T, E), w)
+    w.w_up = z(E, 128, H + 8)
+    refused("w_up", layer(inter=128).backward, z(T, H), f(T, E), w)
+
+
+DENSE = dict(x=z(5, H), w_gate=z(24, H), w_up=z(24, H), w_down=z(H, 24))
+
+
+@pytest.mark.parametrize("name,bad", [("x", f(5, H)), ("x", z(5 * H)), ("w_gate", z(24, H + 8)), ("w_up", z(16, H)),
+                                      ("w_down", z(24, H)), ("w_down", f(H, 24))])
+def test_dense_refuses(name, bad):
+    refused(name, layer().dense, **{**DENSE, name: bad})
+
+
+@pytest.mark.parametrize("name,bad", [("x", z(4, H)), ("w_gate", z(16, H)), ("w_up", f(24, H)), ("w_down", z(24, H)),
+                                      ("grad_y", z(5, H + 8))])
+def test_dense_grad_refuses(name, bad):
+    kept = P.KeptFfn(B.MoeFfnDesc(5, H, 24, 1, 1, 0, 1, 0), z(5, 24), z(5, 24), None, None)
+    refused(name, layer().dense_grad, kept, **{**DENSE, "grad_y": z(5, H), name: bad})
+
+
+NORM = dict(x=z(5, H), w_pre=f(H), o=z(5, H), w_post=f(H), gate=f(H))
+
+
+@pytest.mark.parametrize("name,bad", [("x", z(5 * H)), ("x", z(5, H, dtype=torch.float16)), ("w_pre", z(H)),
+                                      ("w_pre", f(H + 8)), ("o", f(5, H)), ("o", z(4, H)), ("w_post", z(H)),
+                                      ("w_post", f(5)), ("gate", f(5)), ("gate", z(H)), ("by", "rows")])
+def test_norm_refuses(name, bad):
+    refused(name, layer().norm, **{**NORM, name: bad})
+    if name != "x":
+        good = {("r" if k == "x" else k): v for k, v in NORM.items()}
+        refused(name, layer().norm_grad, **{**good, "grad_n": z(5, H), name: bad})
+
+
+def test_norm_without_a_block_takes_nothing_of_it():
+    refused("w_post or gate", layer().norm, z(5, H), f(H), gate=f(H))
+    refused("grad_r", layer().norm_grad, z(5, H), z(5, H), f(H), f(5, H))
+    refused("grad_n", layer().norm_grad, z(5, H), f(5, H), f(H))
+
+
+def test_what_passes_of_training_reaches_the_binding():
+    w = type("W", (), dict(w_gate=z(E, 128, H), w_up=z(E, 128, H), w_down=z(E, H, 128)))()
+    kept = P.KeptFfn(B.MoeFfnDesc(5, H, 24, 1, 1, 0, 1, 0), z(5, 24), z(5, 24), None, None)
+    for call in (lambda: layer(inter=128).experts(w, save="bf16"), lambda: layer(inter=128).experts(w, save="fp8"),
+                 lambda: layer().dense(**DENSE), lambda: layer().dense(**DENSE, save="bf16"),
+                 lambda: layer().dense_grad(kept, **DENSE, grad_y=z(5, H)), lambda: layer().norm(**NORM),
+                 lambda: layer().norm(f(5, H), f(H)), lambda: layer().norm(**{**NORM, "gate": f(5)}, by="row"),
+                 lambda: layer().norm_grad(f(5, H), z(5, H), f(H), f(5, H))):
+        with pytest.raises(ValueError, match="libmoe_layout takes device tensors"):
+            call()
