@@ -10,7 +10,7 @@
 //
 // One persistent kernel, a CTA per SM, in five forms. Roles as in the expert
 // stage: a TMA producer warp, an MMA warp with two 128 x 256 fp32 accumulators in
-// tensor memory, four epilogue warps; in the weights' form a seventh warp that
+// tensor memory, eight epilogue warps; in the weights' form one more warp that
 // clears what the last K block of an expert holds of the next one's rows.
 //
 //   form   D [128 x up to 256]        A                    B                     K
@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "moe_ffn.cuh"
 #include "moe_tc.cuh"
@@ -51,7 +52,8 @@ constexpr int kTileB = kBN * kBK * 2;
 constexpr int kStage = kTileA + kTileB;
 constexpr int kHalfBox = 64 * kBK * 2;    // a box of 64 columns x 64 rows
 constexpr int kFullBox = 128 * kBK * 2;   // a box of 64 columns x 128 rows
-constexpr int kThreads = 192, kThreadsDw = 224;
+constexpr int kEpilogueWarps = 8;  // two for each quarter of tensor memory's lanes
+constexpr int kThreads = 64 + 32 * kEpilogueWarps, kThreadsDw = kThreads + 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemFixed = 1024 + kStages * kStage + (2 * kStages + 7) * 8 + 8;
 constexpr int kSmemMax = 227 * 1024;
@@ -97,6 +99,7 @@ struct FfnArgs {
   int out_cols;   // output columns of a tile: 128 (kUp) or 256
   int ntiles_n, group_n;
   int act, save;
+  int wide;       // every row that the epilogue touches begins on a 32-byte boundary
   int dw_total;   // kDw: tiles of all experts
 };
 
@@ -172,38 +175,69 @@ __device__ __forceinline__ void e4m3x2_to_float(uint16_t c, float *lo, float *hi
   *hi = b;
 }
 
-// ---- epilogues: one thread, its accumulator row ----
+// ---- epilogues: one thread, half of its accumulator row ----
+
+// 32 bytes of a row: one whole sector where rows begin on such a boundary (two stores of 16 bytes each reach L2 as
+// two half sectors), `left` of their elements of 1 << ELEM bytes existing.
+template <int ELEM>
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v, bool wide, int left) {
+  constexpr int per = 32 >> ELEM;  // elements
+  if (wide && left >= per) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+    return;
+  }
+  uint4 *d = static_cast<uint4 *>(dst);
+  if (left > 0) d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+  if (left > per / 2) d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+template <int ELEM>
+__device__ __forceinline__ void load32(const void *src, uint32_t *v, bool wide, int left) {
+  constexpr int per = 32 >> ELEM;
+  if (wide && left >= per) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(src));
+    return;
+  }
+  const uint4 *s = static_cast<const uint4 *>(src);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 a = left > 0 ? __ldg(s) : zero, b = left > per / 2 ? __ldg(s + 1) : zero;
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
 
 // y, dx, dw: 32 columns, rounded.
-__device__ __forceinline__ void store_plain(__nv_bfloat16 *dst, const uint32_t *r, int left) {
-  uint4 *d = reinterpret_cast<uint4 *>(dst);
+__device__ __forceinline__ void store_plain(__nv_bfloat16 *dst, const uint32_t *r, bool wide, int left) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (8 * v < left)
-      d[v] = make_uint4(pack2(__uint_as_float(r[8 * v]), __uint_as_float(r[8 * v + 1])),
-                        pack2(__uint_as_float(r[8 * v + 2]), __uint_as_float(r[8 * v + 3])),
-                        pack2(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
-                        pack2(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
+  for (int v = 0; v < 2; ++v) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      pk[i] = pack2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
+    store32<1>(dst + 16 * v, pk, wide, left - 16 * v);
   }
 }
 
 // h = act(g) u for 32 columns; r: g then u.
-__device__ __forceinline__ void store_hidden(__nv_bfloat16 *dst, const uint32_t (&r)[64], int act, int left) {
-  uint32_t pk[16];
+__device__ __forceinline__ void store_hidden(__nv_bfloat16 *dst, const uint32_t (&r)[64], int act, bool wide, int left) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float h0 = act_of<false>(__uint_as_float(r[2 * i]), act, nullptr) * __uint_as_float(r[32 + 2 * i]);
-    const float h1 = act_of<false>(__uint_as_float(r[2 * i + 1]), act, nullptr) * __uint_as_float(r[33 + 2 * i]);
-    pk[i] = pack2(h0, h1);
+  for (int v = 0; v < 2; ++v) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = 16 * v + 2 * i;
+      const float h0 = act_of<false>(__uint_as_float(r[k]), act, nullptr) * __uint_as_float(r[32 + k]);
+      const float h1 = act_of<false>(__uint_as_float(r[k + 1]), act, nullptr) * __uint_as_float(r[33 + k]);
+      pk[i] = pack2(h0, h1);
+    }
+    store32<1>(dst + 16 * v, pk, wide, left - 16 * v);
   }
-  uint4 *d = reinterpret_cast<uint4 *>(dst);
-#pragma unroll
-  for (int v = 0; v < 4; ++v)
-    if (8 * v < left) d[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
 }
 
 // 32 columns as e4m3 codes of the block's scale (library format: amax / 448 over 128 columns).
-__device__ __forceinline__ void store_codes(uint8_t *dst, const uint32_t *r, const BlockScale &bs) {
+__device__ __forceinline__ void store_codes(uint8_t *dst, const uint32_t *r, const BlockScale &bs, bool wide) {
   uint32_t q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -212,13 +246,11 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const uint32_t *r, con
            (static_cast<uint32_t>(
                 e4m3x2_of_quotients(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]), bs))
             << 16);
-  uint4 *d = reinterpret_cast<uint4 *>(dst);
-  d[0] = make_uint4(q[0], q[1], q[2], q[3]);
-  d[1] = make_uint4(q[4], q[5], q[6], q[7]);
+  store32<0>(dst, q, wide, 32);
 }
 
-__device__ __forceinline__ void epilogue_up(const FfnArgs &a, const Job &t, uint32_t tb, int m) {
-  const bool valid = m < t.rows;
+__device__ __forceinline__ void epilogue_up(const FfnArgs &a, const Job &t, uint32_t tb, int m, int half) {
+  const bool valid = m < t.rows, wide = a.wide != 0;
   const int64_t p = t.row0 + (valid ? m : 0);
   const int left = a.I - t.n0;  // columns of the tile that exist
   const int64_t at = p * a.I + t.n0;
@@ -238,68 +270,64 @@ __device__ __forceinline__ void epilogue_up(const FfnArgs &a, const Job &t, uint
     us = block_scale(ua);
     if (valid) {
       const int64_t sc = p * (a.I / kScaleBlock) + t.n0 / kScaleBlock;
-      a.keep_gate_scales[sc] = gs.s;
-      a.keep_up_scales[sc] = us.s;
+      if (half == 0)
+        a.keep_gate_scales[sc] = gs.s;
+      else
+        a.keep_up_scales[sc] = us.s;
     }
   }
-  for (int c = 0; c < 128; c += 32) {
+  for (int c = 64 * half; c < 64 * half + 64; c += 32) {
     uint32_t r[64];
     tmem_load32x2_wait(tb + c, tb + 128 + c, r);
     if (!valid) continue;
-    store_hidden(static_cast<__nv_bfloat16 *>(a.out0) + at + c, r, a.act, left - c);
+    store_hidden(static_cast<__nv_bfloat16 *>(a.out0) + at + c, r, a.act, wide, left - c);
     if (a.save == MOE_SAVE_BF16) {
-      store_plain(static_cast<__nv_bfloat16 *>(a.keep_gate) + at + c, r, left - c);
-      store_plain(static_cast<__nv_bfloat16 *>(a.keep_up) + at + c, r + 32, left - c);
+      store_plain(static_cast<__nv_bfloat16 *>(a.keep_gate) + at + c, r, wide, left - c);
+      store_plain(static_cast<__nv_bfloat16 *>(a.keep_up) + at + c, r + 32, wide, left - c);
     } else if (a.save == MOE_SAVE_FP8) {
-      store_codes(static_cast<uint8_t *>(a.keep_gate) + at + c, r, gs);
-      store_codes(static_cast<uint8_t *>(a.keep_up) + at + c, r + 32, us);
+      store_codes(static_cast<uint8_t *>(a.keep_gate) + at + c, r, gs, wide);
+      store_codes(static_cast<uint8_t *>(a.keep_up) + at + c, r + 32, us, wide);
     }
   }
 }
 
-__device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint32_t tb, int m) {
-  const bool valid = m < t.rows;
+__device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint32_t tb, int m, int half) {
+  const bool valid = m < t.rows, wide = a.wide != 0, f8 = a.save == MOE_SAVE_FP8;
   const int64_t p = t.row0 + (valid ? m : 0);
-  for (int c = 0; c < t.ncols; c += 32) {
+  const int end = min(t.ncols, 128 * half + 128);
+  for (int c = 128 * half; c < end; c += 32) {
     const int left = a.I - t.n0 - c;
     const int64_t at = p * a.I + t.n0 + c;
     uint32_t gq[16], uq[16];  // 32 values as bf16 pairs, or as codes in the first 8
     float gsc = 1.0f, usc = 1.0f;
     if (valid) {
-      const bool f8 = a.save == MOE_SAVE_FP8;
-      const uint4 *gp = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.gate) + (f8 ? at : 2 * at));
-      const uint4 *up = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.up) + (f8 ? at : 2 * at));
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if ((f8 ? 16 : 8) * v < left && !(f8 && v >= 2)) {
-          const uint4 x = __ldg(gp + v), y = __ldg(up + v);
-          gq[4 * v] = x.x, gq[4 * v + 1] = x.y, gq[4 * v + 2] = x.z, gq[4 * v + 3] = x.w;
-          uq[4 * v] = y.x, uq[4 * v + 1] = y.y, uq[4 * v + 2] = y.z, uq[4 * v + 3] = y.w;
-        } else {
-          gq[4 * v] = gq[4 * v + 1] = gq[4 * v + 2] = gq[4 * v + 3] = 0;
-          uq[4 * v] = uq[4 * v + 1] = uq[4 * v + 2] = uq[4 * v + 3] = 0;
+      if (f8) {
+        load32<0>(static_cast<const uint8_t *>(a.gate) + at, gq, wide, left);
+        load32<0>(static_cast<const uint8_t *>(a.up) + at, uq, wide, left);
+        if (left > 0) {
+          const int64_t sc = p * (a.I / kScaleBlock) + (t.n0 + c) / kScaleBlock;
+          gsc = __ldg(a.gate_scales + sc);
+          usc = __ldg(a.up_scales + sc);
         }
-      }
-      if (f8 && left > 0) {
-        const int64_t sc = p * (a.I / kScaleBlock) + (t.n0 + c) / kScaleBlock;
-        gsc = __ldg(a.gate_scales + sc);
-        usc = __ldg(a.up_scales + sc);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          load32<1>(static_cast<const uint16_t *>(a.gate) + at + 16 * v, gq + 8 * v, wide, left - 16 * v);
+          load32<1>(static_cast<const uint16_t *>(a.up) + at + 16 * v, uq + 8 * v, wide, left - 16 * v);
+        }
       }
     }
     uint32_t r[32];
     tmem_load32_wait(tb + c, r);
     if (!valid) continue;
-    uint4 *od = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out0) + at);
-    uint4 *ou = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out1) + at);
-    uint4 *oh = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out2) + at);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      uint32_t pd[4], pu[4], ph[4];
+    for (int v = 0; v < 2; ++v) {
+      uint32_t pd[8], pu[8], ph[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         float g0, g1, u0, u1;
-        const int k = 4 * v + i;  // the pair of columns 2 k, 2 k + 1
-        if (a.save == MOE_SAVE_FP8) {
+        const int k = 8 * v + i;  // the pair of columns 2 k, 2 k + 1
+        if (f8) {
           e4m3x2_to_float(static_cast<uint16_t>(gq[k >> 1] >> (16 * (k & 1))), &g0, &g1);
           e4m3x2_to_float(static_cast<uint16_t>(uq[k >> 1] >> (16 * (k & 1))), &u0, &u1);
           g0 *= gsc, g1 *= gsc, u0 *= usc, u1 *= usc;
@@ -313,17 +341,15 @@ __device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint
         pu[i] = pack2(h0 * a0, h1 * a1);
         ph[i] = pack2(a0 * u0, a1 * u1);
       }
-      if (8 * v < left) {
-        od[v] = make_uint4(pd[0], pd[1], pd[2], pd[3]);
-        ou[v] = make_uint4(pu[0], pu[1], pu[2], pu[3]);
-        oh[v] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-      }
+      store32<1>(static_cast<__nv_bfloat16 *>(a.out0) + at + 16 * v, pd, wide, left - 16 * v);
+      store32<1>(static_cast<__nv_bfloat16 *>(a.out1) + at + 16 * v, pu, wide, left - 16 * v);
+      store32<1>(static_cast<__nv_bfloat16 *>(a.out2) + at + 16 * v, ph, wide, left - 16 * v);
     }
   }
 }
 
 template <int FORM>
-__device__ __forceinline__ void epilogue_plain(const FfnArgs &a, const Job &t, uint32_t tb, int m) {
+__device__ __forceinline__ void epilogue_plain(const FfnArgs &a, const Job &t, uint32_t tb, int m, int half) {
   bool valid;
   __nv_bfloat16 *dst;
   int width;
@@ -339,15 +365,19 @@ __device__ __forceinline__ void epilogue_plain(const FfnArgs &a, const Job &t, u
     valid = m < t.rows;
     dst = static_cast<__nv_bfloat16 *>(a.out0) + static_cast<int64_t>(t.row0 + (valid ? m : 0)) * width + t.n0;
   }
+  const int end = min(t.ncols, 128 * half + 128);
   if (FORM == kDw && t.kblocks == 0) {  // an expert without rows: its gradient is 0
-    for (int c = 0; valid && c < t.ncols && t.n0 + c < width; c += 8)
+    for (int c = 128 * half; valid && c < end && t.n0 + c < width; c += 8)
       *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
     return;
   }
-  for (int c = 0; c < t.ncols; c += 32) {
-    uint32_t r[32];
-    tmem_load32_wait(tb + c, r);
-    if (valid) store_plain(dst + c, r, width - t.n0 - c);
+  for (int c = 128 * half; c < end; c += 64) {
+    uint32_t r[64];
+    tmem_load32x2_wait(tb + c, tb + c + 32, r);
+    if (valid) {
+      store_plain(dst + c, r, a.wide != 0, width - t.n0 - c);
+      store_plain(dst + c + 32, r + 32, a.wide != 0, width - t.n0 - c - 32);
+    }
   }
 }
 
@@ -377,7 +407,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull + b, 1);
-      mbar_init(tempty + b, 4);
+      mbar_init(tempty + b, kEpilogueWarps);
     }
     mbar_init(tail, 1);
     mbar_init(cleared, 1);
@@ -501,9 +531,9 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
       mbar_wait_bounded(done, 0);
     }
     __syncwarp();
-  } else if (warp < 6) {
-    // ---- epilogue: warps 2..5, warp w reads TMEM lanes 32 * (w % 4) .. + 31 ----
-    const int q = warp & 3;
+  } else if (warp < 2 + kEpilogueWarps) {
+    // ---- epilogue: warp w reads TMEM lanes 32 * (w % 4) .. + 31, of the first or second half of the columns ----
+    const int q = warp & 3, half = (warp - 2) >> 2;
     const int m = q * 32 + lane;
     int lt = 0;
     for (int w = blockIdx.x; w < total; w += gridDim.x, ++lt) {
@@ -517,11 +547,11 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
       const Job t = job_of<FORM>(w, pref, offs, a);
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBN;
       if constexpr (FORM == kUp)
-        epilogue_up(a, t, tb, m);
+        epilogue_up(a, t, tb, m, half);
       else if constexpr (FORM == kDh)
-        epilogue_dh(a, t, tb, m);
+        epilogue_dh(a, t, tb, m, half);
       else
-        epilogue_plain<FORM>(a, t, tb, m);
+        epilogue_plain<FORM>(a, t, tb, m, half);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(tempty + buf));
@@ -646,6 +676,13 @@ FfnArgs base_args(const FfnSizes &s, const int32_t *offsets, int32_t *err) {
 
 int blocks_of(int k) { return (k + kBK - 1) / kBK; }
 
+// Whether rows of `width` elements of these arrays all begin on 32-byte boundaries (null: not used).
+bool wide_rows(int64_t row_bytes, std::initializer_list<const void *> arrays) {
+  bool good = row_bytes % 32 == 0;
+  for (const void *p : arrays) good = good && aligned32(p);
+  return good;
+}
+
 bool good16(const void *p) { return p != nullptr && aligned16(p); }
 bool good4(const void *p) { return p != nullptr && aligned4(p); }
 
@@ -687,6 +724,7 @@ extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_of
   a.kblocks = blocks_of(s.H);
   a.n_total = s.I;
   a.out_cols = 128;
+  a.wide = wide_rows(2 * s.I, {h, gate, up});
   st = launch_form<kUp>(m, a, s, cs);
   if (st != MOE_OK) return st;
   if (!ffn_map(&m.m[0], h, s.I, s.rows, 0, 128) || !ffn_map(&m.m[1], w_down, s.I, s.H, s.E, 128)) return MOE_ECUDA;
@@ -695,6 +733,7 @@ extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_of
   a.kblocks = blocks_of(s.I);
   a.n_total = s.H;
   a.out_cols = kBN;
+  a.wide = wide_rows(2 * s.H, {y});
   return launch_form<kDown>(m, a, s, cs);
 }
 
@@ -740,6 +779,7 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
   a.kblocks = blocks_of(s.H);
   a.n_total = s.I;
   a.out_cols = kBN;
+  a.wide = wide_rows(2 * s.I, {gate, up, grad_gate, grad_up, h});
   st = launch_form<kDh>(m, a, s, cs);
   if (st != MOE_OK) return st;
 
@@ -751,6 +791,7 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
   a.kblocks = 2 * blocks_of(s.I);
   a.n_total = s.H;
   a.out_cols = kBN;
+  a.wide = wide_rows(2 * s.H, {grad_x});
   st = launch_form<kDx>(m, a, s, cs);
   if (st != MOE_OK || !weights) return st;
 
@@ -762,5 +803,6 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
   a.out0 = grad_w_gate;
   a.out1 = grad_w_up;
   a.out2 = grad_w_down;
+  a.wide = wide_rows(2 * s.H, {grad_w_gate, grad_w_up, grad_w_down}) && s.I % 16 == 0;
   return launch_form<kDw>(m, a, s, cs);
 }

@@ -17,18 +17,23 @@ moe_status launch_ffn_few(const FfnSizes &s, const int32_t *offsets, const void 
 
 namespace {
 
-// act(g) and act'(g), in fp32.
+// 1 / (1 + exp(-v)), to a few units in the last place (2^-20 of it where |v| is below 10): what it goes into is
+// rounded to bf16. 0 and 1 at the ends.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+// act(g) and act'(g), in fp32. The second act, g (1 + tanh(z)) / 2 with z = sqrt(2/pi) (g + 0.044715 g^3), is
+// g sigmoid(2 z); so is the derivative: p + g p (1 - p) 2 z'.
 template <bool GRAD>
 __device__ __forceinline__ float act_of(float g, int act, float *da) {
-  if (act == MOE_ACT_SILU) {
-    const float p = 1.0f / (1.0f + expf(-g));
-    if constexpr (GRAD) *da = p * (1.0f + g * (1.0f - p));
-    return g * p;
+  float v = g, dv = 1.0f;
+  if (act != MOE_ACT_SILU) {
+    constexpr float k = 1.5957691216057308f, c = 0.044715f;  // 2 sqrt(2 / pi)
+    v = k * (g + c * g * g * g);
+    if constexpr (GRAD) dv = k * (1.0f + 3.0f * c * g * g);
   }
-  constexpr float k = 0.7978845608028654f, c = 0.044715f;  // sqrt(2 / pi)
-  const float t = tanhf(k * (g + c * g * g * g));
-  if constexpr (GRAD) *da = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * k * (1.0f + 3.0f * c * g * g);
-  return 0.5f * g * (1.0f + t);
+  const float p = sigmoid(v);
+  if constexpr (GRAD) *da = p + g * p * (1.0f - p) * dv;
+  return g * p;
 }
 
 }  // namespace
