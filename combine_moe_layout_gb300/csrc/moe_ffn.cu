@@ -55,8 +55,11 @@ constexpr int kFullBox = 128 * kBK * 2;   // a box of 64 columns x 128 rows
 constexpr int kEpilogueWarps = 8;  // two for each quarter of tensor memory's lanes
 constexpr int kThreads = 64 + 32 * kEpilogueWarps, kThreadsDw = kThreads + 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSmemFixed = 1024 + kStages * kStage + (2 * kStages + 7) * 8 + 8;
+constexpr int kSmemFixed = 1024 + kStages * kStage + (3 * kStages + 5) * 8 + 8;
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kPiece = 32 * 64 * 2;  // kDw: 32 rows x 64 columns of the result, on their way out of a warp
+constexpr int kSmemDw = kSmemFixed + kEpilogueWarps * kPiece;
+static_assert(kSmemDw <= kSmemMax, "");
 
 enum Form { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
 
@@ -81,13 +84,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 }
 
 struct FfnMaps {
-  CUtensorMap m[5];
+  CUtensorMap m[5];  // operands
+  CUtensorMap d[3];  // kDw: the results
 };
 
 struct FfnArgs {
   const int32_t *offsets;  // [E * R + 1], or null: one expert with all rows
   int32_t *err;
-  void *out0, *out1, *out2;             // by form: h | y | dg, du, h | dx | dw_gate, dw_up, dw_down
+  void *out0, *out1, *out2;             // by form: h | y | dg, du, h | dx
   const void *gate, *up;                // kDh: what the forward kept
   const float *gate_scales, *up_scales;
   void *keep_gate, *keep_up;            // kUp: what it keeps
@@ -110,6 +114,11 @@ struct Job {
   int kblocks, tail;  // tail: rows of the last K block (kDw; 64 or 0: whole)
 };
 
+// First packed row of expert e; e = E: behind the last.
+__device__ __forceinline__ int row_offset(const FfnArgs &a, int e) {
+  return a.offsets != nullptr ? __ldg(a.offsets + static_cast<int64_t>(e) * a.R) : (e == 0 ? 0 : a.rows);
+}
+
 template <int FORM>
 __device__ __forceinline__ Job job_of(int w, const int32_t *pref, const int32_t *offs, const FfnArgs &a) {
   Job j;
@@ -131,7 +140,7 @@ __device__ __forceinline__ Job job_of(int w, const int32_t *pref, const int32_t 
     j.n0 = (g * a.group_n + r - m * gw) * kBN;
     const int left = (j.which == 2 ? a.I : a.H) - j.n0;
     j.ncols = min(kBN, (left + 63) & ~63);
-    const int lo = offs[j.e], hi = offs[j.e + 1];
+    const int lo = row_offset(a, j.e), hi = row_offset(a, j.e + 1);
     const bool good = lo >= 0 && hi >= lo && hi <= a.rows;
     j.row0 = good ? lo : 0;
     j.rows = good ? hi - lo : 0;
@@ -348,35 +357,66 @@ __device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint
   }
 }
 
-template <int FORM>
 __device__ __forceinline__ void epilogue_plain(const FfnArgs &a, const Job &t, uint32_t tb, int m, int half) {
-  bool valid;
-  __nv_bfloat16 *dst;
-  int width;
-  if constexpr (FORM == kDw) {
-    width = t.which == 2 ? a.I : a.H;
-    const int height = t.which == 2 ? a.H : a.I;
-    valid = t.m0 + m < height;
-    void *base = t.which == 0 ? a.out0 : (t.which == 1 ? a.out1 : a.out2);
-    dst = static_cast<__nv_bfloat16 *>(base) +
-          (static_cast<int64_t>(t.e) * height + t.m0 + (valid ? m : 0)) * width + t.n0;
-  } else {
-    width = a.n_total;
-    valid = m < t.rows;
-    dst = static_cast<__nv_bfloat16 *>(a.out0) + static_cast<int64_t>(t.row0 + (valid ? m : 0)) * width + t.n0;
-  }
+  const bool valid = m < t.rows;
+  __nv_bfloat16 *dst =
+      static_cast<__nv_bfloat16 *>(a.out0) + static_cast<int64_t>(t.row0 + (valid ? m : 0)) * a.n_total + t.n0;
   const int end = min(t.ncols, 128 * half + 128);
-  if (FORM == kDw && t.kblocks == 0) {  // an expert without rows: its gradient is 0
-    for (int c = 128 * half; valid && c < end && t.n0 + c < width; c += 8)
-      *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
-    return;
-  }
   for (int c = 128 * half; c < end; c += 64) {
     uint32_t r[64];
     tmem_load32x2_wait(tb + c, tb + c + 32, r);
     if (valid) {
-      store_plain(dst + c, r, a.wide != 0, width - t.n0 - c);
-      store_plain(dst + c + 32, r + 32, a.wide != 0, width - t.n0 - c - 32);
+      store_plain(dst + c, r, a.wide != 0, a.n_total - t.n0 - c);
+      store_plain(dst + c + 32, r + 32, a.wide != 0, a.n_total - t.n0 - c - 32);
+    }
+  }
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
+// A weight's gradient leaves through shared memory and TMA: with few K blocks to a tile its stores bound the kernel,
+// and as stores of each thread's own row (32 lines to an instruction) they also held up the clearing of tails, whose
+// shared-memory stores queue behind them (24576 rows of 64 experts, 383 each: 1168 us so, 828 without stores).
+__device__ __forceinline__ void epilogue_dw(const FfnArgs &a, const FfnMaps &maps, const Job &t, uint32_t tb, int q,
+                                            int half, int lane, uint8_t *piece, uint64_t *released) {
+  const int width = t.which == 2 ? a.I : a.H, height = t.which == 2 ? a.H : a.I;
+  const int y = t.m0 + q * 32;
+  const int end = min(t.ncols, 128 * half + 128);
+  for (int c = 128 * half; c < 128 * half + 128; c += 64) {
+    uint32_t r[64];
+    const bool some = c < end && y < height;
+    if (some && t.kblocks != 0) {
+      tmem_load32x2_wait(tb + c, tb + c + 32, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) r[i] = 0;  // an expert without rows: its gradient is 0
+    }
+    if (c == 128 * half + 64) {  // the accumulator has been read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(released));
+    }
+    if (!some) continue;
+    // the piece's last store has read it
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    uint4 *line = reinterpret_cast<uint4 *>(piece + lane * 128);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      line[j ^ (lane & 7)] = make_uint4(pack2(__uint_as_float(r[8 * j]), __uint_as_float(r[8 * j + 1])),
+                                        pack2(__uint_as_float(r[8 * j + 2]), __uint_as_float(r[8 * j + 3])),
+                                        pack2(__uint_as_float(r[8 * j + 4]), __uint_as_float(r[8 * j + 5])),
+                                        pack2(__uint_as_float(r[8 * j + 6]), __uint_as_float(r[8 * j + 7])));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && t.n0 + c < width) {
+      tma_store_3d(&maps.d[t.which], smem_addr(piece), t.n0 + c, y, t.e);
+      bulk_commit();
     }
   }
 }
@@ -384,14 +424,13 @@ __device__ __forceinline__ void epilogue_plain(const FfnArgs &a, const Job &t, u
 template <int FORM>
 __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs a) {
-  constexpr int kT = FORM == kDw ? kThreadsDw : kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage);
+  // kDw: a piece of the result for each epilogue warp, behind the stages
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage + (FORM == kDw ? kEpilogueWarps * kPiece : 0));
   uint64_t *empty = full + kStages;
-  uint64_t *tail = empty + kStages;  // kDw: an expert's last K block has landed; its tail has been cleared
-  uint64_t *cleared = tail + 1;
-  uint64_t *tfull = cleared + 1;
+  uint64_t *landed = empty + kStages;  // kDw: an expert's last K block, before its tail has been cleared
+  uint64_t *tfull = landed + kStages;
   uint64_t *tempty = tfull + 2;
   uint64_t *done = tempty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
@@ -404,13 +443,12 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
+      mbar_init(landed + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, kEpilogueWarps);
     }
-    mbar_init(tail, 1);
-    mbar_init(cleared, 1);
     mbar_init(done, 1);
     *abort = 0;
     fence_mbar_init();
@@ -422,21 +460,23 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  for (int e = tid; e <= a.E; e += kT)
-    offs[e] = a.offsets != nullptr ? a.offsets[static_cast<int64_t>(e) * a.R] : (e == 0 ? 0 : a.rows);
+  if constexpr (FORM != kDw)
+    for (int e = tid; e <= a.E; e += kThreads) offs[e] = row_offset(a, e);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  // (in the weights' form it only looks the offsets over)
-  if (warp == 0) tile_prefix<kBM>(offs, pref, a, lane);
-  __syncthreads();
+  if constexpr (FORM != kDw) {
+    if (warp == 0) tile_prefix<kBM>(offs, pref, a, lane);
+    __syncthreads();
+  }
   const int total = FORM == kDw ? a.dw_total : tile_total(pref, a);
 
   if (warp == 0) {
     if (lane == 0) {
       // ---- TMA producer ----
-      uint32_t it = 0;
+      uint32_t it = 0, tails = 0;  // tails: bit s: the last load into stage s went to `landed`
+      uint32_t landings = 0;       // bit s: parity of the next phase of landed[s]
       bool ok = true;
       for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
         const Job t = job_of<FORM>(w, pref, offs, a);
@@ -447,8 +487,16 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA, fb = smem_addr(full + s);
-          mbar_arrive_expect_tx(full + s, bytes);
+          uint64_t *bar = full + s;
+          if (FORM == kDw && t.tail != 0 && kb == t.kblocks - 1) {
+            bar = landed + s;  // the clearing warp passes it on
+            tails |= 1u << s;
+            landings ^= 1u << s;
+          } else {
+            tails &= ~(1u << s);
+          }
+          const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA, fb = smem_addr(bar);
+          mbar_arrive_expect_tx(bar, bytes);
           if constexpr (FORM == kUp) {
             tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
             tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, fb);
@@ -481,14 +529,17 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
       // the last load issued into each stage lands before the CTA may exit
       for (uint32_t s = 0; s < kStages && s < it; ++s) {
         const uint32_t last = s + ((it - 1 - s) / kStages) * kStages;
-        mbar_wait_bounded(full + s, (last / kStages) & 1u);
+        if ((tails >> s) & 1u)
+          mbar_wait_bounded(landed + s, ((landings >> s) & 1u) ^ 1u);
+        else
+          mbar_wait_bounded(full + s, (last / kStages) & 1u);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       // ---- MMA issuer ----
-      uint32_t it = 0, tails = 0;
+      uint32_t it = 0;
       int lt = 0;
       bool ok = true;
       for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++lt) {
@@ -505,14 +556,6 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
           if (!role_wait(full + s, sph, abort, a.err)) {
             ok = false;
             break;
-          }
-          if (FORM == kDw && t.tail != 0 && kb == t.kblocks - 1) {
-            mbar_arrive(smem_addr(tail));
-            if (!role_wait(cleared, tails & 1u, abort, a.err)) {
-              ok = false;
-              break;
-            }
-            ++tails;
           }
           tc_fence_after();
           const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA;
@@ -550,27 +593,34 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
         epilogue_up(a, t, tb, m, half);
       else if constexpr (FORM == kDh)
         epilogue_dh(a, t, tb, m, half);
+      else if constexpr (FORM == kDw)
+        epilogue_dw(a, maps, t, tb, q, half, lane, smem + kStages * kStage + (warp - 2) * kPiece, tempty + buf);
       else
-        epilogue_plain<FORM>(a, t, tb, m, half);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(tempty + buf));
+        epilogue_plain(a, t, tb, m, half);
+      if constexpr (FORM != kDw) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(tempty + buf));
+      }
     }
+    if (FORM == kDw && lane == 0) bulk_wait_all();
+    __syncwarp();
   } else if constexpr (FORM == kDw) {
     // ---- clears the rows of the last K block that are not the expert's (they may hold anything), in both
     // operands: lines of 128 bytes, one for each k and 64 columns
-    uint32_t it = 0, tails = 0;
+    uint32_t it = 0, landings = 0;
     for (int w = blockIdx.x; w < total; w += gridDim.x) {
       const Job t = job_of<FORM>(w, pref, offs, a);
       it += t.kblocks;
       if (t.tail == 0) continue;
+      // (a barrier of its own for each stage: the stage is not used again before this warp has passed it on, so that
+      // no phase is missed, and it is cleared while the MMAs of the blocks before it run)
       const uint32_t s = (it - 1) % kStages;
-      // (asked for by the MMA warp, which waits: of a stage's own barrier this warp would miss phases)
       int ok = 0;
-      if (lane == 0) ok = role_wait(tail, tails & 1u, abort, a.err) ? 1 : 0;
+      if (lane == 0) ok = role_wait(landed + s, (landings >> s) & 1u, abort, a.err) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      ++tails;
+      landings ^= 1u << s;
       uint8_t *box = smem + s * kStage;
       const int boxes = kBM / 64 + t.ncols / 64;  // those of A, and those of B right behind them
       const int words = (kBK - t.tail) * 8;       // 16-byte words of a box's cleared lines
@@ -579,7 +629,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
           *reinterpret_cast<uint4 *>(box + b * kHalfBox + t.tail * 128 + i * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(cleared));
+      if (lane == 0) mbar_arrive(smem_addr(full + s));
     }
   }
   tc_fence_before();
@@ -633,7 +683,7 @@ template <int FORM>
 moe_status launch_form(const FfnMaps &maps, FfnArgs a, const FfnSizes &s, cudaStream_t stream) {
   const int all = sm_count();
   const int sms = s.num_sms > 0 && s.num_sms < all ? s.num_sms : all;
-  const int smem = kSmemFixed + 12 * (a.E + 1);
+  const int smem = FORM == kDw ? kSmemDw : kSmemFixed + 12 * (a.E + 1);
   if (smem > kSmemMax) return MOE_EINVAL;
   int64_t tiles;
   if (FORM == kDw) {
@@ -797,12 +847,9 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
 
   if (!ffn_map(&m.m[0], grad_gate, s.I, s.rows, 0, 64) || !ffn_map(&m.m[1], grad_up, s.I, s.rows, 0, 64) ||
       !ffn_map(&m.m[2], grad_y, s.H, s.rows, 0, 64) || !ffn_map(&m.m[3], x, s.H, s.rows, 0, 64) ||
-      !ffn_map(&m.m[4], h, s.I, s.rows, 0, 64))
+      !ffn_map(&m.m[4], h, s.I, s.rows, 0, 64) || !ffn_map(&m.d[0], grad_w_gate, s.H, s.I, s.E, 32) ||
+      !ffn_map(&m.d[1], grad_w_up, s.H, s.I, s.E, 32) || !ffn_map(&m.d[2], grad_w_down, s.I, s.H, s.E, 32))
     return MOE_ECUDA;
   a = base_args(s, region_offsets, err);
-  a.out0 = grad_w_gate;
-  a.out1 = grad_w_up;
-  a.out2 = grad_w_down;
-  a.wide = wide_rows(2 * s.H, {grad_w_gate, grad_w_up, grad_w_down}) && s.I % 16 == 0;
   return launch_form<kDw>(m, a, s, cs);
 }
