@@ -105,6 +105,7 @@ struct FfnArgs {
   int act, save;
   int wide;       // every row that the epilogue touches begins on a 32-byte boundary
   int dw_total;   // kDw: tiles of all experts
+  int first;      // the first kernel of its call
 };
 
 struct Job {
@@ -300,6 +301,29 @@ __device__ __forceinline__ void epilogue_up(const FfnArgs &a, const Job &t, uint
   }
 }
 
+// dg, du and h of 16 columns, from dh and what was kept (8 words of bf16 pairs, or 4 of codes).
+template <bool F8>
+__device__ __forceinline__ void dh_of(const uint32_t *gq, const uint32_t *uq, float gsc, float usc, const uint32_t *dh,
+                                      int act, uint32_t (&pd)[8], uint32_t (&pu)[8], uint32_t (&ph)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float g0, g1, u0, u1;
+    if constexpr (F8) {
+      e4m3x2_to_float(static_cast<uint16_t>(gq[k >> 1] >> (16 * (k & 1))), &g0, &g1);
+      e4m3x2_to_float(static_cast<uint16_t>(uq[k >> 1] >> (16 * (k & 1))), &u0, &u1);
+      g0 *= gsc, g1 *= gsc, u0 *= usc, u1 *= usc;
+    } else {
+      g0 = lo_of(gq[k]), g1 = hi_of(gq[k]), u0 = lo_of(uq[k]), u1 = hi_of(uq[k]);
+    }
+    float d0, d1;
+    const float a0 = act_of<true>(g0, act, &d0), a1 = act_of<true>(g1, act, &d1);
+    const float h0 = __uint_as_float(dh[2 * k]), h1 = __uint_as_float(dh[2 * k + 1]);
+    pd[k] = pack2(h0 * u0 * d0, h1 * u1 * d1);
+    pu[k] = pack2(h0 * a0, h1 * a1);
+    ph[k] = pack2(a0 * u0, a1 * u1);
+  }
+}
+
 __device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint32_t tb, int m, int half) {
   const bool valid = m < t.rows, wide = a.wide != 0, f8 = a.save == MOE_SAVE_FP8;
   const int64_t p = t.row0 + (valid ? m : 0);
@@ -332,24 +356,10 @@ __device__ __forceinline__ void epilogue_dh(const FfnArgs &a, const Job &t, uint
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       uint32_t pd[8], pu[8], ph[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float g0, g1, u0, u1;
-        const int k = 8 * v + i;  // the pair of columns 2 k, 2 k + 1
-        if (f8) {
-          e4m3x2_to_float(static_cast<uint16_t>(gq[k >> 1] >> (16 * (k & 1))), &g0, &g1);
-          e4m3x2_to_float(static_cast<uint16_t>(uq[k >> 1] >> (16 * (k & 1))), &u0, &u1);
-          g0 *= gsc, g1 *= gsc, u0 *= usc, u1 *= usc;
-        } else {
-          g0 = lo_of(gq[k]), g1 = hi_of(gq[k]), u0 = lo_of(uq[k]), u1 = hi_of(uq[k]);
-        }
-        float d0, d1;
-        const float a0 = act_of<true>(g0, a.act, &d0), a1 = act_of<true>(g1, a.act, &d1);
-        const float h0 = __uint_as_float(r[2 * k]), h1 = __uint_as_float(r[2 * k + 1]);
-        pd[i] = pack2(h0 * u0 * d0, h1 * u1 * d1);
-        pu[i] = pack2(h0 * a0, h1 * a1);
-        ph[i] = pack2(a0 * u0, a1 * u1);
-      }
+      if (f8)
+        dh_of<true>(gq + 4 * v, uq + 4 * v, gsc, usc, r + 16 * v, a.act, pd, pu, ph);
+      else
+        dh_of<false>(gq + 8 * v, uq + 8 * v, 1.0f, 1.0f, r + 16 * v, a.act, pd, pu, ph);
       store32<1>(static_cast<__nv_bfloat16 *>(a.out0) + at + 16 * v, pd, wide, left - 16 * v);
       store32<1>(static_cast<__nv_bfloat16 *>(a.out1) + at + 16 * v, pu, wide, left - 16 * v);
       store32<1>(static_cast<__nv_bfloat16 *>(a.out2) + at + 16 * v, ph, wide, left - 16 * v);
@@ -419,6 +429,57 @@ __device__ __forceinline__ void epilogue_dw(const FfnArgs &a, const FfnMaps &map
       bulk_commit();
     }
   }
+}
+
+// The loads of K block kb of a tile: A and B.
+template <int FORM>
+__device__ __forceinline__ void load_a(const FfnMaps &maps, const Job &t, int kb, uint32_t sa, uint32_t bar) {
+  if constexpr (FORM == kDw) {  // maps: dg, du, dy (A), x, h (B)
+    for (int c = 0; c < kBM; c += 64)
+      tma_load_2d(sa + c / 64 * kHalfBox, &maps.m[t.which], t.m0 + c, t.row0 + kb * kBK, bar);
+  } else if constexpr (FORM == kDx) {  // dg, du (A), w_gate, w_up (B)
+    const int second = kb >= t.kblocks / 2 ? 1 : 0;
+    tma_load_2d(sa, &maps.m[second], (kb - second * (t.kblocks / 2)) * kBK, t.row0, bar);
+  } else {
+    tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, bar);
+  }
+}
+
+template <int FORM>
+__device__ __forceinline__ void load_b(const FfnMaps &maps, const Job &t, int kb, uint32_t sb, uint32_t bar) {
+  if constexpr (FORM == kUp) {
+    tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, bar);
+    tma_load_3d(sb + kFullBox, &maps.m[2], kb * kBK, t.n0, t.e, bar);
+  } else if constexpr (FORM == kDown) {
+    tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, bar);
+    if (t.ncols > 128) tma_load_3d(sb + kFullBox, &maps.m[1], kb * kBK, t.n0 + 128, t.e, bar);
+  } else if constexpr (FORM == kDh) {
+    for (int c = 0; c < t.ncols; c += 64)
+      tma_load_3d(sb + c / 64 * kHalfBox, &maps.m[1], t.n0 + c, kb * kBK, t.e, bar);
+  } else if constexpr (FORM == kDx) {
+    const int second = kb >= t.kblocks / 2 ? 1 : 0;
+    const int k = (kb - second * (t.kblocks / 2)) * kBK;
+    for (int c = 0; c < t.ncols; c += 64)
+      tma_load_3d(sb + c / 64 * kHalfBox, &maps.m[2 + second], t.n0 + c, k, t.e, bar);
+  } else {
+    for (int c = 0; c < t.ncols; c += 64)
+      tma_load_2d(sb + c / 64 * kHalfBox, &maps.m[t.which == 2 ? 4 : 3], t.n0 + c, t.row0 + kb * kBK, bar);
+  }
+}
+
+// The MMAs of one K block.
+template <int FORM>
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t sa, uint32_t sb, uint32_t idesc, bool first) {
+#pragma unroll
+  for (int kk = 0; kk < kBK / kUK; ++kk)
+    mma_bf16(d, a_is_mn(FORM) ? sw128_desc_mn(sa + kk * kUK * 128) : sw128_desc(sa + kk * kUK * 2),
+             b_is_mn(FORM) ? sw128_desc_mn(sb + kk * kUK * 128) : sw128_desc(sb + kk * kUK * 2), idesc,
+             !first || kk != 0);
+}
+
+template <int FORM>
+__device__ __forceinline__ uint32_t idesc_of(const Job &t) {
+  return idesc_bf16(kBM, t.ncols) | (a_is_mn(FORM) ? 1u << 15 : 0u) | (b_is_mn(FORM) ? 1u << 16 : 0u);
 }
 
 template <int FORM>
@@ -497,32 +558,8 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
           }
           const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA, fb = smem_addr(bar);
           mbar_arrive_expect_tx(bar, bytes);
-          if constexpr (FORM == kUp) {
-            tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
-            tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, fb);
-            tma_load_3d(sb + kFullBox, &maps.m[2], kb * kBK, t.n0, t.e, fb);
-          } else if constexpr (FORM == kDown) {
-            tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
-            tma_load_3d(sb, &maps.m[1], kb * kBK, t.n0, t.e, fb);
-            if (t.ncols > 128) tma_load_3d(sb + kFullBox, &maps.m[1], kb * kBK, t.n0 + 128, t.e, fb);
-          } else if constexpr (FORM == kDh) {
-            tma_load_2d(sa, &maps.m[0], kb * kBK, t.row0, fb);
-            for (int c = 0; c < t.ncols; c += 64)
-              tma_load_3d(sb + c / 64 * kHalfBox, &maps.m[1], t.n0 + c, kb * kBK, t.e, fb);
-          } else if constexpr (FORM == kDx) {
-            const int second = kb >= t.kblocks / 2 ? 1 : 0;
-            const int k = (kb - second * (t.kblocks / 2)) * kBK;
-            tma_load_2d(sa, &maps.m[second], k, t.row0, fb);
-            for (int c = 0; c < t.ncols; c += 64)
-              tma_load_3d(sb + c / 64 * kHalfBox, &maps.m[2 + second], t.n0 + c, k, t.e, fb);
-          } else {
-            // maps: dg, du, dy (A), x, h (B)
-            const int k = t.row0 + kb * kBK;
-            for (int c = 0; c < kBM; c += 64)
-              tma_load_2d(sa + c / 64 * kHalfBox, &maps.m[t.which], t.m0 + c, k, fb);
-            for (int c = 0; c < t.ncols; c += 64)
-              tma_load_2d(sb + c / 64 * kHalfBox, &maps.m[t.which == 2 ? 4 : 3], t.n0 + c, k, fb);
-          }
+          load_a<FORM>(maps, t, kb, sa, fb);
+          load_b<FORM>(maps, t, kb, sb, fb);
           ++it;
         }
       }
@@ -544,8 +581,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
       bool ok = true;
       for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++lt) {
         const Job t = job_of<FORM>(w, pref, offs, a);
-        const uint32_t idesc = idesc_bf16(kBM, t.ncols) | (a_is_mn(FORM) ? 1u << 15 : 0u) |
-                               (b_is_mn(FORM) ? 1u << 16 : 0u);
+        const uint32_t idesc = idesc_of<FORM>(t);
         const int buf = lt & 1;
         const uint32_t ph = (lt >> 1) & 1;
         if (!role_wait(tempty + buf, ph ^ 1u, abort, a.err)) break;
@@ -559,11 +595,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
           }
           tc_fence_after();
           const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA;
-#pragma unroll
-          for (int kk = 0; kk < kBK / kUK; ++kk)
-            mma_bf16(d, a_is_mn(FORM) ? sw128_desc_mn(sa + kk * kUK * 128) : sw128_desc(sa + kk * kUK * 2),
-                     b_is_mn(FORM) ? sw128_desc_mn(sb + kk * kUK * 128) : sw128_desc(sb + kk * kUK * 2), idesc,
-                     (kb | kk) != 0);
+          mma_block<FORM>(d, sa, sb, idesc, kb == 0);
           mma_commit(smem_addr(empty + s));
           ++it;
         }
@@ -641,6 +673,289 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Few tiles (short batches): a cluster of S CTAs shares a tile, each with its part of K, so that every SM streams
+// weights. The parts are added over the cluster: a tile is 8 slices (of 32 columns, or of 16 of g and the same 16 of
+// u), slice j is CTA j % S's, and every CTA puts its sums of a slice into the owner's shared memory, where the
+// stages were; the owner adds them in order and does what the form does with its columns.
+//   64 rows of one expert, 7168 -> 2048: 62 us with a CTA per tile (16 and 28 tiles).
+// ---------------------------------------------------------------------------
+constexpr int kMaxSplit = 8;
+constexpr int kSlices = 8;
+constexpr int kSliceBytes = kBM * 32 * 4;  // a slice's sums of one CTA: 32 columns of 128 rows
+constexpr int kTops = kSlices * 2 * kBM * 8;  // largest magnitudes (of g, u) of a row's 16 parts
+constexpr int kSmemSplit = kSmemFixed + kTops;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_index() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Slices that a CTA of a cluster of S owns at most, and whether their parts fit where the stages were.
+__host__ __device__ constexpr int slices_of(int S) { return (kSlices + S - 1) / S; }
+constexpr bool split_fits(int S) { return slices_of(S) * S * kSliceBytes <= kStages * kStage; }
+
+// 16 columns of a row (kUp: 8 of g, then 8 of u) whose sums are v.
+template <int FORM>
+__device__ __forceinline__ void finish16(const FfnArgs &a, const Job &t, int64_t p, int col, const uint32_t (&v)[16],
+                                         float g_top, float u_top) {
+  const bool wide = a.wide != 0;
+  const int left = a.n_total - t.n0 - col;
+  const int64_t at = p * a.n_total + t.n0 + col;
+  if (left <= 0) return;
+  if constexpr (FORM == kUp) {
+    uint32_t pk[4], pg[4], pu[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
+      const float u0 = __uint_as_float(v[8 + 2 * i]), u1 = __uint_as_float(v[9 + 2 * i]);
+      pk[i] = pack2(act_of<false>(g0, a.act, nullptr) * u0, act_of<false>(g1, a.act, nullptr) * u1);
+      pg[i] = pack2(g0, g1);
+      pu[i] = pack2(u0, u1);
+    }
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out0) + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    if (a.save == MOE_SAVE_BF16) {
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.keep_gate) + at) = make_uint4(pg[0], pg[1], pg[2], pg[3]);
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.keep_up) + at) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+    } else if (a.save == MOE_SAVE_FP8) {
+      const BlockScale gs = block_scale(g_top), us = block_scale(u_top);
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q[i] = static_cast<uint32_t>(e4m3x2_of_quotients(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), gs)) |
+               static_cast<uint32_t>(e4m3x2_of_quotients(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]), gs))
+                   << 16;
+        q[2 + i] =
+            static_cast<uint32_t>(e4m3x2_of_quotients(__uint_as_float(v[8 + 4 * i]), __uint_as_float(v[9 + 4 * i]), us)) |
+            static_cast<uint32_t>(e4m3x2_of_quotients(__uint_as_float(v[10 + 4 * i]), __uint_as_float(v[11 + 4 * i]), us))
+                << 16;
+      }
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.keep_gate) + at) = make_uint2(q[0], q[1]);
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.keep_up) + at) = make_uint2(q[2], q[3]);
+      if (col == 0) {
+        const int64_t sc = p * (a.I / kScaleBlock) + t.n0 / kScaleBlock;
+        a.keep_gate_scales[sc] = gs.s;
+        a.keep_up_scales[sc] = us.s;
+      }
+    }
+  } else if constexpr (FORM == kDh) {
+    uint32_t gq[8], uq[8], pd[8], pu[8], ph[8];
+    if (a.save == MOE_SAVE_FP8) {
+      const int64_t sc = p * (a.I / kScaleBlock) + (t.n0 + col) / kScaleBlock;
+      const uint4 g = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.gate) + at));
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.up) + at));
+      gq[0] = g.x, gq[1] = g.y, gq[2] = g.z, gq[3] = g.w;
+      uq[0] = u.x, uq[1] = u.y, uq[2] = u.z, uq[3] = u.w;
+      dh_of<true>(gq, uq, __ldg(a.gate_scales + sc), __ldg(a.up_scales + sc), v, a.act, pd, pu, ph);
+    } else {
+      load32<1>(static_cast<const uint16_t *>(a.gate) + at, gq, wide, left);
+      load32<1>(static_cast<const uint16_t *>(a.up) + at, uq, wide, left);
+      dh_of<false>(gq, uq, 1.0f, 1.0f, v, a.act, pd, pu, ph);
+    }
+    store32<1>(static_cast<__nv_bfloat16 *>(a.out0) + at, pd, wide, left);
+    store32<1>(static_cast<__nv_bfloat16 *>(a.out1) + at, pu, wide, left);
+    store32<1>(static_cast<__nv_bfloat16 *>(a.out2) + at, ph, wide, left);
+  } else {
+    uint32_t pk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pk[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    store32<1>(static_cast<__nv_bfloat16 *>(a.out0) + at, pk, wide, left);
+  }
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_split_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs a, int S) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
+  float2 *tops = reinterpret_cast<float2 *>(smem + kStages * kStage);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage + kTops);
+  uint64_t *empty = full + kStages;
+  uint64_t *done = empty + kStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int32_t *offs = reinterpret_cast<int32_t *>(tmem_slot + 2);
+  int32_t *pref = offs + (a.E + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(done, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (tid == 32)
+    for (int i = 0; i < 5; ++i) prefetch_tensormap(&maps.m[i]);
+  // The first kernel of a call reads nothing before its wait. The second one runs once the first has passed its own:
+  // offsets and weights are final then, and the rows alone are waited for.
+  if (a.first) grid_dependency_wait();
+  grid_dependents_launch();
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), kBN);
+    tmem_relinquish();
+  }
+  for (int e = tid; e <= a.E; e += kThreads) offs[e] = row_offset(a, e);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == 0) tile_prefix<kBM>(offs, pref, a, lane);
+  __syncthreads();
+  const int w = static_cast<int>(cluster_index());
+  const bool some = w < tile_total(pref, a);  // the same in the whole cluster
+  Job t{};
+  int kb0 = 0, kb1 = 0;
+  if (some) {
+    t = job_of<FORM>(w, pref, offs, a);
+    kb0 = t.kblocks * rank / S;
+    kb1 = t.kblocks * (rank + 1) / S;
+  }
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t bytes = kTileA + t.ncols * kBK * 2;
+      int early = kb0;  // K blocks whose weights have been asked for before the wait
+      if (!a.first) {
+        for (; early < kb1 && early < kb0 + kStages; ++early) {
+          const int s = early - kb0;
+          mbar_arrive_expect_tx(full + s, bytes);
+          load_b<FORM>(maps, t, early, smem_addr(smem + s * kStage) + kTileA, smem_addr(full + s));
+        }
+        grid_dependency_wait();
+      }
+      uint32_t it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+        const uint32_t sa = smem_addr(smem + s * kStage), fb = smem_addr(full + s);
+        if (kb >= early) {
+          if (!role_wait(empty + s, ph ^ 1u, abort, a.err)) break;
+          mbar_arrive_expect_tx(full + s, bytes);
+          load_b<FORM>(maps, t, kb, sa + kTileA, fb);
+        }
+        load_a<FORM>(maps, t, kb, sa, fb);
+      }
+      for (uint32_t s = 0; s < kStages && s < it; ++s) {
+        const uint32_t last = s + ((it - 1 - s) / kStages) * kStages;
+        mbar_wait_bounded(full + s, (last / kStages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      const uint32_t idesc = idesc_of<FORM>(t);
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+        if (!role_wait(full + s, ph, abort, a.err)) break;
+        tc_fence_after();
+        const uint32_t sa = smem_addr(smem + s * kStage);
+        mma_block<FORM>(tmem, sa, sa + kTileA, idesc, kb == kb0);
+        mma_commit(smem_addr(empty + s));
+      }
+      mma_commit(smem_addr(done));
+    }
+    __syncwarp();
+  }
+  if (!a.first && warp != 0) grid_dependency_wait();  // (what was kept, and this call's results, come after it)
+  if (!mbar_wait_bounded(done, 0)) latch_error(a.err, MOE_ETIMEOUT);
+  tc_fence_after();
+  // Every CTA's MMAs have read their stages: they take the sums from here on.
+  cluster_sync_all();
+  if (warp >= 2 && some) {
+    const int q = warp & 3, half = (warp - 2) >> 2, m = q * 32 + lane;
+    for (int i = half; i < kSlices / 2; i += 2) {
+      uint32_t r[64];
+      if (FORM == kUp)
+        tmem_load32x2_wait(tmem + (static_cast<uint32_t>(q * 32) << 16) + 32 * i,
+                           tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 + 32 * i, r);
+      else
+        tmem_load32x2_wait(tmem + (static_cast<uint32_t>(q * 32) << 16) + 64 * i,
+                           tmem + (static_cast<uint32_t>(q * 32) << 16) + 64 * i + 32, r);
+      if (m >= t.rows) continue;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = 2 * i + x;
+        const uint32_t to = map_rank(smem_addr(smem + ((j / S) * S + rank) * kSliceBytes + m * 128), j % S);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          // kUp: words 0-3: 16 of g, 4-7: the same of u
+          const int o = FORM == kUp ? (v < 4 ? 16 * x + 4 * v : 32 + 16 * x + 4 * (v - 4)) : 32 * x + 4 * v;
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((v ^ (m & 7)) << 4)),
+                       "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3])
+                       : "memory");
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kBN);
+  }
+  // a thread: a row, and half of each slice
+  const int m = tid & 127, part = (tid - 64) >> 7;
+  const int row = (m + 64) & 127;  // (threads 64 .. 319)
+  const bool mine = tid >= 64 && some && row < t.rows && !*abort;
+  const bool f8 = FORM == kUp && a.save == MOE_SAVE_FP8;
+  for (int pass = f8 ? 0 : 1; pass < 2; ++pass) {
+    for (int j = rank; j < kSlices && mine; j += S) {
+      uint32_t v[16];
+      float f[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+      for (int src = 0; src < S; ++src) {
+        const uint8_t *from = smem + ((j / S) * S + src) * kSliceBytes + row * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // kUp: 8 of g (words 2 part, 2 part + 1) and of u (4 + ..); else 16 columns
+          const int word = FORM == kUp ? (i < 2 ? 2 * part + i : 4 + 2 * part + i - 2) : 4 * part + i;
+          const float4 x = *reinterpret_cast<const float4 *>(from + ((word ^ (row & 7)) << 4));
+          f[4 * i] += x.x, f[4 * i + 1] += x.y, f[4 * i + 2] += x.z, f[4 * i + 3] += x.w;
+        }
+      }
+      if (f8 && pass == 0) {
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g = fmaxf(g, fabsf(f[i])), u = fmaxf(u, fabsf(f[8 + i]));
+        for (int to = 0; to < S; ++to)
+          asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                           map_rank(smem_addr(tops + (2 * j + part) * kBM + row), to)),
+                       "f"(g), "f"(u)
+                       : "memory");
+        continue;
+      }
+      float g = 0.0f, u = 0.0f;
+      if (f8)
+        for (int i = 0; i < 2 * kSlices; ++i) {
+          const float2 x = tops[i * kBM + row];
+          g = fmaxf(g, x.x), u = fmaxf(u, x.y);
+        }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(f[i]);
+      finish16<FORM>(a, t, t.row0 + row, FORM == kUp ? 16 * j + 8 * part : 32 * j + 16 * part, v, g, u);
+    }
+    if (pass == 0) cluster_sync_all();
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 // Map of a row-major bf16 [z][rows][cols] array (2-D when z = 0), boxes of 64 columns x box_rows rows.
@@ -679,6 +994,43 @@ int group_width(int concurrent, int tile_rows, int tile_cols, int ntiles_n) {
   return static_cast<int>(g < 1 ? 1 : (g > ntiles_n ? ntiles_n : g));
 }
 
+// Tiles of a launch, at most: an expert with rows has one that is not full.
+int64_t most_tiles(const FfnArgs &a) {
+  const int64_t experts = a.E < a.rows ? a.E : a.rows;
+  return ((a.rows - experts) / kBM + experts) * a.ntiles_n;
+}
+
+// CTAs that share a tile: as many as there are SMs for, with at least four K blocks each.
+int split_of(const FfnArgs &a, int sms) {
+  const int64_t tiles = most_tiles(a);
+  int S = static_cast<int>(sms / tiles < kMaxSplit ? sms / tiles : kMaxSplit);
+  if (S > a.kblocks / 4) S = a.kblocks / 4;
+  while (S > 1 && !split_fits(S)) --S;
+  return S;
+}
+
+template <int FORM>
+moe_status launch_split(const FfnMaps &maps, const FfnArgs &a, int S, cudaStream_t stream) {
+  const int smem = kSmemSplit + 12 * (a.E + 1);
+  if (!raise_smem_limit(ffn_split_kernel<FORM>, smem)) return MOE_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most_tiles(a) * S), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = MOE_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, ffn_split_kernel<FORM>, maps, a, S) != cudaSuccess) return MOE_ECUDA;
+  return launch_status();
+}
+
 template <int FORM>
 moe_status launch_form(const FfnMaps &maps, FfnArgs a, const FfnSizes &s, cudaStream_t stream) {
   const int all = sm_count();
@@ -696,7 +1048,11 @@ moe_status launch_form(const FfnMaps &maps, FfnArgs a, const FfnSizes &s, cudaSt
   } else {
     a.ntiles_n = (a.n_total + a.out_cols - 1) / a.out_cols;
     a.group_n = group_width(sms, kBM, kBN, a.ntiles_n);
-    tiles = (static_cast<int64_t>(a.rows) / kBM + a.E) * a.ntiles_n;
+    tiles = most_tiles(a);
+  }
+  if constexpr (FORM != kDw) {
+    const int S = split_of(a, sms);
+    if (S > 1 && kSmemSplit + 12 * (a.E + 1) <= kSmemMax) return launch_split<FORM>(maps, a, S, stream);
   }
   if (!raise_smem_limit(ffn_gemm_kernel<FORM>, smem)) return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
@@ -775,6 +1131,7 @@ extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_of
   a.n_total = s.I;
   a.out_cols = 128;
   a.wide = wide_rows(2 * s.I, {h, gate, up});
+  a.first = 1;
   st = launch_form<kUp>(m, a, s, cs);
   if (st != MOE_OK) return st;
   if (!ffn_map(&m.m[0], h, s.I, s.rows, 0, 128) || !ffn_map(&m.m[1], w_down, s.I, s.H, s.E, 128)) return MOE_ECUDA;
@@ -830,6 +1187,7 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
   a.n_total = s.I;
   a.out_cols = kBN;
   a.wide = wide_rows(2 * s.I, {gate, up, grad_gate, grad_up, h});
+  a.first = 1;
   st = launch_form<kDh>(m, a, s, cs);
   if (st != MOE_OK) return st;
 
