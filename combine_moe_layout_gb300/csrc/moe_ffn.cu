@@ -872,7 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
-  if (!a.first && warp != 0) grid_dependency_wait();  // (what was kept, and this call's results, come after it)
+  // (the results come after it; lane 0 of warp 0 has waited, the others of its warp and of every other have not)
+  if (!a.first) grid_dependency_wait();
   if (!mbar_wait_bounded(done, 0)) latch_error(a.err, MOE_ETIMEOUT);
   tc_fence_after();
   // Every CTA's MMAs have read their stages: they take the sums from here on.
@@ -891,12 +892,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int j = 2 * i + x;
-        const uint32_t to = map_rank(smem_addr(smem + ((j / S) * S + rank) * kSliceBytes + m * 128), j % S);
+        const uint32_t to = map_rank(smem_addr(smem + ((j / S) * S + rank) * kSliceBytes + m * 16), j % S);
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           // kUp: words 0-3: 16 of g, 4-7: the same of u
           const int o = FORM == kUp ? (v < 4 ? 16 * x + 4 * v : 32 + 16 * x + 4 * (v - 4)) : 32 * x + 4 * v;
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((v ^ (m & 7)) << 4)),
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + v * (kBM * 16)),
                        "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3])
                        : "memory");
         }
@@ -909,29 +910,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kBN);
   }
-  // a thread: a row, and half of each slice
-  const int m = tid & 127, part = (tid - 64) >> 7;
-  const int row = (m + 64) & 127;  // (threads 64 .. 319)
-  const bool mine = tid >= 64 && some && row < t.rows && !*abort;
+  // items: half a slice of a row, over as many threads as there are
   const bool f8 = FORM == kUp && a.save == MOE_SAVE_FP8;
+  const int own = some && !*abort ? (kSlices - rank + S - 1) / S : 0;
+  const int items = 2 * own * t.rows;
   for (int pass = f8 ? 0 : 1; pass < 2; ++pass) {
-    for (int j = rank; j < kSlices && mine; j += S) {
-      uint32_t v[16];
+    for (int item = tid; item < items; item += kThreads) {
+      const int row = item % t.rows, rest = item / t.rows, part = rest & 1, local = rest >> 1;
+      const int j = local * S + rank;
       float f[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) f[i] = 0.0f;
       for (int src = 0; src < S; ++src) {
-        const uint8_t *from = smem + ((j / S) * S + src) * kSliceBytes + row * 128;
+        const uint8_t *from = smem + (local * S + src) * kSliceBytes + row * 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // kUp: 8 of g (words 2 part, 2 part + 1) and of u (4 + ..); else 16 columns
           const int word = FORM == kUp ? (i < 2 ? 2 * part + i : 4 + 2 * part + i - 2) : 4 * part + i;
-          const float4 x = *reinterpret_cast<const float4 *>(from + ((word ^ (row & 7)) << 4));
+          const float4 x = *reinterpret_cast<const float4 *>(from + word * (kBM * 16));
           f[4 * i] += x.x, f[4 * i + 1] += x.y, f[4 * i + 2] += x.z, f[4 * i + 3] += x.w;
         }
       }
+      float g = 0.0f, u = 0.0f;
       if (f8 && pass == 0) {
-        float g = 0.0f, u = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) g = fmaxf(g, fabsf(f[i])), u = fmaxf(u, fabsf(f[8 + i]));
         for (int to = 0; to < S; ++to)
@@ -941,12 +942,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "memory");
         continue;
       }
-      float g = 0.0f, u = 0.0f;
-      if (f8)
+      if (f8) {
+#pragma unroll
         for (int i = 0; i < 2 * kSlices; ++i) {
           const float2 x = tops[i * kBM + row];
           g = fmaxf(g, x.x), u = fmaxf(u, x.y);
         }
+      }
+      uint32_t v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(f[i]);
       finish16<FORM>(a, t, t.row0 + row, FORM == kUp ? 16 * j + 8 * part : 32 * j + 16 * part, v, g, u);
