@@ -86,6 +86,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 struct FfnMaps {
   CUtensorMap m[5];  // operands
   CUtensorMap d[3];  // kDw: the results
+  CUtensorMap zeros[4];  // kDw: boxes of 1, 2, 4 and 8 lines, unswizzled
 };
 
 struct FfnArgs {
@@ -467,14 +468,16 @@ __device__ __forceinline__ void load_b(const FfnMaps &maps, const Job &t, int kb
   }
 }
 
-// The MMAs of one K block.
+// The MMAs of one K block; of an expert's last one (kDw) only the steps of 16 rows that hold one of its rows.
 template <int FORM>
-__device__ __forceinline__ void mma_block(uint32_t d, uint32_t sa, uint32_t sb, uint32_t idesc, bool first) {
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t sa, uint32_t sb, uint32_t idesc, bool first,
+                                          int steps = kBK / kUK) {
 #pragma unroll
   for (int kk = 0; kk < kBK / kUK; ++kk)
-    mma_bf16(d, a_is_mn(FORM) ? sw128_desc_mn(sa + kk * kUK * 128) : sw128_desc(sa + kk * kUK * 2),
-             b_is_mn(FORM) ? sw128_desc_mn(sb + kk * kUK * 128) : sw128_desc(sb + kk * kUK * 2), idesc,
-             !first || kk != 0);
+    if (FORM != kDw || kk < steps)
+      mma_bf16(d, a_is_mn(FORM) ? sw128_desc_mn(sa + kk * kUK * 128) : sw128_desc(sa + kk * kUK * 2),
+               b_is_mn(FORM) ? sw128_desc_mn(sb + kk * kUK * 128) : sw128_desc(sb + kk * kUK * 2), idesc,
+               !first || kk != 0);
 }
 
 template <int FORM>
@@ -566,10 +569,8 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
       // the last load issued into each stage lands before the CTA may exit
       for (uint32_t s = 0; s < kStages && s < it; ++s) {
         const uint32_t last = s + ((it - 1 - s) / kStages) * kStages;
-        if ((tails >> s) & 1u)
-          mbar_wait_bounded(landed + s, ((landings >> s) & 1u) ^ 1u);
-        else
-          mbar_wait_bounded(full + s, (last / kStages) & 1u);
+        if ((tails >> s) & 1u) mbar_wait_bounded(landed + s, ((landings >> s) & 1u) ^ 1u);
+        mbar_wait_bounded(full + s, (last / kStages) & 1u);
       }
     }
     __syncwarp();
@@ -595,7 +596,8 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
           }
           tc_fence_after();
           const uint32_t sa = smem_addr(smem + s * kStage), sb = sa + kTileA;
-          mma_block<FORM>(d, sa, sb, idesc, kb == 0);
+          mma_block<FORM>(d, sa, sb, idesc, kb == 0,
+                          t.tail != 0 && kb == t.kblocks - 1 ? (t.tail + kUK - 1) / kUK : kBK / kUK);
           mma_commit(smem_addr(empty + s));
           ++it;
         }
@@ -614,12 +616,12 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     for (int w = blockIdx.x; w < total; w += gridDim.x, ++lt) {
       const int buf = lt & 1;
       const uint32_t ph = (lt >> 1) & 1;
+      const Job t = job_of<FORM>(w, pref, offs, a);
       int ok = 0;
       if (lane == 0) ok = role_wait(tfull + buf, ph, abort, a.err) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const Job t = job_of<FORM>(w, pref, offs, a);
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBN;
       if constexpr (FORM == kUp)
         epilogue_up(a, t, tb, m, half);
@@ -638,31 +640,42 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     if (FORM == kDw && lane == 0) bulk_wait_all();
     __syncwarp();
   } else if constexpr (FORM == kDw) {
-    // ---- clears the rows of the last K block that are not the expert's (they may hold anything), in both
-    // operands: lines of 128 bytes, one for each k and 64 columns
-    uint32_t it = 0, landings = 0;
-    for (int w = blockIdx.x; w < total; w += gridDim.x) {
-      const Job t = job_of<FORM>(w, pref, offs, a);
-      it += t.kblocks;
-      if (t.tail == 0) continue;
-      // (a barrier of its own for each stage: the stage is not used again before this warp has passed it on, so that
-      // no phase is missed, and it is cleared while the MMAs of the blocks before it run)
-      const uint32_t s = (it - 1) % kStages;
-      int ok = 0;
-      if (lane == 0) ok = role_wait(landed + s, (landings >> s) & 1u, abort, a.err) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      landings ^= 1u << s;
-      uint8_t *box = smem + s * kStage;
-      const int boxes = kBM / 64 + t.ncols / 64;  // those of A, and those of B right behind them
-      const int words = (kBK - t.tail) * 8;       // 16-byte words of a box's cleared lines
-      for (int b = 0; b < boxes; ++b)
-        for (int i = lane; i < words; i += 32)
-          *reinterpret_cast<uint4 *>(box + b * kHalfBox + t.tail * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(full + s));
+    // ---- clears the rows of the last K block that are not the expert's (they may hold anything), up to the next
+    // multiple of 16, in both operands: lines of 128 bytes, one for each k and 64 columns. By TMA loads from behind the
+    // array's last row, which fill them with zeros and complete on the stage's barrier: written by the warp itself
+    // they needed a fence between the proxies, which took as long as two blocks (24576 rows of 64 experts, 383 each:
+    // 1153 us so) ----
+    if (lane == 0) {
+      uint32_t it = 0, landings = 0;
+      for (int w = blockIdx.x; w < total; w += gridDim.x) {
+        const Job t = job_of<FORM>(w, pref, offs, a);
+        it += t.kblocks;
+        if (t.tail == 0) continue;
+        // (a barrier of its own for each stage: the stage is not used again before this warp has passed it on, so
+        // that no phase is missed, and it is cleared while the MMAs of the blocks before it run)
+        const uint32_t s = (it - 1) % kStages;
+        if (!role_wait(landed + s, (landings >> s) & 1u, abort, a.err)) break;
+        landings ^= 1u << s;
+        const uint32_t box = smem_addr(smem + s * kStage) + t.tail * 128;
+        const int boxes = kBM / 64 + t.ncols / 64;  // those of A, and those of B right behind them
+        const int lines = -t.tail & (kUK - 1);
+        const uint32_t fb = smem_addr(full + s);
+        if (lines == 0) {
+          mbar_arrive(fb);
+          continue;
+        }
+        mbar_arrive_expect_tx(full + s, boxes * lines * 128);
+        for (int b = 0; b < boxes; ++b) {
+          uint32_t to = box + b * kHalfBox;
+          for (int i = 0; i < 4; ++i)  // 1, 2, 4, 8 lines
+            if ((lines >> i) & 1) {
+              tma_load_2d(to, &maps.zeros[i], 0, a.rows, fb);
+              to += 128u << i;
+            }
+        }
+      }
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -962,7 +975,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Host side.
 // ---------------------------------------------------------------------------
 // Map of a row-major bf16 [z][rows][cols] array (2-D when z = 0), boxes of 64 columns x box_rows rows.
-bool ffn_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t z, int box_rows) {
+bool ffn_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t z, int box_rows,
+             CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(z)};
@@ -970,7 +984,7 @@ bool ffn_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, z > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1211,6 +1225,8 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
       !ffn_map(&m.m[4], h, s.I, s.rows, 0, 64) || !ffn_map(&m.d[0], grad_w_gate, s.H, s.I, s.E, 32) ||
       !ffn_map(&m.d[1], grad_w_up, s.H, s.I, s.E, 32) || !ffn_map(&m.d[2], grad_w_down, s.I, s.H, s.E, 32))
     return MOE_ECUDA;
+  for (int i = 0; i < 4; ++i)
+    if (!ffn_map(&m.zeros[i], x, s.H, s.rows, 0, 1 << i, CU_TENSOR_MAP_SWIZZLE_NONE)) return MOE_ECUDA;
   a = base_args(s, region_offsets, err);
   return launch_form<kDw>(m, a, s, cs);
 }
