@@ -33,6 +33,7 @@
 // fp32 throughout.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -1017,25 +1018,10 @@ int64_t most_tiles(const FfnArgs &a) {
   return ((a.rows - experts) / kBM + experts) * a.ntiles_n;
 }
 
-// CTAs that share a tile: as many as there are SMs for, with at least four K blocks each.
-int split_of(const FfnArgs &a, int sms) {
-  const int64_t tiles = most_tiles(a);
-  int S = static_cast<int>(sms / tiles < kMaxSplit ? sms / tiles : kMaxSplit);
-  if (S > a.kblocks / 4) S = a.kblocks / 4;
-  while (S > 1 && !split_fits(S)) --S;
-  return S;
-}
-
-template <int FORM>
-moe_status launch_split(const FfnMaps &maps, const FfnArgs &a, int S, cudaStream_t stream) {
-  const int smem = kSmemSplit + 12 * (a.E + 1);
-  if (!raise_smem_limit(ffn_split_kernel<FORM>, smem)) return MOE_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(most_tiles(a) * S), 1, 1);
+void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int S, int smem, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = MOE_PDL;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -1044,6 +1030,49 @@ moe_status launch_split(const FfnMaps &maps, const FfnArgs &a, int S, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+}
+
+// Clusters of S CTAs that run at one time (a cluster stays within a GPC, so fewer than the SMs would hold), asked of
+// the device once.
+template <int FORM>
+int clusters_at_once(int S) {
+  static std::atomic<int> known[64][kMaxSplit + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed);
+  if (n != 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, S, kSmemMax, nullptr);
+  cfg.gridDim = dim3(S, 1, 1);
+  if (!raise_smem_limit(ffn_split_kernel<FORM>, kSmemMax) ||
+      cudaOccupancyMaxActiveClusters(&n, ffn_split_kernel<FORM>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();  // an answer, not a failed call
+    n = -1;
+  }
+  known[dev][S].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs that share a tile: as many as leave every cluster its place at once (with 16 tiles in clusters of 8 the last
+// two ran after the others, and 64 rows of 7168 -> 2048 took 40 us), with at least four K blocks each.
+template <int FORM>
+int split_of(const FfnArgs &a, int sms) {
+  const int64_t tiles = most_tiles(a);
+  int S = static_cast<int>(sms / tiles < kMaxSplit ? sms / tiles : kMaxSplit);
+  if (S > a.kblocks / 4) S = a.kblocks / 4;
+  while (S > 1 && !(split_fits(S) && tiles <= clusters_at_once<FORM>(S))) --S;
+  return S;
+}
+
+template <int FORM>
+moe_status launch_split(const FfnMaps &maps, const FfnArgs &a, int S, cudaStream_t stream) {
+  const int smem = kSmemSplit + 12 * (a.E + 1);
+  if (!raise_smem_limit(ffn_split_kernel<FORM>, smem)) return MOE_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, S, smem, stream);
+  cfg.gridDim = dim3(static_cast<unsigned>(most_tiles(a) * S), 1, 1);
   if (cudaLaunchKernelEx(&cfg, ffn_split_kernel<FORM>, maps, a, S) != cudaSuccess) return MOE_ECUDA;
   return launch_status();
 }
@@ -1068,7 +1097,7 @@ moe_status launch_form(const FfnMaps &maps, FfnArgs a, const FfnSizes &s, cudaSt
     tiles = most_tiles(a);
   }
   if constexpr (FORM != kDw) {
-    const int S = split_of(a, sms);
+    const int S = split_of<FORM>(a, sms);
     if (S > 1 && kSmemSplit + 12 * (a.E + 1) <= kSmemMax) return launch_split<FORM>(maps, a, S, stream);
   }
   if (!raise_smem_limit(ffn_gemm_kernel<FORM>, smem)) return MOE_ECUDA;
