@@ -520,7 +520,13 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
   }
   if (tid == 32)
     for (int i = 0; i < 5; ++i) prefetch_tensormap(&maps.m[i]);
-  grid_dependency_wait();
+  // The first kernel of a call reads nothing before its wait; the offsets are final once it has passed its own. The
+  // next one may begin early, on SMs that have run out of tiles.
+  constexpr bool kFirst = FORM == kUp || FORM == kDh;
+  if constexpr (kFirst) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+  }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -534,6 +540,10 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
   if constexpr (FORM != kDw) {
     if (warp == 0) tile_prefix<kBM>(offs, pref, a, lane);
     __syncthreads();
+  }
+  if constexpr (!kFirst) {
+    grid_dependency_wait();
+    if (FORM == kDx) grid_dependents_launch();
   }
   const int total = FORM == kDw ? a.dw_total : tile_total(pref, a);
 

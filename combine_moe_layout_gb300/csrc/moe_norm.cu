@@ -479,10 +479,13 @@ moe_status check_norm(const moe_norm_desc *d) {
 
 bool good16(const void *p) { return p != nullptr && aligned16(p); }
 
-// CTAs of a gradient, each with its part of the sums over rows: by the sizes alone, so that the sums are the same on
-// every device. One on each of 152 SMs where two rows fill much of the shared memory, else two.
+// CTAs on an SM: short rows leave a CTA few warps (4063 rows of 200: 22 us with two).
+int norm_ctas(int dim) { return dim > 4096 ? 1 : (dim > 1024 ? 2 : (dim > 256 ? 4 : 8)); }
+
+// CTAs of a gradient, each with its part of the sums over rows: by the sizes alone (152 SMs), so that the sums are the
+// same on every device.
 int norm_parts(const moe_norm_desc *d) {
-  const int most = d->dim > 4096 ? 152 : 304;
+  const int most = 152 * norm_ctas(d->dim);
   return d->rows < most ? d->rows : most;
 }
 
@@ -575,7 +578,8 @@ extern "C" moe_status moe_norm(const moe_norm_desc *desc, const void *x, const v
   a.eps = desc->eps;
   a.alpha = desc->alpha;
   a.err = err;
-  const NormShape s = norm_shape(a.H, static_cast<int64_t>(a.H) * ((desc->stream_fp32 ? 4 : 2) + (o != nullptr ? 2 : 0)), 2);
+  const NormShape s = norm_shape(a.H, static_cast<int64_t>(a.H) * ((desc->stream_fp32 ? 4 : 2) + (o != nullptr ? 2 : 0)),
+                                 norm_ctas(a.H) > 2 ? norm_ctas(a.H) : 2);
   const int room = sm_count() * s.ctas;
   return launch_norm_any<false>(desc->stream_fp32 != 0, a.rows < room ? a.rows : room, s, a,
                                 static_cast<cudaStream_t>(stream));
@@ -633,7 +637,7 @@ extern "C" moe_status moe_norm_grad(const moe_norm_desc *desc, const void *r, co
   const int64_t of_stream = desc->stream_fp32 ? 4 : 2;
   const int64_t row_bytes = a.H * (of_stream * (grad_r != nullptr ? 2 : 1) + (o != nullptr ? 4 : 2));
   const int grid = norm_parts(desc);
-  const NormShape s = norm_shape(a.H, row_bytes, grid > 152 ? 2 : 1);
+  const NormShape s = norm_shape(a.H, row_bytes, norm_ctas(a.H));
   const moe_status st = launch_norm_any<true>(desc->stream_fp32 != 0, grid, s, a, cs);
   if (st != MOE_OK) return st;
   NormSumArgs b{a.parts, w_post, gate, grad_w_pre, w_post != nullptr ? grad_w_post : nullptr,
