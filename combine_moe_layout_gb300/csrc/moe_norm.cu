@@ -76,28 +76,53 @@ __device__ __forceinline__ void store8(void *base, int64_t at, const float (&v)[
 
 __device__ __forceinline__ void vector8(const float *w, int64_t at, float (&v)[8]) { load8<true>(w, at, v); }
 
-// Sums over the block, every thread gets them; `part` is [2][N][32] floats, its halves taken in turn so that one
-// barrier does.
-template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float *part, int &turn) {
+// A sum over the block, every thread gets it; `part` is [2][32], its halves taken in turn so that one barrier does.
+__device__ __forceinline__ float block_sum(float v, float *part, int &turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (warps == 1) return;
-  float *mine = part + turn * N * 32;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps == 1) return v;
+  float *mine = part + turn * 32;
   turn ^= 1;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine[i * 32 + warp] = v[i];
+  if (lane == 0) mine[warp] = v;
   __syncthreads();
+  v = lane < warps ? mine[lane] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < warps ? mine[i * 32 + lane] : 0.0f;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The same for six sums of a row: each step of the butterfly sends half of the values that are left, so that nine
+// shuffles do (30 one by one), and eight more behind the barrier. `part` is [2][8][32].
+__device__ __forceinline__ void block_sums6(float (&v)[6], float *part, int &turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const bool b4 = (lane & 16) != 0, b3 = (lane & 8) != 0, b2 = (lane & 4) != 0;
+  // values 0-3 stay in the lower lanes, 4-7 (6 and 7: nothing) in the upper ones
+  float x[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int i = 0; i < 4; ++i) {
+    const float hi = i < 2 ? v[i + 4] : 0.0f;
+    x[i] = (b4 ? hi : v[i]) + __shfl_xor_sync(0xffffffffu, b4 ? v[i] : hi, 16);
+  }
+  float y[2];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int i = 0; i < 2; ++i) y[i] = (b3 ? x[i + 2] : x[i]) + __shfl_xor_sync(0xffffffffu, b3 ? x[i] : x[i + 2], 8);
+  float z = (b2 ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, b2 ? y[0] : y[1], 4);
+  z += __shfl_xor_sync(0xffffffffu, z, 2);
+  z += __shfl_xor_sync(0xffffffffu, z, 1);
+  // lanes 4 i .. 4 i + 3 have value i
+  if (warps > 1) {
+    float *mine = part + turn * 8 * 32;
+    turn ^= 1;
+    if ((lane & 3) == 0) mine[(lane >> 2) * 32 + warp] = z;
+    __syncthreads();
+    z = 0.0f;
+    for (int w = lane & 3; w < warps; w += 4) z += mine[(lane >> 2) * 32 + w];
+    z += __shfl_xor_sync(0xffffffffu, z, 2);
+    z += __shfl_xor_sync(0xffffffffu, z, 1);
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, z, 4 * i);
 }
 
 // Two fp32 operations in one instruction.
@@ -198,6 +223,33 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
   uint32_t phase = 0;
   const int vecs = a.H / 8;
   const float inv = 1.0f / static_cast<float>(a.H);
+  // the thread's columns: w_pre and c = w_post gate (of channels), kept where registers allow
+  constexpr bool kKeep = NV <= 2;
+  float w_kept[kKeep ? NV : 1][8], c_kept[kKeep ? NV : 1][8];
+  const bool scaled = a.w_post != nullptr || a.channel_gate;
+  auto columns = [&](int v, float (&c)[8]) {
+    if (a.w_post != nullptr) {
+      vector8(a.w_post, v * 8, c);
+      if (a.channel_gate) {
+        float g[8];
+        vector8(a.gate, v * 8, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] *= g[k];
+      }
+    } else {
+      vector8(a.gate, v * 8, c);
+    }
+  };
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < vecs) {
+        vector8(a.w_pre, v * 8, w_kept[i]);
+        if (scaled) columns(v, c_kept[i]);
+      }
+    }
+  }
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
     const void *px, *po;
     if constexpr (RING) {
@@ -212,7 +264,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
       px = static_cast<const uint8_t *>(a.x) + t * a.H * (F32 ? 4 : 2);
       po = static_cast<const uint8_t *>(a.o) + t * a.H * 2;
     }
-    float x[NV][8], b[NV][8], sum[1];
+    float x[NV][8], b[NV][8];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -231,24 +283,17 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
           if (threadIdx.x + i * blockDim.x < vecs)
 #pragma unroll
             for (int k = 0; k < 8; ++k) ss += b[i][k] * b[i][k];
-        sum[0] = ss;
-        block_sums<1>(sum, &part[0][0], turn);
-        scale *= 1.0f / sqrtf(sum[0] * inv + a.eps);
+        scale *= 1.0f / sqrtf(block_sum(ss, &part[0][0], turn) * inv + a.eps);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < vecs) {
-          float w[8];
-          if (a.w_post != nullptr) {
-            vector8(a.w_post, v * 8, w);
+          if (scaled) {
+            float c[8];
+            if constexpr (!kKeep) columns(v, c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) b[i][k] *= w[k];
-          }
-          if (a.channel_gate) {
-            vector8(a.gate, v * 8, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) b[i][k] *= w[k];
+            for (int k = 0; k < 8; ++k) b[i][k] *= kKeep ? c_kept[kKeep ? i : 0][k] : c[k];
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[i][k] += scale * b[i][k];
@@ -265,23 +310,22 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
         for (int k = 0; k < 8; ++k) ss += x[i][k] * x[i][k];
       }
     }
-    sum[0] = ss;
-    block_sums<1>(sum, &part[0][0], turn);
+    const float total = block_sum(ss, &part[0][0], turn);
     if constexpr (RING) {
       // every thread has read its part of the stage
       const int64_t next = t + static_cast<int64_t>(ring.stages) * gridDim.x;
       if (threadIdx.x == 0 && next < a.rows) ring.issue(stage, next);
       if (++stage == ring.stages) stage = 0, phase ^= 1u;
     }
-    const float q = 1.0f / sqrtf(sum[0] * inv + a.eps);
+    const float q = 1.0f / sqrtf(total * inv + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < vecs) {
         float w[8];
-        vector8(a.w_pre, v * 8, w);
+        if constexpr (!kKeep) vector8(a.w_pre, v * 8, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] *= q * w[k];
+        for (int k = 0; k < 8; ++k) x[i][k] *= q * (kKeep ? w_kept[kKeep ? i : 0][k] : w[k]);
         store8<false>(a.n, t * a.H + v * 8, x[i]);
       }
     }
@@ -290,7 +334,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
 
 template <int NV, bool F32, bool RING, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormArgs a) {
-  __shared__ float part[2][6][32];
+  __shared__ float part[2][8][32];
   extern __shared__ __align__(128) uint8_t smem[];
   RowRing ring;
   if constexpr (RING)
@@ -376,7 +420,7 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormArgs a) {
     float s[6];
 #pragma unroll
     for (int i = 0; i < 6; ++i) s[i] = s2[i].x + s2[i].y;
-    block_sums<6>(s, &part[0][0][0], turn);
+    block_sums6(s, &part[0][0][0], turn);
     if constexpr (RING) {
       // every thread has left the last row's stage
       if (threadIdx.x == 0 && waiting >= 0) ring.issue(left, waiting);
@@ -579,7 +623,7 @@ extern "C" moe_status moe_norm(const moe_norm_desc *desc, const void *x, const v
   a.alpha = desc->alpha;
   a.err = err;
   const NormShape s = norm_shape(a.H, static_cast<int64_t>(a.H) * ((desc->stream_fp32 ? 4 : 2) + (o != nullptr ? 2 : 0)),
-                                 norm_ctas(a.H) > 2 ? norm_ctas(a.H) : 2);
+                                 norm_ctas(a.H));
   const int room = sm_count() * s.ctas;
   return launch_norm_any<false>(desc->stream_fp32 != 0, a.rows < room ? a.rows : room, s, a,
                                 static_cast<cudaStream_t>(stream));
