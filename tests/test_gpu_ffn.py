@@ -342,3 +342,83 @@ def test_captured_and_replayed_beside_another_stream():
     for got, w in zip([c.y, c.gate, c.up, c.gx] + c.gw, want):
         assert torch.equal(got[:c.n] if got.shape[0] == c.rows else got, w[:c.n] if got.shape[0] == c.rows else w)
     assert B.moe_get_error(c.err) == B.MOE_OK
+
+
+def off_by_16_bytes(t):
+    """The same values in memory that begins on 16 bytes and not on 32."""
+    e = 16 // t.element_size()
+    room = torch.zeros(t.numel() + e, dtype=t.dtype, device=t.device)
+    v = room[e:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("n", [5, 40, 300, 3000])
+def test_matrices_that_begin_on_16_bytes(n):
+    c = Case([n, 20], 256, 384, save=B.MOE_SAVE_BF16)
+    for name in ("x", "w_gate", "w_up", "w_down", "h", "y", "gate", "up"):
+        setattr(c, name, off_by_16_bytes(getattr(c, name)))
+    c.forward()
+    c.check_forward()
+    c.keep_made()
+    c.backward()
+    for name in ("gate", "up", "grad_y", "hg", "gg", "gu", "gx"):
+        setattr(c, name, off_by_16_bytes(getattr(c, name)))
+    c.gw = [off_by_16_bytes(t) for t in c.gw]
+    c.backward(reuse=True)
+    c.check_backward()
+
+
+@pytest.mark.parametrize("save", [B.MOE_SAVE_BF16, B.MOE_SAVE_FP8])
+@pytest.mark.parametrize("counts,H,I", [([3000, 900], 512, 640), ([40] * 70, 256, 256)])
+def test_many_tiles(counts, H, I, save):
+    """More tiles than there are SMs: every CTA takes several."""
+    c = Case(counts, H, I, save=save, behind=5, seed=6)
+    c.forward()
+    c.check_forward()
+    c.keep_made()
+    c.backward()
+    c.check_backward()
+
+
+def test_two_calls_at_once_on_two_streams():
+    a = Case([70, 9, 130], 264, 200, save=B.MOE_SAVE_BF16, behind=2)
+    b = Case([500, 300], 512, 392, save=B.MOE_SAVE_BF16, seed=7)
+    for c in (a, b):
+        c.keep_made()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for c, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                c.backward()
+    torch.cuda.synchronize()
+    a.check_backward()
+    b.check_backward()
+
+
+def test_results_do_not_depend_on_timing():
+    c = Case([200, 37], 520, 392, save=B.MOE_SAVE_BF16)
+    c.keep_made()
+    first = None
+    for _ in range(3):
+        c.forward()
+        c.gate, c.up = c.gate.clone(), c.up.clone()
+        c.backward()
+        got = [c.y[:c.n].clone(), c.gx[:c.n].clone()] + [t.clone() for t in c.gw]
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(got, first))
+
+
+def test_the_first_call_of_a_size_in_a_capture():
+    """Limits and numbers that are asked of the device once may be asked while a stream is captured."""
+    c = Case([90], 1032, 264, save=B.MOE_SAVE_BF16, num_sms=90)
+    c.keep_made()
+    want = Case([90], 1032, 264, save=B.MOE_SAVE_BF16, num_sms=90)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        want.forward()
+    g.replay()
+    torch.cuda.synchronize()
+    want.check_forward()
