@@ -28,6 +28,12 @@
 // zeros, whatever the next expert's weights hold, and widths need only be
 // multiples of 8.
 //
+// Measured, among others: 24576 rows of 64 uneven experts, 4096 -> 1408, kept in 8
+// bits: forward 787 us (1.08 PFLOP/s; 665 with 384 rows each), gradients 1748 us;
+// 4096 rows, 4096 -> 14336: forward 860 us (1.68 PFLOP/s), gradients 2118 us. Bound
+// by the tensor cores under the power limit, less the rows that an expert's last
+// tile does not have, and in dw of short experts by its results' way out.
+//
 // What is rounded: h, dg and du to bf16 between two products (each is an operand
 // of bf16 tensor cores: 2^-9 of a term, as its output's own rounding), sums in
 // fp32 throughout.
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
 // weights. The parts are added over the cluster: a tile is 8 slices (of 32 columns, or of 16 of g and the same 16 of
 // u), slice j is CTA j % S's, and every CTA puts its sums of a slice into the owner's shared memory, where the
 // stages were; the owner adds them in order and does what the form does with its columns.
-//   64 rows of one expert, 7168 -> 2048: 62 us with a CTA per tile (16 and 28 tiles).
+//   64 rows of one expert, 7168 -> 2048: 28.8 us so, 62 with a CTA per tile (16 and 28 tiles).
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplit = 8;
 constexpr int kSlices = 8;

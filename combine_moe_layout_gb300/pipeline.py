@@ -302,7 +302,7 @@ class LocalMoe:
         if save not in SAVE:
             raise ValueError(f"LocalMoe: save is {save!r}, not None, 'bf16' or 'fp8'")
         with self._on(stream):
-            self._kept_now = save is not None
+            self._kept_now = False
             if save is not None:
                 if self.kept is None or self.kept.desc.save != SAVE[save]:
                     n, H = self.packed_x.shape
@@ -312,6 +312,7 @@ class LocalMoe:
                 k = self.kept
                 B.moe_ffn(k.desc, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up, weights.w_down,
                           self.h, self.packed_y, k.gate, k.gate_scales, k.up, k.up_scales, self.err)
+                self._kept_now = True
                 return
             B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate,
                                  weights.w_up, self.h, self.err)

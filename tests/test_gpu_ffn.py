@@ -281,6 +281,14 @@ def test_offsets_that_are_no_ranges_are_an_error_and_no_rows():
     assert bool((c.gx[30:] == 7.0).all()) and not any(t[1:].any() for t in c.gw)
 
 
+def test_offsets_that_are_no_ranges_of_few_rows():
+    c = Case([5, 4, 3], 128, 128)
+    c.offsets.copy_(torch.tensor([0, 5, 3, 1 << 20], dtype=torch.int32))
+    c.forward()
+    assert B.moe_get_error(c.err) == B.MOE_EINVAL
+    assert bool((c.y[5:] == 7.0).all()) and bool((c.y[:5] != 7.0).any())
+
+
 def test_no_rows():
     c = Case([0], 128, 128, save=B.MOE_SAVE_BF16)
     c.forward()
