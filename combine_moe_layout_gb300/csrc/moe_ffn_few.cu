@@ -15,9 +15,10 @@
 // before it waits for h.
 //
 // Measured (one call among others, weights from HBM) against tiles on the tensor
-// cores, whose 128 rows are then mostly empty: 7168 -> 2048 1 row 18.5 us against
-// 27, 16 rows 21 against 26; 4096 -> 14336 59.7 (5.9 TB/s) against 82, 63.6 against
-// 64.6; 2048 -> 1408 7.4 against 14, 8 against 14. Beyond 16 rows the tiles take over.
+// cores, whose 128 rows are then mostly empty: 7168 -> 2048 1 row 18.1 us against
+// 27, 16 rows 20.6 against 26; 4096 -> 14336 58.6 (6.0 TB/s) against 82, 64.7 against
+// 66.1; 2048 -> 1408 7.2 against 13, 8 against 13.5. Beyond 16 rows the tiles take
+// over.
 #include <cuda_bf16.h>
 
 #include "moe_ffn.cuh"
@@ -27,7 +28,6 @@ namespace {
 
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kUnroll = 4;  // chunks in flight
 
 struct FewArgs {
   const int32_t *offsets;
@@ -63,7 +63,7 @@ __device__ __forceinline__ uint4 load_weight(const __nv_bfloat16 *p) {
 
 // UP: linear 1; else linear 2. NT: tiles of 8 rows.
 template <bool UP, int NT>
-__global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const FewArgs a) {
   __shared__ float part[kFewWarps][NT * 4][32];
   __shared__ int first[kFewRows], expert_of[kFewRows], rows_of[kFewRows], active_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -71,7 +71,9 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const FewArgs a) {
 
   int e = 0, row0 = 0, nrows = a.rows, block = blockIdx.x;
   const bool dense = a.offsets == nullptr;
-  uint4 wa[kUnroll], wb[kUnroll];
+  // chunks in flight: each is asked for again as soon as its registers have been multiplied, two CTAs on an SM
+  constexpr int kUnroll = NT == 1 ? 7 : 4;
+  uint4 wa[kUnroll], wb[kUnroll], xa[kUnroll][NT];
   const __nv_bfloat16 *ra, *rb;
   bool la, lb;
   // the lane's two weight rows: columns block * 8 + lr of gate and up, or block * 16 + lr and + 8 of down
@@ -90,13 +92,20 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const FewArgs a) {
       rb = a.w0 + (static_cast<int64_t>(e) * a.N + (lb ? j + 8 : 0)) * a.K + lk;
     }
   };
-  auto fetch = [&](int c0) {
+  auto fetch = [&](int u, int chunk) {
+    const int k = chunk * 32;
+    const bool in = k + lk < a.K;
+    wa[u] = in && la ? load_weight(ra + k) : make_uint4(0, 0, 0, 0);
+    wb[u] = in && lb ? load_weight(rb + k) : make_uint4(0, 0, 0, 0);
+  };
+  auto fetch_rows = [&](int u, int chunk) {
+    const int k = chunk * 32 + lk;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int k = (c0 + u * kFewWarps) * 32;
-      const bool in = k + lk < a.K;
-      wa[u] = in && la ? load_weight(ra + k) : make_uint4(0, 0, 0, 0);
-      wb[u] = in && lb ? load_weight(rb + k) : make_uint4(0, 0, 0, 0);
+    for (int n = 0; n < NT; ++n) {
+      const int r = n * 8 + lr;
+      xa[u][n] = k < a.K && r < nrows
+                     ? *reinterpret_cast<const uint4 *>(a.in + static_cast<int64_t>(row0 + r) * a.K + k)
+                     : make_uint4(0, 0, 0, 0);
     }
   };
 
@@ -132,36 +141,27 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const FewArgs a) {
   }
   rows_at();
   const int chunks = (a.K + 31) / 32;
-  fetch(warp);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) fetch(u, warp + u * kFewWarps);
   if (!UP && dense) grid_dependency_wait();
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) fetch_rows(u, warp + u * kFewWarps);
 
   float c[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
   for (int c0 = warp; c0 < chunks; c0 += kUnroll * kFewWarps) {
-    uint4 xa[kUnroll][NT];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int k = (c0 + u * kFewWarps) * 32 + lk;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int r = n * 8 + lr;
-        xa[u][n] = k < a.K && r < nrows
-                       ? *reinterpret_cast<const uint4 *>(a.in + static_cast<int64_t>(row0 + r) * a.K + k)
-                       : make_uint4(0, 0, 0, 0);
+        mma16816(c[n], wa[u].x, wb[u].x, wa[u].y, wb[u].y, xa[u][n].x, xa[u][n].y);
+        mma16816(c[n], wa[u].z, wb[u].z, wa[u].w, wb[u].w, xa[u][n].z, xa[u][n].w);
       }
+      const int next = c0 + (kUnroll + u) * kFewWarps;
+      fetch(u, next);
+      fetch_rows(u, next);
     }
-    uint4 va[kUnroll], vb[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) va[u] = wa[u], vb[u] = wb[u];
-    if (c0 + kUnroll * kFewWarps < chunks) fetch(c0 + kUnroll * kFewWarps);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma16816(c[n], va[u].x, vb[u].x, va[u].y, vb[u].y, xa[u][n].x, xa[u][n].y);
-        mma16816(c[n], va[u].z, vb[u].z, va[u].w, vb[u].w, xa[u][n].z, xa[u][n].w);
-      }
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)
