@@ -181,6 +181,13 @@ struct RowRing {
   }
 };
 
+// After a copy that did not arrive: the error, and a wait (bounded too) for the copies of the other stages, so that
+// none lands in shared memory that is no longer this CTA's.
+__device__ __forceinline__ void give_up(const RowRing &r, int stage, uint32_t phase, int32_t *err) {
+  latch_error(err, MOE_ETIMEOUT);
+  for (int s = 0; s < r.stages; ++s) mbar_wait_bounded(r.full + s, s >= stage ? phase : phase ^ 1u);
+}
+
 __device__ __forceinline__ RowRing make_ring(const NormArgs &a, uint8_t *smem, int stages, const void *p0, bool f0,
                                              const void *p1, bool f1, const void *p2, bool f2, const void *p3,
                                              bool f3) {
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
     const void *px, *po;
     if constexpr (RING) {
       if (!mbar_wait_bounded(ring.full + stage, phase)) {
-        latch_error(a.err, MOE_ETIMEOUT);
+        give_up(ring, stage, phase, a.err);
         return;
       }
       const uint8_t *d = ring.data + static_cast<size_t>(stage) * ring.stage_bytes;
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormArgs a) {
     const void *pr, *pn, *pd, *po;
     if constexpr (RING) {
       if (!mbar_wait_bounded(ring.full + stage, phase)) {
-        latch_error(a.err, MOE_ETIMEOUT);
+        give_up(ring, stage, phase, a.err);
         return;
       }
       const uint8_t *d = ring.data + static_cast<size_t>(stage) * ring.stage_bytes;
