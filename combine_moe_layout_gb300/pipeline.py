@@ -234,7 +234,7 @@ class LocalMoe:
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.grad_y = self.grad_x = self.grad_weights = self.grad_logits = None  # allocated by the first backward
         self.kept = None  # what the last forward with ``save`` kept, for backward
-        self._kept_now = False  # the last forward was one
+        self._kept_now = False  # it was kept of the batch that the layer's buffers hold
         self.grad_gate = self.grad_up = self.grad_packed_x = None
         self.grad_w_gate = self.grad_w_up = self.grad_w_down = None  # by the first backward with the experts' weights
         self.u = None  # the last shared's scratch, its first part
@@ -274,50 +274,62 @@ class LocalMoe:
         _expect("logits", logits, torch.bfloat16 if self.opts.logits_bf16 else torch.float32, self.desc.tokens_per_rank,
                 self.desc.num_experts)
 
-    def route(self, logits, bias=None, stream=None):
+    def _expect_routing(self, logits, bias):
         self._expect_logits(logits)
         if bias is not None:
             _expect("bias", bias, torch.float32, self.desc.num_experts)
+
+    def route(self, logits, bias=None, stream=None):
+        self._expect_routing(logits, bias)
         with self._on(stream):
-            B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err)
+            self._route(logits, bias)
+
+    def _route(self, logits, bias):
+        self._kept_now = False  # what was kept belongs to the choices before these
+        B.moe_gate(self.desc, self.opts, logits, bias, self.topk_idx, self.topk_weights, self.err)
 
     def sort(self, x, stream=None):
         _expect("x", x, torch.bfloat16, *self.out.shape)
         with self._on(stream):
-            B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed,
-                       self.err)
+            self._sort(x)
 
-    def _expect_weights(self, weights):
+    def _sort(self, x):
+        self._kept_now = False
+        B.moe_sort(self.desc, self.topk_idx, x, None, self.region_offsets, self.packed_x, None, self.tok_packed, self.err)
+
+    def _expect_experts(self, weights, save):
         E, H, I = self.desc.num_experts, self.desc.hidden, self.inter
         if not I:
             raise ValueError("LocalMoe: a layer made with inter = 0 has no expert stage")
         _expect("w_gate", weights.w_gate, torch.bfloat16, E, I, H)
         _expect("w_up", weights.w_up, torch.bfloat16, E, I, H)
         _expect("w_down", weights.w_down, torch.bfloat16, E, H, I)
+        if save not in SAVE:
+            raise ValueError(f"LocalMoe: save is {save!r}, not None, 'bf16' or 'fp8'")
 
     def experts(self, weights, stream=None, save=None):
         """The expert stage on the sorted rows (weights: workloads.ExpertWeights). save: "bf16" or "fp8" keeps what
-        backward needs of it (kept)."""
-        self._expect_weights(weights)
-        if save not in SAVE:
-            raise ValueError(f"LocalMoe: save is {save!r}, not None, 'bf16' or 'fp8'")
+        backward needs of it (kept), until the next route, sort or experts."""
+        self._expect_experts(weights, save)
         with self._on(stream):
-            self._kept_now = False
-            if save is not None:
-                if self.kept is None or self.kept.desc.save != SAVE[save]:
-                    n, H = self.packed_x.shape
-                    desc = B.MoeFfnDesc(n, H, self.inter, self.desc.num_experts, 1, B.MOE_ACT_SILU, SAVE[save], 0)
-                    self.kept = _keep(desc, self.device)
-                    self._keep_for(self._streams.values())
-                k = self.kept
-                B.moe_ffn(k.desc, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up, weights.w_down,
-                          self.h, self.packed_y, k.gate, k.gate_scales, k.up, k.up_scales, self.err)
-                self._kept_now = True
-                return
-            B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate,
-                                 weights.w_up, self.h, self.err)
-            B.moe_expert_down(self.desc, self.inter, self.region_offsets, self.h, weights.w_down, self.packed_y,
-                              self.err)
+            self._experts(weights, save)
+
+    def _experts(self, weights, save):
+        self._kept_now = False
+        if save is not None:
+            if self.kept is None or self.kept.desc.save != SAVE[save]:
+                n, H = self.packed_x.shape
+                desc = B.MoeFfnDesc(n, H, self.inter, self.desc.num_experts, 1, B.MOE_ACT_SILU, SAVE[save], 0)
+                self.kept = _keep(desc, self.device)
+                self._keep_for(self._streams.values())
+            k = self.kept
+            B.moe_ffn(k.desc, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up, weights.w_down, self.h,
+                      self.packed_y, k.gate, k.gate_scales, k.up, k.up_scales, self.err)
+            self._kept_now = True
+            return
+        B.moe_expert_gate_up(self.desc, self.inter, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up,
+                             self.h, self.err)
+        B.moe_expert_down(self.desc, self.inter, self.region_offsets, self.h, weights.w_down, self.packed_y, self.err)
 
     def unsort(self, stream=None):
         with self._on(stream):
@@ -326,11 +338,16 @@ class LocalMoe:
 
     def forward(self, x, logits, weights, bias=None, stream=None, save=None):
         """x [tokens][hidden], logits [tokens][num_experts] -> the routed experts' output [tokens][hidden], a buffer of
-        the layer that the next forward writes again. save as in experts."""
-        self.route(logits, bias, stream)
-        self.sort(x, stream)
-        self.experts(weights, stream, save)
-        return self.unsort(stream)
+        the layer that the next forward writes again. save as in experts. What it refuses it refuses before its first
+        launch, with the last batch as it was."""
+        self._expect_routing(logits, bias)
+        _expect("x", x, torch.bfloat16, *self.out.shape)
+        self._expect_experts(weights, save)
+        with self._on(stream):
+            self._route(logits, bias)
+            self._sort(x)
+            self._experts(weights, save)
+            return self.unsort()
 
     def backward(self, grad_out, logits, expert_grad, stream=None):
         """The gradients of x and of the logits, in buffers of the layer that the next backward writes again.
@@ -343,7 +360,7 @@ class LocalMoe:
         self._expect_logits(logits)
         own = hasattr(expert_grad, "w_gate")
         if own:
-            self._expect_weights(expert_grad)
+            self._expect_experts(expert_grad, None)
             if not self._kept_now:
                 raise ValueError("LocalMoe: backward with the experts' weights follows a forward with save")
         with self._on(stream):
