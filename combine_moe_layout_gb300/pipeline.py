@@ -206,7 +206,8 @@ class LocalMoe:
     output back through moe_unsort_grad, the experts' gradient (moe_ffn_grad, from what a forward with ``save`` kept, or
     the caller's own), moe_sort_grad and moe_gate_grad. shared runs the projection beside the experts with the adapters
     of the batch's requests, dense a feed-forward block of all tokens, norm the norms around a block; their results are
-    new tensors. The buffers of forward and backward are allocated once.
+    new tensors. The buffers of forward and backward are allocated once, those of a ``save`` by the first forward with
+    it, and stay: a captured graph may be replayed after a forward that kept another format.
 
     Each method runs on ``stream`` (None: the current one) whole, what it does with torch and expert_grad included.
     The layer may have been made on another stream: the first call on a stream waits for that one's work up to then.
@@ -234,6 +235,7 @@ class LocalMoe:
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.grad_y = self.grad_x = self.grad_weights = self.grad_logits = None  # allocated by the first backward
         self.kept = None  # what the last forward with ``save`` kept, for backward
+        self._kept_by = {}  # by ``save``: a graph captured with one format writes to its buffers after a call with another
         self._kept_now = False  # it was kept of the batch that the layer's buffers hold
         self.grad_gate = self.grad_up = self.grad_packed_x = None
         self.grad_w_gate = self.grad_w_up = self.grad_w_down = None  # by the first backward with the experts' weights
@@ -264,7 +266,7 @@ class LocalMoe:
 
     def _keep_for(self, streams):
         """The layer's buffers are given out again, after the layer, only when these streams have passed them."""
-        kept = vars(self.kept).values() if self.kept is not None else ()
+        kept = (t for k in self._kept_by.values() for t in vars(k).values())
         for t in (*vars(self).values(), *kept):
             if isinstance(t, torch.Tensor):
                 for s in streams:
@@ -317,12 +319,12 @@ class LocalMoe:
     def _experts(self, weights, save):
         self._kept_now = False
         if save is not None:
-            if self.kept is None or self.kept.desc.save != SAVE[save]:
+            if save not in self._kept_by:
                 n, H = self.packed_x.shape
                 desc = B.MoeFfnDesc(n, H, self.inter, self.desc.num_experts, 1, B.MOE_ACT_SILU, SAVE[save], 0)
-                self.kept = _keep(desc, self.device)
+                self._kept_by[save] = _keep(desc, self.device)
                 self._keep_for(self._streams.values())
-            k = self.kept
+            self.kept = k = self._kept_by[save]
             B.moe_ffn(k.desc, self.region_offsets, self.packed_x, weights.w_gate, weights.w_up, weights.w_down, self.h,
                       self.packed_y, k.gate, k.gate_scales, k.up, k.up_scales, self.err)
             self._kept_now = True

@@ -88,3 +88,29 @@ def test_a_call_that_fails_on_its_way_leaves_nothing_kept(calls, monkeypatch, fa
     with pytest.raises(B.MoeError):
         m.forward(X, LOGITS, Weights(), save="bf16")
     refused_backward(m, calls)
+
+
+def test_each_format_keeps_its_buffers(calls):
+    """A captured forward writes to the addresses of its capture at every replay, whatever a call between them kept."""
+    m = layer()
+    held = {}
+    for save in ("fp8", "bf16", "fp8", "bf16"):
+        m.forward(X, LOGITS, Weights(), save=save)
+        assert m.kept.desc.save == P.SAVE[save]
+        now = [t.data_ptr() for t in (m.kept.gate, m.kept.up, m.kept.gate_scales, m.kept.up_scales) if t is not None]
+        assert held.setdefault(save, (m.kept, now)) == (m.kept, now)
+        m.forward(X, LOGITS, Weights())  # nor one that keeps nothing
+    assert len({p for _, now in held.values() for p in now}) == 6
+
+
+def test_every_formats_buffers_stay_for_a_stream(calls, monkeypatch):
+    """They are given out again, after the layer, only when every stream that used it has passed them."""
+    m = layer()
+    for save in ("fp8", "bf16"):
+        m.forward(X, LOGITS, Weights(), save=save)
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append(t.data_ptr()))
+    m._keep_for([None])
+    for k in m._kept_by.values():
+        for t in (k.gate, k.up, k.gate_scales, k.up_scales):
+            assert t is None or t.data_ptr() in seen
