@@ -354,13 +354,14 @@ class LocalMoe:
     def backward(self, grad_out, logits, expert_grad, stream=None):
         """The gradients of x and of the logits, in buffers of the layer that the next backward writes again.
         expert_grad: the experts' weights, after a forward with ``save``, which leaves the weights' gradients in
-        grad_w_gate, grad_w_up and grad_w_down, buffers of the layer too. Or a function of the caller's,
-        expert_grad(packed_x, region_offsets, grad_y): from the gradient of packed_y to that of packed_x, row by row,
-        both bf16 [tokens * topk][hidden]. It is called with ``stream`` as the current one. Rows at or above
-        region_offsets' last entry belong to no choice: packed_x and grad_y hold nothing of this batch there."""
+        grad_w_gate, grad_w_up and grad_w_down, buffers of the layer too. Or a function of the caller's (whatever can be
+        called, a module that holds weights among them), expert_grad(packed_x, region_offsets, grad_y): from the
+        gradient of packed_y to that of packed_x, row by row, both bf16 [tokens * topk][hidden]. It is called with
+        ``stream`` as the current one. Rows at or above region_offsets' last entry belong to no choice: packed_x and
+        grad_y hold nothing of this batch there."""
         _expect("grad_out", grad_out, torch.bfloat16, *self.out.shape)
         self._expect_logits(logits)
-        own = hasattr(expert_grad, "w_gate")
+        own = hasattr(expert_grad, "w_gate") and not callable(expert_grad)
         if own:
             self._expect_experts(expert_grad, None)
             if not self._kept_now:

@@ -114,3 +114,26 @@ def test_every_formats_buffers_stay_for_a_stream(calls, monkeypatch):
     for k in m._kept_by.values():
         for t in (k.gate, k.up, k.gate_scales, k.up_scales):
             assert t is None or t.data_ptr() in seen
+
+
+class Experts(torch.nn.Module):
+    """The caller's own experts, which hold their weights and give their gradient when they are called."""
+
+    def __init__(self):
+        super().__init__()
+        self.w_gate, self.w_up, self.w_down = (torch.nn.Parameter(t) for t in vars(Weights()).values())
+        self.asked = 0
+
+    def forward(self, packed_x, region_offsets, grad_y):
+        self.asked += 1
+        return grad_y
+
+
+@pytest.mark.parametrize("save", [None, "bf16"])
+def test_what_can_be_called_is_called_whatever_it_holds(calls, save):
+    m, own = layer(), Experts()
+    m.forward(X, LOGITS, Weights(), save=save)
+    calls.clear()
+    m.backward(X, LOGITS, own)
+    assert own.asked == 1 and calls == ["moe_unsort_grad", "moe_sort_grad", "moe_gate_grad"]
+    assert m.grad_w_gate is None
