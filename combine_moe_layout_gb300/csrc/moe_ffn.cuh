@@ -29,7 +29,8 @@ __device__ __forceinline__ float act_of(float g, int act, float *da) {
   if (act != MOE_ACT_SILU) {
     constexpr float k = 1.5957691216057308f, c = 0.044715f;  // 2 sqrt(2 / pi)
     v = k * (g + c * g * g * g);
-    if constexpr (GRAD) dv = k * (1.0f + 3.0f * c * g * g);
+    // (p (1 - p) is 0 long before g^2 overflows, and would make the derivative NaN with it)
+    if constexpr (GRAD) dv = k * (1.0f + 3.0f * c * fminf(g * g, 1e30f));
   }
   const float p = sigmoid(v);
   if constexpr (GRAD) *da = p + g * p * (1.0f - p) * dv;
