@@ -100,10 +100,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 }
 
 // Bounded wait for phase `parity` of an mbarrier; false after giving up.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity, uint64_t limit = kMbarWaitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (global_timer_ns() - t0 < kMbarWaitNs)
+  while (global_timer_ns() - t0 < limit)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }

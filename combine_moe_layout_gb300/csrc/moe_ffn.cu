@@ -68,6 +68,11 @@ constexpr int kPiece = 32 * 64 * 2;  // kDw: 32 rows x 64 columns of the result,
 constexpr int kSmemDw = kSmemFixed + kEpilogueWarps * kPiece;
 static_assert(kSmemDw <= kSmemMax, "");
 
+// A wait for something that comes after n K blocks (a whole tile's, or those of every tile up to the next one with a
+// tail) allows for each of them 10 us, ten times what one takes when its operands come from HBM: a weight's gradient over
+// 2^27 rows has two million blocks in a tile and takes longer than a wait for one copy may.
+__device__ __forceinline__ uint64_t blocks_ns(uint32_t n) { return kMbarWaitNs + n * 10000ull; }
+
 enum Form { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
 
 __host__ __device__ constexpr bool a_is_mn(int form) { return form == kDw; }
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
       const uint32_t ph = (lt >> 1) & 1;
       const Job t = job_of<FORM>(w, pref, offs, a);
       int ok = 0;
-      if (lane == 0) ok = role_wait(tfull + buf, ph, abort, a.err) ? 1 : 0;
+      if (lane == 0) ok = role_wait(tfull + buf, ph, abort, a.err, blocks_ns(t.kblocks)) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
     // they needed a fence between the proxies, which took as long as two blocks (24576 rows of 64 experts, 383 each:
     // 1153 us so) ----
     if (lane == 0) {
-      uint32_t it = 0, landings = 0;
+      uint32_t it = 0, landings = 0, seen = 0;  // seen: blocks up to the last wait
       for (int w = blockIdx.x; w < total; w += gridDim.x) {
         const Job t = job_of<FORM>(w, pref, offs, a);
         it += t.kblocks;
@@ -671,7 +676,8 @@ __global__ void __launch_bounds__(FORM == kDw ? kThreadsDw : kThreads, 1)
         // (a barrier of its own for each stage: the stage is not used again before this warp has passed it on, so
         // that no phase is missed, and it is cleared while the MMAs of the blocks before it run)
         const uint32_t s = (it - 1) % kStages;
-        if (!role_wait(landed + s, (landings >> s) & 1u, abort, a.err)) break;
+        if (!role_wait(landed + s, (landings >> s) & 1u, abort, a.err, blocks_ns(it - seen))) break;
+        seen = it;
         landings ^= 1u << s;
         const uint32_t box = smem_addr(smem + s * kStage) + t.tail * 128;
         const int boxes = kBM / 64 + t.ncols / 64;  // those of A, and those of B right behind them
@@ -904,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // (the results come after it; lane 0 of warp 0 has waited, the others of its warp and of every other have not)
   if (!a.first) grid_dependency_wait();
-  if (!mbar_wait_bounded(done, 0)) latch_error(a.err, MOE_ETIMEOUT);
+  if (!mbar_wait_bounded(done, 0, blocks_ns(kb1 - kb0))) latch_error(a.err, MOE_ETIMEOUT);
   tc_fence_after();
   // Every CTA's MMAs have read their stages: they take the sums from here on.
   cluster_sync_all();

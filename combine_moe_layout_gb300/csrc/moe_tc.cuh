@@ -128,13 +128,14 @@ __device__ __forceinline__ void tmem_load32x2_wait(uint32_t taddr0, uint32_t tad
 
 // Bounded wait on an mbarrier phase that also gives up as soon as another role
 // of the CTA has aborted; a timeout records MOE_ETIMEOUT and aborts the CTA.
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *err) {
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *err,
+                                          uint64_t limit = kMbarWaitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (global_timer_ns() - t0 > kMbarWaitNs) {
+    if (global_timer_ns() - t0 > limit) {
       *abort = 1;
       latch_error(err, MOE_ETIMEOUT);
       return false;
