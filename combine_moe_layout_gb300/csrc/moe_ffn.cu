@@ -1020,7 +1020,9 @@ moe_status check_ffn(const moe_ffn_desc *d, FfnSizes *s) {
   if (d->act != MOE_ACT_SILU && d->act != MOE_ACT_GELU_TANH) return MOE_EINVAL;
   if (d->save != MOE_SAVE_NONE && d->save != MOE_SAVE_BF16 && d->save != MOE_SAVE_FP8) return MOE_EINVAL;
   if (d->save == MOE_SAVE_FP8 && d->inter % kScaleBlock != 0) return MOE_EINVAL;
-  // tiles are counted in 32 bits
+  // rows, columns and tiles are counted in 32 bits, those of a last tile that are not there among them
+  constexpr int32_t most = INT32_MAX - kBN + 1;
+  if (d->rows > most || d->hidden > most || d->inter > most) return MOE_EINVAL;
   const int64_t wide = (d->hidden > d->inter ? d->hidden : d->inter) / 64 + 1;
   if ((d->rows / kBM + static_cast<int64_t>(d->num_experts)) * wide > INT32_MAX ||
       3 * d->num_experts * (static_cast<int64_t>(d->hidden) / 64 + 1) * (d->inter / 64 + 1) > INT32_MAX)
@@ -1204,7 +1206,7 @@ extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_of
   a.kblocks = blocks_of(s.H);
   a.n_total = s.I;
   a.out_cols = 128;
-  a.wide = wide_rows(2 * s.I, {h, gate, up});
+  a.wide = wide_rows(INT64_C(2) * s.I, {h, gate, up});
   a.first = 1;
   st = launch_form<kUp>(m, a, s, cs);
   if (st != MOE_OK) return st;
@@ -1214,7 +1216,7 @@ extern "C" moe_status moe_ffn(const moe_ffn_desc *desc, const int32_t *region_of
   a.kblocks = blocks_of(s.I);
   a.n_total = s.H;
   a.out_cols = kBN;
-  a.wide = wide_rows(2 * s.H, {y});
+  a.wide = wide_rows(INT64_C(2) * s.H, {y});
   return launch_form<kDown>(m, a, s, cs);
 }
 
@@ -1260,7 +1262,7 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
   a.kblocks = blocks_of(s.H);
   a.n_total = s.I;
   a.out_cols = kBN;
-  a.wide = wide_rows(2 * s.I, {gate, up, grad_gate, grad_up, h});
+  a.wide = wide_rows(INT64_C(2) * s.I, {gate, up, grad_gate, grad_up, h});
   a.first = 1;
   st = launch_form<kDh>(m, a, s, cs);
   if (st != MOE_OK) return st;
@@ -1273,7 +1275,7 @@ extern "C" moe_status moe_ffn_grad(const moe_ffn_desc *desc, const int32_t *regi
   a.kblocks = 2 * blocks_of(s.I);
   a.n_total = s.H;
   a.out_cols = kBN;
-  a.wide = wide_rows(2 * s.H, {grad_x});
+  a.wide = wide_rows(INT64_C(2) * s.H, {grad_x});
   st = launch_form<kDx>(m, a, s, cs);
   if (st != MOE_OK || !weights) return st;
 

@@ -542,9 +542,9 @@ typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 } moe_act;
 typedef enum { MOE_SAVE_NONE = 0, MOE_SAVE_BF16 = 1, MOE_SAVE_FP8 = 2 } moe_save;
 
 typedef struct {
-  int32_t rows;        /* rows of x: at least region_offsets' last entry; >= 0 */
-  int32_t hidden;      /* H, a multiple of 8 */
-  int32_t inter;       /* I, a multiple of 8; of 128 with MOE_SAVE_FP8 */
+  int32_t rows;        /* rows of x: at least region_offsets' last entry; 0 .. 2^31 - 256 */
+  int32_t hidden;      /* H, a multiple of 8; at most 2^31 - 256 */
+  int32_t inter;       /* I, a multiple of 8 (of 128 with MOE_SAVE_FP8); at most 2^31 - 256 */
   int32_t num_experts; /* E, 1 .. MOE_FFN_MAX_EXPERTS */
   int32_t num_ranks;   /* R: region_offsets has E*R + 1 entries, expert e's rows begin at entry e*R; >= 1 */
   int32_t act;         /* moe_act */
