@@ -32,3 +32,32 @@ def test_a_graph_outlives_a_forward_with_another_format(first, other):
         assert all(bool((t == 3).all()) for t in room)
         s.backward(s.forward(other)[0])
     assert s.layer.error() == B.MOE_OK
+
+
+@pytest.mark.parametrize("save", ["fp8", "bf16"])
+def test_a_first_step_in_a_capture(save):
+    """What the layer keeps and the gradients' buffers are allocated in the capture, and used outside of it too, also
+    when the graph is gone."""
+    s, ref = Step(T=70), Step(T=70)
+    want = {k: v.clone() for k, v in ref.backward(ref.forward(save)[0]).items()}
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = s.backward(s.forward(save)[0])
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        for name, w in want.items():
+            assert torch.equal(got[name], w), name
+        eager = s.backward(s.forward(save)[0])
+        for name, w in want.items():
+            assert torch.equal(eager[name], w), name
+    torch.cuda.synchronize()
+    del g, got
+    torch.cuda.empty_cache()
+    room = [torch.full((1 << 20,), 3, dtype=torch.uint8, device="cuda") for _ in range(32)]
+    eager = s.backward(s.forward(save)[0])
+    for name, w in want.items():
+        assert torch.equal(eager[name], w), name
+    assert all(bool((t == 3).all()) for t in room)
+    assert s.layer.error() == B.MOE_OK
