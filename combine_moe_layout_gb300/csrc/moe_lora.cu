@@ -10,11 +10,11 @@
 // writing only the accumulator rows of the tokens that use it (the MMA's
 // disable-output-lane mask, so no adapter's value, not even a NaN, reaches
 // another request's row). y is rounded once. u is rounded to bf16 too, which is what
-// the tensor cores take: up to 2^-9 of each u_i b_i, which is more than rounding y
+// the tensor cores take: up to 2^-8 of each u_i b_i, which is more than rounding y
 // costs where these cancel. Over ten shapes the error of y against 64 bits
 // (relative, over the whole matrix) is 1.70e-3 to 2.35e-3, where y's rounding alone
 // leaves 1.63e-3 to 1.68e-3. A call may ask for u in two parts, its rounding and the
-// rounding of what that left (2^-18 of u), which meet the same B_a one after the
+// rounding of what that left (2^-17 of u), which meet the same B_a one after the
 // other, with the error of y's rounding alone (1.63e-3 to 1.70e-3). That takes
 // 9.8 us for 9.7 (one token, 4096 -> 4096, rank 16), 17.3 for 15.5 (64 tokens, 7168
 // -> 2048, 32 adapters), 22.2 for 20.7 (389 tokens, 2056 -> 4104) and 191 for 179

@@ -399,7 +399,7 @@ class LocalMoe:
         [tokens][in] and w [out][in] bf16, lora_a [A][rank][in] and lora_b [A][out][rank] bf16, scales [A] float32 or
         None, adapter [tokens] int32. The result is the caller's own: it and the scratch u are new in each call, so
         that two projections, on one stream or on two, share nothing. u_parts: u = x lora_a^T as two bf16 parts, or as
-        one, which takes up to a tenth less time and leaves 2^-9 of u."""
+        one, which takes up to a tenth less time and leaves up to 2^-8 of u."""
         bf16 = torch.bfloat16
         if u_parts not in (1, 2):
             raise ValueError(f"LocalMoe: u_parts is {u_parts!r}, not 1 or 2")
