@@ -18,7 +18,8 @@ moe_status launch_ffn_few(const FfnSizes &s, const int32_t *offsets, const void 
 namespace {
 
 // 1 / (1 + exp(-v)), to a few units in the last place (2^-20 of it where |v| is below 10): what it goes into is
-// rounded to bf16. 0 and 1 at the ends.
+// rounded to bf16. 0 and 1 at the ends. With expf and a division that rounds, 333 rows of 12 experts take 23.6 us for
+// 22.7 and their gradients 46.5 for 45.2, 64 rows of 7168 -> 2048 29.4 for 28.8, 24576 rows 792 for 789.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
 // act(g) and act'(g), in fp32. The second act, g (1 + tanh(z)) / 2 with z = sqrt(2/pi) (g + 0.044715 g^3), is

@@ -11,14 +11,17 @@
 // a row of x; which k a lane's registers stand for is the same permutation on both
 // sides, so that the product is that of the formula.
 //
-// Linear 2 is released as soon as linear 1 has begun and fetches its first weights
-// before it waits for h.
+// Linear 2 is released as soon as linear 1 has begun. In a dense block it fetches its
+// first weights before it waits for h; with offsets it waits first (which experts
+// have rows it reads from them).
 //
 // Measured (one call among others, weights from HBM) against tiles on the tensor
 // cores, whose 128 rows are then mostly empty: 7168 -> 2048 1 row 18.1 us against
 // 27, 16 rows 20.6 against 26; 4096 -> 14336 58.6 (6.0 TB/s) against 82, 64.7 against
-// 66.1; 2048 -> 1408 7.2 against 13, 8 against 13.5. Beyond 16 rows the tiles take
-// over.
+// 66.1; 2048 -> 1408 7.2 against 13, 8 against 13.5. Rows of 64 experts, 4096 -> 1408:
+// 1 row 12.7 us against 18.4, 4 rows 31.4 against 34.9, 8 rows 60.2 against 65.7, 16
+// rows 111 against 91 (each expert that has a row takes its own CTAs, which nearly all
+// have one row). Beyond 16 rows the tiles take over.
 #include <cuda_bf16.h>
 
 #include "moe_ffn.cuh"

@@ -13,12 +13,14 @@
 // mean(t o) is linear in dr, so that it follows from sums over grad_r, dn w_pre and r
 // alone: a row's six sums are taken together and cost one barrier.
 //
-// Every row is read and written once. 8192 rows of 7168: forward 117 us (fp32
-// stream, 89 % of the copy rate), gradients 138 us (bf16, 76 %: a row's chain and
-// its instructions). All
-// arithmetic and sums are in fp32; a column's sum over rows is taken by each CTA
-// for its own rows in order, and the CTAs' parts are then added in order, so that
-// results do not depend on timing.
+// Every row is read and written once. 8192 rows of 7168: forward 118 us (fp32
+// stream, 88 % of the copy rate), gradients 138 us (bf16, 76 %: a row's chain and
+// its instructions). Rows above 8192 columns have four vectors to a thread, and the
+// gradient's column sums no longer fit its registers: 2048 rows of 16384 in bf16 take
+// 77 us (3.5 TB/s) and 174 us (2.3 TB/s), of 32768 (1024 threads, straight from
+// memory) 184 us and 622 us (1.3 TB/s). All arithmetic and sums are in fp32; a
+// column's sum over rows is taken by each CTA for its own rows in order, and the CTAs'
+// parts are then added in order, so that results do not depend on timing.
 #include <cuda_bf16.h>
 
 #include "moe_common.cuh"
@@ -532,7 +534,8 @@ moe_status check_norm(const moe_norm_desc *d) {
 
 bool good16(const void *p) { return p != nullptr && aligned16(p); }
 
-// CTAs on an SM: short rows leave a CTA few warps (4063 rows of 200: 22 us with two).
+// CTAs on an SM: short rows leave a CTA few warps (4063 rows of 200: forward 5.8 us, 16.5 with two; gradients 15.0 and
+// 19.5).
 int norm_ctas(int dim) { return dim > 4096 ? 1 : (dim > 1024 ? 2 : (dim > 256 ? 4 : 8)); }
 
 // CTAs of a gradient, each with its part of the sums over rows: by the sizes alone (152 SMs), so that the sums are the

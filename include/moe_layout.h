@@ -506,7 +506,7 @@ typedef struct {
  *   u[t] = bf16_rne( scales[a] * x[t] lora_a[a]^T ),
  *   y[t] = bf16_rne( x[t] w^T + u[t] lora_b[a]^T ),
  * or, with u_parts = 2, u[t] and u'[t] = bf16_rne( scales[a] * x[t] lora_a[a]^T - u[t] ) and the sum of both with
- * lora_b[a]^T (u' is 0 where u is not finite), so that rounding u leaves 2^-18 of it instead of 2^-9;
+ * lora_b[a]^T (u' is 0 where u is not finite), so that rounding u leaves 2^-17 of it instead of 2^-8;
  * products in bf16 accumulated in fp32 on the tensor cores; adapter -1 has no
  * second term. Adapters of a smaller rank are padded with zero rows of lora_a or
  * zero columns of lora_b. The adapters may be in any order over the tokens; a
@@ -555,7 +555,8 @@ typedef struct {
 /* For every packed row p of expert e:
  *   g = x_p w_gate[e]^T, u = x_p w_up[e]^T, h_p = bf16_rne( act(g) * u ), y_p = bf16_rne( h_p w_down[e]^T ),
  * act(g) = g / (1 + exp(-g)), or g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2; products of bf16 values summed in
- * fp32, act in fp32. With save, g and u are kept as it says (from their fp32 values).
+ * fp32 by the tensor cores, which drop what falls below a sum's last place (a relative 4e-6 with 4096 inputs); act and
+ * its derivative in fp32, to 2^-20 (1 + |g|). With save, g and u are kept as it says (from their fp32 values).
  *   region_offsets [E*R + 1] int32, or NULL with E = 1: all rows; x [rows][H], w_gate and w_up [E][I][H], w_down
  *   [E][H][I] bf16 (read); h [rows][I] bf16 (written: scratch), y [rows][H] bf16 (written); gate, up [rows][I] bf16
  *   or e4m3, gate_scales, up_scales [rows][I/128] float (written with save; NULL where not used). Rows at or above
